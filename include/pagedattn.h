@@ -346,6 +346,161 @@ int pa_copy_blocks_fp8(uint8_t *k_cache, uint8_t *v_cache, int32_t num_blocks,
                        const int32_t *src_dst_pairs, int32_t num_pairs, cudaStream_t stream);
 
 /*
+ * A step's integer inputs built on the GPU from the requests' lengths: what
+ * the pages' block manager does on the host when a step is scheduled ("blocks
+ * are allocated on demand as a block fills": "PagedAttention 显存分页与连续批处理
+ * 实战", comparison table and TypeScript Block Manager), so that a loop of
+ * steps can run without the host between them.
+ *
+ * Request s has c = context_lens[s] tokens in the cache and gets n =
+ * new_lens[s] more (0 allowed), which need ceil((c + n) / block_size) -
+ * ceil(c / block_size) blocks.  Requests are served in order while the blocks
+ * and the token rows last: the first request that does not fit in what is
+ * left of the free list or of num_tokens ends the served ones, and it and all
+ * after it get no block and no row.  Blocks are taken from the top of the free
+ * list (its entry free_count - 1 first), as the host allocator hands them out.
+ *   block_tables[s, j]    the new block's id, for j = ceil(c / block_size) ..
+ *                         ceil((c + n) / block_size) - 1 (other entries are
+ *                         left as they are)
+ *   seq_lens[s]           c + n (c when the request was not served)
+ *   query_start_loc[s]    new tokens of the served requests before s
+ *   slot_mapping[t]       slot of the token in row t; -1 past the last token
+ *   positions[a, t]       position of the token in row t, c + i for the i-th
+ *                         new one, plus position_offsets[s], alike on every
+ *                         axis; 0 past the last token.  (A caller with image
+ *                         or video tokens overwrites their columns.)
+ *   free_count_out        free_count minus the blocks handed out
+ * These are pa_rotary_reshape_and_cache's, pa_reshape_and_cache's and
+ * pa_paged_attention's inputs.  Copy-on-write stays with the caller: the block
+ * that holds position c - 1 must be the request's own when c is not a
+ * multiple of block_size (pa_copy_blocks).
+ *
+ *   context_lens, new_lens [num_seqs] int32, read
+ *   position_offsets [num_seqs] int32, read, or NULL (0)
+ *   block_tables  [num_seqs, max_blocks] int32, entries 0 .. ceil(c /
+ *                 block_size) - 1 set; read and written
+ *   free_blocks   [num_blocks] int32, read; the first free_count entries are
+ *                 distinct free block ids
+ *   free_count, free_count_out  [1] int32, read and written; may be the same
+ *   seq_lens      [num_seqs] int32, written; may be context_lens itself (a
+ *                 replayed step then goes on from the last one)
+ *   query_start_loc [num_seqs + 1], slot_mapping [num_tokens] int32, written
+ *   positions     [num_axes, num_tokens] int32, written (num_axes 0 .. 4; 0:
+ *                 not written, may be NULL)
+ * No two of the other arrays may overlap.  All 4-byte aligned.  num_seqs is at
+ * most 16384.  Flags PA_ERR_DEVICE_BOUNDS: a request that was not served; a
+ * negative length or c + n > max_blocks * block_size (that request gets no
+ * block and no row, later ones are served); a free_count outside [0,
+ * num_blocks] (taken as 0); a block id outside [0, num_blocks) (-1 goes into
+ * the table and the slot).
+ */
+int pa_build_step(const int32_t *context_lens, const int32_t *new_lens,
+                  const int32_t *position_offsets, int32_t num_seqs, int32_t num_tokens,
+                  int32_t num_axes, int32_t *block_tables, int32_t max_blocks,
+                  int32_t block_size, const int32_t *free_blocks, const int32_t *free_count,
+                  int32_t *free_count_out, int32_t num_blocks, int32_t *seq_lens,
+                  int32_t *query_start_loc, int32_t *slot_mapping, int32_t *positions,
+                  cudaStream_t stream);
+
+/*
+ * Rotary positions with one or several axes on a step's queries and keys, and
+ * the slot scatter of its keys and values (pa_reshape_and_cache) in the same
+ * pass.  The pages have no counterpart: they take q, k and v as given.
+ *
+ * Pair i (i < rotary_dim / 2) of every q and k head of token t is turned by
+ *   theta = positions[axes[i], t] * inv_freq[i]   (radians),
+ *   (x1, x2) -> (x1 cos theta - x2 sin theta, x2 cos theta + x1 sin theta),
+ * with (x1, x2) the elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when
+ * interleaved is not 0.  Elements from rotary_dim on are passed through.  With
+ * one axis these are ordinary rotary positions; with several (time, height,
+ * width of image and video tokens) each frequency belongs to the axis axes[i]
+ * names.  theta is taken modulo a turn in 64-bit integer arithmetic, so far
+ * positions lose nothing; the rotation is fp32 and each result is rounded
+ * once, to bf16 (nearest even) or, for keys in the 8-bit cache, to its code.
+ *
+ *   q             [num_tokens, num_q_heads, head_dim] bf16, read; token t at
+ *                 q + t * q_stride elements, its heads contiguous (so q, k and
+ *                 v may be slices of one projection's output)
+ *   k, v          [num_tokens, num_kv_heads, head_dim] bf16, read, alike
+ *   positions     num_axes rows of num_tokens int32 (any sign), row a at
+ *                 positions + a * positions_stride
+ *   inv_freq      [rotary_dim / 2] double, finite, |inv_freq| < 2^31
+ *   axes          [rotary_dim / 2] int32 in [0, num_axes), or NULL (axis 0)
+ *   q_out         [num_tokens, num_q_heads, head_dim] bf16, written, every
+ *                 row; may be q itself when q_stride is the row's length
+ *   k_cache, v_cache  as pa_reshape_and_cache (as pa_reshape_and_cache_fp8
+ *                 for the _fp8 form), written at the tokens' slots
+ *   slot_mapping  [num_tokens] int32, read; distinct; negative: the token's
+ *                 key and value are not written (its q_out row is)
+ * head_dim 64 or 128; rotary_dim a multiple of 16 up to head_dim (0: none);
+ * num_axes 1 .. 4; strides multiples of 8 elements; q, k, v, q_out and the
+ * caches 16-byte aligned.  A slot past the pool is skipped, an axis or a
+ * frequency out of range is taken as 0; each flags PA_ERR_DEVICE_BOUNDS.
+ */
+int pa_rotary_reshape_and_cache(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k,
+                                int64_t k_stride, const pa_bf16 *v, int64_t v_stride,
+                                int32_t num_tokens, const int32_t *positions,
+                                int64_t positions_stride, int32_t num_axes,
+                                const double *inv_freq, const int32_t *axes, int32_t rotary_dim,
+                                int32_t interleaved, pa_bf16 *q_out, pa_bf16 *k_cache,
+                                pa_bf16 *v_cache, int32_t num_blocks, int32_t block_size,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                const int32_t *slot_mapping, cudaStream_t stream);
+int pa_rotary_reshape_and_cache_fp8(const pa_bf16 *q, int64_t q_stride, const pa_bf16 *k,
+                                    int64_t k_stride, const pa_bf16 *v, int64_t v_stride,
+                                    int32_t num_tokens, const int32_t *positions,
+                                    int64_t positions_stride, int32_t num_axes,
+                                    const double *inv_freq, const int32_t *axes,
+                                    int32_t rotary_dim, int32_t interleaved, pa_bf16 *q_out,
+                                    uint8_t *k_cache, uint8_t *v_cache, int32_t num_blocks,
+                                    int32_t block_size, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim,
+                                    const int32_t *slot_mapping, cudaStream_t stream);
+
+/*
+ * pa_paged_attention with a sliding window and sink tokens: the query row at
+ * position p attends to the positions j <= p with p - j < window or
+ * j < num_sinks (the row's own position always among them).  The pages have
+ * no counterpart: their attention is over the whole sequence.
+ *
+ * Only block-table entries of blocks that hold a key some row of the call
+ * sees are read: with first = seq_lens[s] - q_len - window + 1 (the first
+ * row's first position), entries whose blocks lie wholly between num_sinks
+ * and first may hold anything, and their blocks may have been freed and
+ * reused (a rolling cache).  Cached rows outside every row's view have no
+ * effect, whatever they hold; within a request's prompt chunk, a key or value
+ * that is not finite reaches the rows that see it and, for values, may reach
+ * the rows computed with them (128 / group consecutive tokens).
+ *
+ *   window        >= 1; a window of max_seq_len or more is
+ *                 pa_paged_attention_qrange
+ *   num_sinks     >= 0
+ *   min_q_len     as pa_paged_attention_qrange (0 or 1: no bound)
+ * Everything else (layouts, workspace of pa_workspace_size() bytes, errors,
+ * precision) as pa_paged_attention, and as pa_paged_attention_fp8 for the
+ * 8-bit cache's form.
+ */
+int pa_paged_attention_window(const pa_bf16 *q, const pa_bf16 *k_cache, const pa_bf16 *v_cache,
+                              int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim,
+                              const int32_t *block_tables, int32_t max_blocks,
+                              const int32_t *seq_lens, const int32_t *query_start_loc,
+                              int32_t num_seqs, int32_t num_tokens, int32_t min_q_len,
+                              int32_t max_q_len, int32_t max_seq_len, int32_t window,
+                              int32_t num_sinks, float scale, pa_bf16 *out, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+int pa_paged_attention_window_fp8(const pa_bf16 *q, const uint8_t *k_cache,
+                                  const uint8_t *v_cache, int32_t num_blocks,
+                                  int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, const int32_t *block_tables,
+                                  int32_t max_blocks, const int32_t *seq_lens,
+                                  const int32_t *query_start_loc, int32_t num_seqs,
+                                  int32_t num_tokens, int32_t min_q_len, int32_t max_q_len,
+                                  int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                                  float scale, pa_bf16 *out, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word that
  * the kernels of this library set on the current device.  Returns PA_OK,
  * PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT or PA_ERR_CUDA.

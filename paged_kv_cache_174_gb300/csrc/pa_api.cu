@@ -316,7 +316,17 @@ int paged_attention_impl(const pa_bf16* q, KvCache kv,
                          cudaStream_t stream, const pa_bf16* fuse_k_new = nullptr,
                          const pa_bf16* fuse_v_new = nullptr,
                          const int32_t* fuse_slot_mapping = nullptr,
-                         bool fuse_any_q_len = false);
+                         bool fuse_any_q_len = false, int32_t window = 0,
+                         int32_t num_sinks = 0);
+
+// The sliding window's arguments; a window that hides nothing (all of a
+// request's keys in the window, or all of them sinks) is plain attention.
+int check_window(int32_t* window, int32_t num_sinks, int32_t max_seq_len) {
+  if (*window < 1) return fail(PA_ERR_INVALID_ARG, "window %d < 1", *window);
+  if (num_sinks < 0) return fail(PA_ERR_INVALID_ARG, "num_sinks %d < 0", num_sinks);
+  if (*window >= max_seq_len || num_sinks >= max_seq_len) *window = 0;
+  return PA_OK;
+}
 
 }  // namespace
 
@@ -399,6 +409,215 @@ int pa_paged_attention_fp8(const pa_bf16* q, const uint8_t* k_cache, const uint8
                               ~size_t(0), stream);
 }
 
+int pa_paged_attention_window(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                              int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim,
+                              const int32_t* block_tables, int32_t max_blocks,
+                              const int32_t* seq_lens, const int32_t* query_start_loc,
+                              int32_t num_seqs, int32_t num_tokens, int32_t min_q_len,
+                              int32_t max_q_len, int32_t max_seq_len, int32_t window,
+                              int32_t num_sinks, float scale, pa_bf16* out, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  int st = check_window(&window, num_sinks, max_seq_len);
+  if (st) return st;
+  return paged_attention_impl(q, KvCache{k_cache, v_cache, false}, num_blocks, block_size,
+                              num_q_heads, num_kv_heads, head_dim, block_tables, max_blocks,
+                              seq_lens, query_start_loc, num_seqs, num_tokens, min_q_len,
+                              max_q_len, max_seq_len, scale, out, workspace, workspace_bytes,
+                              ~size_t(0), stream, nullptr, nullptr, nullptr, false, window,
+                              num_sinks);
+}
+
+int pa_paged_attention_window_fp8(const pa_bf16* q, const uint8_t* k_cache,
+                                  const uint8_t* v_cache, int32_t num_blocks,
+                                  int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, const int32_t* block_tables,
+                                  int32_t max_blocks, const int32_t* seq_lens,
+                                  const int32_t* query_start_loc, int32_t num_seqs,
+                                  int32_t num_tokens, int32_t min_q_len, int32_t max_q_len,
+                                  int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                                  float scale, pa_bf16* out, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+  int st = check_window(&window, num_sinks, max_seq_len);
+  if (st) return st;
+  return paged_attention_impl(q, KvCache{k_cache, v_cache, true}, num_blocks, block_size,
+                              num_q_heads, num_kv_heads, head_dim, block_tables, max_blocks,
+                              seq_lens, query_start_loc, num_seqs, num_tokens, min_q_len,
+                              max_q_len, max_seq_len, scale, out, workspace, workspace_bytes,
+                              ~size_t(0), stream, nullptr, nullptr, nullptr, false, window,
+                              num_sinks);
+}
+
+int pa_build_step(const int32_t* context_lens, const int32_t* new_lens,
+                  const int32_t* position_offsets, int32_t num_seqs, int32_t num_tokens,
+                  int32_t num_axes, int32_t* block_tables, int32_t max_blocks,
+                  int32_t block_size, const int32_t* free_blocks, const int32_t* free_count,
+                  int32_t* free_count_out, int32_t num_blocks, int32_t* seq_lens,
+                  int32_t* query_start_loc, int32_t* slot_mapping, int32_t* positions,
+                  cudaStream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0 || num_axes < 0 || max_blocks < 0)
+    return fail(PA_ERR_INVALID_ARG, "negative size argument");
+  if (block_size <= 0 || num_blocks <= 0)
+    return fail(PA_ERR_INVALID_ARG, "block_size %d and num_blocks %d must be positive",
+                block_size, num_blocks);
+  if ((int64_t)num_blocks * block_size > INT32_MAX ||
+      (int64_t)max_blocks * block_size > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "more than 2^31 - 1 token slots or positions");
+  if (num_axes > pa::kMaxRotaryAxes)
+    return fail(PA_ERR_UNSUPPORTED, "num_axes %d (at most %d)", num_axes, pa::kMaxRotaryAxes);
+  if (num_seqs > pa::kMaxPlanSeqs)
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs %d (at most %d)", num_seqs, pa::kMaxPlanSeqs);
+  if (!free_blocks || !free_count || !free_count_out || !query_start_loc ||
+      (num_seqs > 0 && (!context_lens || !new_lens || !seq_lens)) ||
+      (num_seqs > 0 && max_blocks > 0 && !block_tables) ||
+      (num_tokens > 0 && (!slot_mapping || (num_axes > 0 && !positions))))
+    return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  const void* all[] = {context_lens, new_lens,   position_offsets, block_tables, free_blocks,
+                       free_count,   free_count_out, seq_lens, query_start_loc, slot_mapping,
+                       positions};
+  for (const void* x : all)
+    if (!aligned(x, 4)) return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  pa::StepPlanArgs a;
+  a.context_lens = context_lens;
+  a.new_lens = new_lens;
+  a.position_offsets = position_offsets;
+  a.block_tables = block_tables;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.free_count_out = free_count_out;
+  a.seq_lens = seq_lens;
+  a.query_start_loc = query_start_loc;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.num_axes = num_axes;
+  a.max_blocks = max_blocks;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  int st = device_state(&a.err, nullptr);
+  if (st) return st;
+  pa::NvtxRange range("pa_build_step (tables, slots, positions)");
+  cudaError_t e = pa::launch_build_step(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "build_step launch");
+  return PA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+int rotary_cache_impl(const pa_bf16* q, int64_t q_stride, const pa_bf16* k, int64_t k_stride,
+                      const pa_bf16* v, int64_t v_stride, int32_t num_tokens,
+                      const int32_t* positions, int64_t positions_stride, int32_t num_axes,
+                      const double* inv_freq, const int32_t* axes, int32_t rotary_dim,
+                      int32_t interleaved, pa_bf16* q_out, KvCache cache, int32_t num_blocks,
+                      int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                      int32_t head_dim, const int32_t* slot_mapping, cudaStream_t stream) {
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  int st = check_cache_geometry(num_blocks, block_size, num_kv_heads, head_dim);
+  if (st) return st;
+  if (num_q_heads <= 0) return fail(PA_ERR_INVALID_ARG, "num_q_heads %d", num_q_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "rotary positions with head_dim %d (64 or 128)", head_dim);
+  if (rotary_dim < 0 || rotary_dim > head_dim)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d outside [0, head_dim %d]", rotary_dim,
+                head_dim);
+  if (rotary_dim % 16)
+    return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d (a multiple of 16)", rotary_dim);
+  if (num_axes < 1) return fail(PA_ERR_INVALID_ARG, "num_axes %d < 1", num_axes);
+  if (num_axes > pa::kMaxRotaryAxes)
+    return fail(PA_ERR_UNSUPPORTED, "num_axes %d (at most %d)", num_axes, pa::kMaxRotaryAxes);
+  if (cache.fp8 && block_size % pa::kFp8PageTokens)
+    return fail(PA_ERR_UNSUPPORTED, "8-bit cache with block_size %d (a multiple of 16)",
+                block_size);
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || !q_out || !cache.k || !cache.v || !slot_mapping ||
+      (rotary_dim > 0 && (!positions || !inv_freq)))
+    return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(cache.k, 16) || !aligned(cache.v, 16))
+    return fail(PA_ERR_INVALID_ARG, "q, k, v, q_out and the caches must be 16-byte aligned");
+  if (!aligned(positions, 4) || !aligned(slot_mapping, 4) || !aligned(axes, 4) ||
+      !aligned(inv_freq, 8))
+    return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned, inv_freq 8-byte");
+  const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+  if (q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return fail(PA_ERR_INVALID_ARG, "token strides must be multiples of 8 elements");
+  if (num_tokens > 1 && (q_stride < q_row || k_stride < kv_row || v_stride < kv_row))
+    return fail(PA_ERR_INVALID_ARG, "a token stride is shorter than the token's row");
+  if (num_axes > 1 && positions_stride < num_tokens)
+    return fail(PA_ERR_INVALID_ARG, "positions_stride %lld < num_tokens %d",
+                (long long)positions_stride, num_tokens);
+  if (q == q_out && num_tokens > 1 && q_stride != q_row)
+    return fail(PA_ERR_INVALID_ARG, "q_out may only be q itself when q's rows are contiguous");
+  pa::RotaryArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.positions_stride = positions_stride;
+  a.inv_freq = inv_freq;
+  a.axes = axes;
+  a.slot_mapping = slot_mapping;
+  a.q_out = q_out;
+  a.k_cache = const_cast<void*>(cache.k);
+  a.v_cache = const_cast<void*>(cache.v);
+  a.num_slots = (int64_t)num_blocks * block_size;
+  a.num_tokens = num_tokens;
+  a.n_q = num_q_heads;
+  a.n_kv = num_kv_heads;
+  a.head_dim = head_dim;
+  a.rotary_dim = rotary_dim;
+  a.num_axes = num_axes;
+  a.interleaved = interleaved != 0;
+  a.fp8 = cache.fp8;
+  st = device_state(&a.err, nullptr);
+  if (st) return st;
+  pa::NvtxRange range("rotary positions + slot scatter");
+  cudaError_t e = pa::launch_rotary_cache(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rotary_reshape_and_cache launch");
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_rotary_reshape_and_cache(const pa_bf16* q, int64_t q_stride, const pa_bf16* k,
+                                int64_t k_stride, const pa_bf16* v, int64_t v_stride,
+                                int32_t num_tokens, const int32_t* positions,
+                                int64_t positions_stride, int32_t num_axes,
+                                const double* inv_freq, const int32_t* axes, int32_t rotary_dim,
+                                int32_t interleaved, pa_bf16* q_out, pa_bf16* k_cache,
+                                pa_bf16* v_cache, int32_t num_blocks, int32_t block_size,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                const int32_t* slot_mapping, cudaStream_t stream) {
+  return rotary_cache_impl(q, q_stride, k, k_stride, v, v_stride, num_tokens, positions,
+                           positions_stride, num_axes, inv_freq, axes, rotary_dim, interleaved,
+                           q_out, KvCache{k_cache, v_cache, false}, num_blocks, block_size,
+                           num_q_heads, num_kv_heads, head_dim, slot_mapping, stream);
+}
+
+int pa_rotary_reshape_and_cache_fp8(const pa_bf16* q, int64_t q_stride, const pa_bf16* k,
+                                    int64_t k_stride, const pa_bf16* v, int64_t v_stride,
+                                    int32_t num_tokens, const int32_t* positions,
+                                    int64_t positions_stride, int32_t num_axes,
+                                    const double* inv_freq, const int32_t* axes,
+                                    int32_t rotary_dim, int32_t interleaved, pa_bf16* q_out,
+                                    uint8_t* k_cache, uint8_t* v_cache, int32_t num_blocks,
+                                    int32_t block_size, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim,
+                                    const int32_t* slot_mapping, cudaStream_t stream) {
+  return rotary_cache_impl(q, q_stride, k, k_stride, v, v_stride, num_tokens, positions,
+                           positions_stride, num_axes, inv_freq, axes, rotary_dim, interleaved,
+                           q_out, KvCache{k_cache, v_cache, true}, num_blocks, block_size,
+                           num_q_heads, num_kv_heads, head_dim, slot_mapping, stream);
+}
+
 }  // extern "C"
 
 namespace {
@@ -412,7 +631,8 @@ int paged_attention_impl(const pa_bf16* q, KvCache kv,
                          pa_bf16* out, void* workspace, size_t workspace_bytes, size_t split_cap,
                          cudaStream_t stream, const pa_bf16* fuse_k_new,
                          const pa_bf16* fuse_v_new,
-                         const int32_t* fuse_slot_mapping, bool fuse_any_q_len) {
+                         const int32_t* fuse_slot_mapping, bool fuse_any_q_len,
+                         int32_t window, int32_t num_sinks) {
   const bool fuse = fuse_slot_mapping != nullptr;  // pa_decode_step
   int st = check_cache_geometry(num_blocks, block_size, num_kv_heads, head_dim);
   if (st) return st;
@@ -496,6 +716,14 @@ int paged_attention_impl(const pa_bf16* q, KvCache kv,
   a.err = err;
   a.after_prefill = false;
   a.no_decode = min_q_len >= 2;
+  a.window = window;
+  a.num_sinks = num_sinks;
+  if (window > 0) {
+    pa::NvtxRange range("sliding-window attention");
+    cudaError_t e = pa::launch_window(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "window attention launch");
+    return PA_OK;
+  }
 
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   if (max_q_len >= 2) {

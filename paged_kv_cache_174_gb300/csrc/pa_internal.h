@@ -71,6 +71,10 @@ struct AttnArgs {
   // (which triggers its dependents at once and writes only prefill rows):
   // the decode kernel may then start on SMs it leaves free.
   bool after_prefill;
+  // Sliding window (0: none): position p attends to positions above p - window
+  // and to the first num_sinks ones.
+  int32_t window;
+  int32_t num_sinks;
   // The caller promised that no request has exactly one query row: the
   // decode kernel is not launched, and the prefill kernel flags a request
   // with one row as a bounds error instead of leaving its row unwritten.
@@ -136,6 +140,52 @@ cudaError_t launch_swap(uint16_t* k_cache, uint16_t* v_cache, int32_t num_blocks
                         int64_t block_elems, const int32_t* ids, int32_t n, uint16_t* staging,
                         uint16_t* host_k, uint16_t* host_v, bool out, unsigned* err,
                         cudaStream_t stream);
+
+// A step's integer inputs from the requests' lengths (pa_step.cu).
+struct StepPlanArgs {
+  const int32_t* context_lens;      // [num_seqs]
+  const int32_t* new_lens;          // [num_seqs]
+  const int32_t* position_offsets;  // [num_seqs] or null
+  int32_t* block_tables;            // [num_seqs, max_blocks]
+  const int32_t* free_blocks;       // [num_blocks], the last free_count on top
+  const int32_t* free_count;        // [1]
+  int32_t* free_count_out;          // [1]
+  int32_t* seq_lens;                // [num_seqs]
+  int32_t* query_start_loc;         // [num_seqs + 1]
+  int32_t* slot_mapping;            // [num_tokens]
+  int32_t* positions;               // [num_axes, num_tokens]
+  unsigned* err;
+  int32_t num_seqs, num_tokens, num_axes, max_blocks, block_size, num_blocks;
+};
+constexpr int kMaxPlanSeqs = 16384;  // three words of shared memory each
+cudaError_t launch_build_step(const StepPlanArgs& p, cudaStream_t stream);
+
+constexpr int kMaxRotaryAxes = 4;
+
+// Rotary positions on q and k with the slot scatter of k and v (pa_rotary.cu).
+struct RotaryArgs {
+  const uint16_t* q;  // token rows at these strides (elements), heads contiguous
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* positions;  // [num_axes] rows at positions_stride
+  int64_t positions_stride;
+  const double* inv_freq;  // [rotary_dim / 2]
+  const int32_t* axes;     // [rotary_dim / 2] or null (axis 0)
+  const int32_t* slot_mapping;
+  uint16_t* q_out;  // [num_tokens, n_q, head_dim]
+  void* k_cache;    // bf16 values, or (fp8) pages of E4M3 codes and row scales
+  void* v_cache;
+  unsigned* err;
+  int64_t num_slots;
+  int32_t num_tokens, n_q, n_kv, head_dim, rotary_dim, num_axes;
+  bool interleaved;
+  bool fp8;
+};
+cudaError_t launch_rotary_cache(const RotaryArgs& p, cudaStream_t stream);
+
+// Attention with a sliding window (AttnArgs.window > 0; pa_window.cu).
+cudaError_t launch_window(const AttnArgs& a, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, unsigned* err,
                                          cudaStream_t stream);

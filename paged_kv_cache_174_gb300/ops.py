@@ -10,6 +10,7 @@ raises :class:`PagedAttnError`.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -103,6 +104,18 @@ def _load() -> ctypes.CDLL:
     L.pa_paged_attention_fp8.restype = ctypes.c_int
     L.pa_copy_blocks_fp8.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp]
     L.pa_copy_blocks_fp8.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    L.pa_build_step.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp,
+                                vp, vp, vp]
+    L.pa_build_step.restype = ctypes.c_int
+    for name in ("pa_rotary_reshape_and_cache", "pa_rotary_reshape_and_cache_fp8"):
+        getattr(L, name).argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, vp, i32,
+                                     i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+        getattr(L, name).restype = ctypes.c_int
+    for name in ("pa_paged_attention_window", "pa_paged_attention_window_fp8"):
+        getattr(L, name).argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32,
+                                     i32, i32, i32, i32, i32, i32, f32, vp, vp, sz, vp]
+        getattr(L, name).restype = ctypes.c_int
     L.pa_step_graph_create.argtypes = [ctypes.POINTER(StepBuffers), ctypes.POINTER(vp)]
     L.pa_step_graph_create.restype = ctypes.c_int
     L.pa_step_graph_launch.argtypes = [vp, vp]
@@ -529,6 +542,312 @@ def copy_blocks_fp8(k_cache, v_cache, src_dst_pairs: torch.Tensor, *, num_kv_hea
     _check(L.pa_copy_blocks_fp8(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, num_kv_heads,
                                 head_dim, src_dst_pairs.data_ptr(), src_dst_pairs.shape[0],
                                 _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Operators around a step: its integer inputs from the requests' lengths,
+# rotary positions with the slot scatter, attention with a sliding window.
+# These run on the device of their tensors (all on one), whichever device is
+# current, and allocate what the caller does not pass on the stream they use.
+# ---------------------------------------------------------------------------
+
+def _one_device(named) -> torch.device:
+    """The one CUDA device of the (name, tensor) pairs whose tensor is not None."""
+    device = None
+    for name, t in named:
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
+    return device
+
+
+@contextlib.contextmanager
+def _other_device_or_stream(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(int(stream), device)
+            with torch.cuda.stream(s):
+                yield s.cuda_stream
+
+
+class _Here:
+    """The plain case of _launching: current device, current stream."""
+
+    def __enter__(self):
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_AND_NOW = _Here()
+
+
+def _launching(device, stream):
+    """Context with the tensors' device current and the stream's allocator in
+    use; its value is the stream's handle."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE_AND_NOW
+    return _other_device_or_stream(device, stream)
+
+
+def _int32_out(t, name, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _need(t, name, torch.int32)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
+               free_blocks: torch.Tensor, free_count: torch.Tensor, *, block_size: int,
+               num_tokens: int, num_axes: int = 1,
+               position_offsets: Optional[torch.Tensor] = None,
+               seq_lens: Optional[torch.Tensor] = None,
+               query_start_loc: Optional[torch.Tensor] = None,
+               slot_mapping: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None,
+               free_count_out: Optional[torch.Tensor] = None, stream=None):
+    """A step's block tables, slots, start locations and positions on the GPU
+    from the requests' lengths (see pa_build_step).
+
+    ``block_tables`` [S, max_blocks] is updated in place with blocks from the
+    top of ``free_blocks`` (its first ``free_count`` entries; one entry per
+    block of the pool), ``free_count`` [1] is updated in place unless
+    ``free_count_out`` is given.  Returns (seq_lens [S], query_start_loc
+    [S + 1], slot_mapping [num_tokens], positions [num_axes, num_tokens]); each
+    may be passed in to be written (seq_lens may be context_lens itself).
+    """
+    L = _load()
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(free_blocks, "free_blocks", torch.int32, 1)
+    _need(free_count, "free_count", torch.int32)
+    S, T, A = context_lens.shape[0], int(num_tokens), int(num_axes)
+    if new_lens.shape[0] != S or block_tables.shape[0] != S:
+        raise ValueError("context_lens [S], new_lens [S], block_tables [S, max_blocks] disagree")
+    if T < 0 or A < 0:
+        raise ValueError(f"num_tokens {T} and num_axes {A} must not be negative")
+    if free_count.numel() != 1:
+        raise ValueError("free_count must hold one value")
+    if free_count_out is None:
+        free_count_out = free_count
+    else:
+        _need(free_count_out, "free_count_out", torch.int32)
+        if free_count_out.numel() != 1:
+            raise ValueError("free_count_out must hold one value")
+    if position_offsets is not None:
+        _need(position_offsets, "position_offsets", torch.int32, 1)
+        if position_offsets.shape[0] != S:
+            raise ValueError("position_offsets must be [S]")
+    device = _one_device((("context_lens", context_lens), ("new_lens", new_lens),
+                          ("block_tables", block_tables), ("free_blocks", free_blocks),
+                          ("free_count", free_count), ("free_count_out", free_count_out),
+                          ("position_offsets", position_offsets), ("seq_lens", seq_lens),
+                          ("query_start_loc", query_start_loc), ("slot_mapping", slot_mapping),
+                          ("positions", positions)))
+    with _launching(device, stream) as handle:
+        seq_lens = _int32_out(seq_lens, "seq_lens", (S,), device)
+        query_start_loc = _int32_out(query_start_loc, "query_start_loc", (S + 1,), device)
+        slot_mapping = _int32_out(slot_mapping, "slot_mapping", (T,), device)
+        positions = _int32_out(positions, "positions", (A, T), device)
+        _check(L.pa_build_step(
+            context_lens.data_ptr(), new_lens.data_ptr(),
+            None if position_offsets is None else position_offsets.data_ptr(), S, T, A,
+            block_tables.data_ptr(), block_tables.shape[1], int(block_size),
+            free_blocks.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
+            free_blocks.shape[0], seq_lens.data_ptr(), query_start_loc.data_ptr(),
+            slot_mapping.data_ptr(), positions.data_ptr(), handle))
+    return seq_lens, query_start_loc, slot_mapping, positions
+
+
+def _token_rows(t, name):
+    """A bf16 CUDA tensor [T, heads, d] whose tokens may be strided: (T, heads,
+    d, token stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
+    T, heads, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+    if T > 1 and (st < heads * d or st % 8):
+        raise ValueError(f"{name}'s tokens must not overlap, at a stride of a multiple of 8")
+    return T, heads, d, st if T > 1 else heads * d
+
+
+def _rotary(fp8, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, axes, interleaved,
+            q_out, stream):
+    L = _load()
+    T, nq, d, q_stride = _token_rows(q, "q")
+    Tk, nkv, dk, k_stride = _token_rows(k, "k")
+    Tv, nv, dv, v_stride = _token_rows(v, "v")
+    if (Tk, Tv) != (T, T) or nv != nkv or (dk, dv) != (d, d):
+        raise ValueError("q [T, n_q, d], k and v [T, n_kv, d] disagree")
+    if fp8:
+        nb, bs = _fp8_geometry(k_cache, v_cache, nkv, d)
+    else:
+        _need(k_cache, "k_cache", torch.bfloat16, 4)
+        _need(v_cache, "v_cache", torch.bfloat16, 4)
+        nb, bs, n, dc = k_cache.shape
+        if v_cache.shape != k_cache.shape or (n, dc) != (nkv, d):
+            raise ValueError("caches must be alike, [num_blocks, block_size, n_kv, d]")
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    half = inv_freq.shape[0]
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must be [T]")
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+        raise TypeError("positions must be a torch.int32 tensor")
+    if not positions.is_cuda:
+        raise ValueError("positions must be a CUDA tensor")
+    if positions.dim() not in (1, 2) or positions.shape[-1] != T or \
+            (T > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be [T] or [num_axes, T] with contiguous rows")
+    A = 1 if positions.dim() == 1 else positions.shape[0]
+    p_stride = T if positions.dim() == 1 else max(positions.stride(0), T)
+    if A > 1 and positions.stride(0) < T:
+        raise ValueError("the rows of positions overlap")
+    if axes is not None:
+        _need(axes, "axes", torch.int32, 1)
+        if axes.shape[0] != half:
+            raise ValueError("axes must name an axis for each entry of inv_freq")
+    device = _one_device((("q", q), ("k", k), ("v", v), ("positions", positions),
+                          ("inv_freq", inv_freq), ("k_cache", k_cache), ("v_cache", v_cache),
+                          ("slot_mapping", slot_mapping), ("axes", axes), ("q_out", q_out)))
+    with _launching(device, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty(T, nq, d, dtype=torch.bfloat16, device=device)
+        _need(q_out, "q_out", torch.bfloat16, 3)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        fn = L.pa_rotary_reshape_and_cache_fp8 if fp8 else L.pa_rotary_reshape_and_cache
+        _check(fn(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, T,
+                  positions.data_ptr(), p_stride, A, inv_freq.data_ptr(),
+                  None if axes is None else axes.data_ptr(), 2 * half, int(bool(interleaved)),
+                  q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
+                  slot_mapping.data_ptr(), handle))
+    return q_out
+
+
+def rotary_reshape_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             positions: torch.Tensor, inv_freq: torch.Tensor,
+                             k_cache: torch.Tensor, v_cache: torch.Tensor,
+                             slot_mapping: torch.Tensor, *, axes: Optional[torch.Tensor] = None,
+                             interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """Rotary positions on q [T, n_q, d] and k [T, n_kv, d], and the slot
+    scatter of k and v, in one pass (see pa_rotary_reshape_and_cache).
+
+    ``positions`` int32 [T] or [num_axes, T]; ``inv_freq`` float64 [rotary_dim /
+    2] and ``axes`` int32 of the same length (each frequency's axis; None: axis
+    0) on the device.  q, k and v may be slices of one projection's output
+    (heads contiguous, tokens strided).  Returns the rotated queries, ``q_out``
+    (q itself to rotate in place).
+    """
+    return _rotary(False, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, axes,
+                   interleaved, q_out, stream)
+
+
+def rotary_reshape_and_cache_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 positions: torch.Tensor, inv_freq: torch.Tensor,
+                                 k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 slot_mapping: torch.Tensor, *,
+                                 axes: Optional[torch.Tensor] = None, interleaved: bool = False,
+                                 q_out: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """rotary_reshape_and_cache into the 8-bit cache: the rotated keys and the
+    values are quantised per (token, kv head) row as reshape_and_cache_fp8 does."""
+    return _rotary(True, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, axes,
+                   interleaved, q_out, stream)
+
+
+def _window_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+                      window, num_sinks, min_q_len, max_q_len, max_seq_len, out, workspace,
+                      stream):
+    L = _load()
+    _need(q, "q", torch.bfloat16, 3)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(query_start_loc, "query_start_loc", torch.int32, 1)
+    T, nq, d = q.shape
+    if fp8:
+        _need(k_cache, "k_cache", torch.uint8, 3)
+        nkv = k_cache.shape[2] // fp8_page_bytes(1, d)
+        nb, bs = _fp8_geometry(k_cache, v_cache, nkv, d)
+        if nkv <= 0 or nq % nkv != 0:
+            raise ValueError(f"num_q_heads {nq} must be a multiple of num_kv_heads {nkv}")
+        S = seq_lens.shape[0]
+        if block_tables.shape[0] != S or query_start_loc.shape[0] != S + 1:
+            raise ValueError("block_tables [S, max_blocks], seq_lens [S], "
+                             "query_start_loc [S + 1] disagree")
+        if out is not None and out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    else:
+        _need(k_cache, "k_cache", torch.bfloat16, 4)
+        _need(v_cache, "v_cache", torch.bfloat16, 4)
+        T, nq, d, nb, bs, nkv, S = _attention_shapes(q, k_cache, v_cache, block_tables, seq_lens,
+                                                     query_start_loc, out)
+    device = _one_device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                          ("block_tables", block_tables), ("seq_lens", seq_lens),
+                          ("query_start_loc", query_start_loc), ("out", out),
+                          ("workspace", workspace)))
+    with _launching(device, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, "out", torch.bfloat16, 3)
+        if workspace is None:
+            workspace = alloc_workspace(S, T, nq, nkv, d, max_q_len, max_seq_len, device)
+        _need_workspace(workspace)
+        fn = L.pa_paged_attention_window_fp8 if fp8 else L.pa_paged_attention_window
+        _check(fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
+                  block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+                  query_start_loc.data_ptr(), S, T, int(min_q_len), int(max_q_len),
+                  int(max_seq_len), int(window), int(num_sinks), float(scale), out.data_ptr(),
+                  workspace.data_ptr(), workspace.numel(), handle))
+    return out
+
+
+def paged_attention_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           query_start_loc: torch.Tensor, scale: float, *, window: int,
+                           num_sinks: int = 0, max_q_len: int, max_seq_len: int,
+                           out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None,
+                           min_q_len: int = 0) -> torch.Tensor:
+    """paged_attention with a sliding window and sink tokens: position p attends
+    to j <= p with p - j < window or j < num_sinks (see
+    pa_paged_attention_window).  Table entries of blocks that no row sees may
+    hold anything.  Returns ``out``."""
+    return _window_attention(False, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                             scale, window, num_sinks, min_q_len, max_q_len, max_seq_len, out,
+                             workspace, stream)
+
+
+def paged_attention_window_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                               query_start_loc: torch.Tensor, scale: float, *, window: int,
+                               num_sinks: int = 0, max_q_len: int, max_seq_len: int,
+                               out: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None, stream=None,
+                               min_q_len: int = 0) -> torch.Tensor:
+    """paged_attention_window over the 8-bit cache."""
+    return _window_attention(True, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                             scale, window, num_sinks, min_q_len, max_q_len, max_seq_len, out,
+                             workspace, stream)
 
 
 def selftest_wait_timeout(limit_ns: int = 5_000_000, stream=None) -> None:

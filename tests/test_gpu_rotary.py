@@ -1,0 +1,216 @@
+"""Rotary positions with the slot scatter on the GPU against 64-bit rotation:
+both caches, several axes, pairings, partial rotation, far and negative
+positions, strided inputs, skipped slots, in-place use."""
+import numpy as np
+import pytest
+import torch
+
+import step_reference as R
+from paged_kv_cache_174_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(seed, T, nq, nkv, d, rot, axes, far, packed=False, bs=16, skip=0.2, scale=1.0):
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    widths = [nq * d, nkv * d, nkv * d]
+    if packed:
+        qkv = (torch.randn(T, sum(widths) + 8, generator=g) * scale).bfloat16().cuda()
+        parts = qkv[:, 8:].split(widths, 1)
+    else:
+        parts = [(torch.randn(T, w, generator=g) * scale).bfloat16().cuda() for w in widths]
+    q, k, v = (p.unflatten(1, (-1, d)) for p in parts)
+    pos = torch.from_numpy(rng.integers(-far // 4, far, (axes, T)).astype(np.int32)).cuda()
+    freq = 10000.0 ** (-np.arange(rot // 2) * 2.0 / max(1, rot))
+    of = rng.integers(0, axes, rot // 2).astype(np.int32)
+    nb = -(-T // bs) + 2
+    slots = rng.permutation(nb * bs)[:T].astype(np.int32)
+    slots[rng.random(T) < skip] = -rng.integers(1, 9)
+    return q, k, v, pos, freq, of, slots, nb
+
+
+def _f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _check_bf16(got, ref, size, what):
+    y, tol = ref, R.HALF_BF16 * np.abs(ref) + 2.0 ** -20 * size
+    off = np.abs(got - y)
+    # cos and sin of an angle right to 2^-24 of a turn, two fp32 products and
+    # a sum: 2^-20 of |x1| + |x2|; then one rounding to bf16
+    assert (off <= tol).all(), f"{what}: {float((off - tol).max()):.3e} past the tolerance"
+    assert np.array_equal(got[size == 0], y[size == 0]), f"{what}: passed-through elements"
+
+
+CASES = [
+    # T, n_q, n_kv, d, rot, axes, interleaved, far, packed, block size
+    (1, 4, 2, 64, 64, 1, False, 4096, False, 16),
+    (3, 8, 1, 128, 128, 3, False, 1 << 20, True, 16),
+    (65, 32, 8, 128, 128, 3, False, 32768, True, 16),
+    (130, 16, 2, 64, 32, 2, True, 1 << 20, False, 32),
+    (77, 6, 3, 128, 96, 4, True, 2 ** 31 - 1, True, 16),
+    (257, 5, 5, 64, 48, 3, False, 2 ** 31 - 1, False, 32),
+    (31, 1, 1, 128, 16, 1, False, 100, True, 48),
+    (9, 8, 8, 64, 0, 1, False, 100, False, 16),
+]
+
+
+@pytest.mark.parametrize("T,nq,nkv,d,rot,axes,inter,far,packed,bs", CASES)
+def test_bf16(T, nq, nkv, d, rot, axes, inter, far, packed, bs):
+    q, k, v, pos, freq, of, slots, nb = _inputs(T, T, nq, nkv, d, rot, axes, far, packed, bs)
+    kc = torch.full((nb, bs, nkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    vc = torch.full_like(kc, 9.0)
+    before = [x.clone() for x in (q, k, v)]
+    out = ops.rotary_reshape_and_cache(
+        q, k, v, pos, torch.from_numpy(freq).cuda(), kc, vc, torch.from_numpy(slots).cuda(),
+        axes=torch.from_numpy(of).cuda() if axes > 1 else None, interleaved=inter)
+    ops.check_device_errors()
+    for x, y in zip((q, k, v), before):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))  # inputs only read
+    P, ax = pos.cpu().numpy(), of if axes > 1 else None
+    ref, size = R.rotate(_f64(q), P, freq, ax, inter)
+    _check_bf16(_f64(out), ref, size, "q")
+    kref, ksize = R.rotate(_f64(k), P, freq, ax, inter)
+    at = np.nonzero(slots >= 0)[0]
+    rows = _f64(kc).reshape(-1, nkv, d)
+    _check_bf16(rows[slots[at]], kref[at], ksize[at], "k")
+    vrows = _f64(vc).reshape(-1, nkv, d)
+    assert np.array_equal(vrows[slots[at]], _f64(v)[at])
+    rest = np.setdiff1d(np.arange(nb * bs), slots[at])
+    assert (rows[rest] == 7.0).all() and (vrows[rest] == 9.0).all()
+
+
+@pytest.mark.parametrize("T,nq,nkv,d,rot,axes,inter,far,packed,bs", CASES)
+def test_fp8(T, nq, nkv, d, rot, axes, inter, far, packed, bs):
+    q, k, v, pos, freq, of, slots, nb = _inputs(T, T, nq, nkv, d, rot, axes, far, packed, bs,
+                                                scale=3.0)
+    k[0].zero_()  # an all-zero row
+    kc, vc = ops.empty_fp8_cache(nb, bs, nkv, d)
+    kw, vw = ops.empty_fp8_cache(nb, bs, nkv, d)
+    dslots = torch.from_numpy(slots).cuda()
+    out = ops.rotary_reshape_and_cache_fp8(
+        q, k, v, pos, torch.from_numpy(freq).cuda(), kc, vc, dslots,
+        axes=torch.from_numpy(of).cuda() if axes > 1 else None, interleaved=inter)
+    # values are stored as the plain scatter stores them
+    ops.reshape_and_cache_fp8(k.contiguous(), v.contiguous(), kw, vw, dslots)
+    ops.check_device_errors()
+    assert torch.equal(vc, vw)
+    P, ax = pos.cpu().numpy(), of if axes > 1 else None
+    ref, size = R.rotate(_f64(q), P, freq, ax, inter)
+    _check_bf16(_f64(out), ref, size, "q")
+    codes, scales = ops.fp8_cache_views(kc, nkv, d)
+    value = _f64(codes.view(torch.float8_e4m3fn)).reshape(-1, nkv, d)
+    scale = _f64(scales).reshape(-1, nkv)
+    at = np.nonzero(slots >= 0)[0]
+    kref, ksize = R.rotate(_f64(k), P, freq, ax, inter)
+    kref, ksize = kref[at], ksize[at]
+    top = np.abs(kref).max(-1)
+    want = np.where(top > 0, top / 448.0, 1.0)
+    got = scale[slots[at]]
+    # the row's maximum is off by 2^-20 of a pair's |x1| + |x2| at most, which
+    # is at most sqrt(2) times a rotated pair's length, itself at most sqrt(2)
+    # times the maximum when the pair is the largest: 2^-18 covers it
+    assert (np.abs(got - want) <= 2.0 ** -18 * want).all()
+    mid = value[slots[at]] * got[..., None]
+    # half a step of a code: 2^-4 of the value, or 2^-10 in units of the scale
+    # among the subnormals
+    tol = np.maximum(2.0 ** -4 * np.abs(kref), 2.0 ** -10 * want[..., None]) * (1 + 2.0 ** -10) \
+        + 2.0 ** -17 * top[..., None] + 1e-30
+    assert (np.abs(mid - kref) <= tol).all()
+    rest = np.setdiff1d(np.arange(nb * bs), slots[at])
+    assert (value[rest] == 0).all() and (scale[rest] == 0).all()
+
+
+def test_in_place_queries_and_given_stream():
+    q, k, v, pos, freq, of, slots, nb = _inputs(5, 40, 8, 2, 128, 128, 3, 9999)
+    f, a, s = torch.from_numpy(freq).cuda(), torch.from_numpy(of).cuda(), \
+        torch.from_numpy(slots).cuda()
+    kc = torch.zeros(nb, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    want = ops.rotary_reshape_and_cache(q, k, v, pos, f, kc, vc, s, axes=a)
+    kc2, vc2, q2 = torch.zeros_like(kc), torch.zeros_like(kc), q.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ops.rotary_reshape_and_cache(q2, k, v, pos, f, kc2, vc2, s, axes=a, q_out=q2,
+                                       stream=side)
+    side.synchronize()
+    ops.check_device_errors()
+    assert got is q2
+    for x, y in ((want, q2), (kc, kc2), (vc, vc2)):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    # one axis of positions as [T], and as rows of a wider (padded) array
+    one = ops.rotary_reshape_and_cache(q, k, v, pos[1].contiguous(), f, kc, vc, s)
+    wide = torch.zeros(3, 64, dtype=torch.int32, device="cuda")
+    wide[0, :40] = pos[1]
+    two = ops.rotary_reshape_and_cache(q, k, v, wide[:, :40], f, kc, vc, s)
+    assert torch.equal(one.view(torch.int16), two.view(torch.int16))
+
+
+def test_values_out_of_range_are_flagged():
+    q, k, v, pos, freq, of, slots, nb = _inputs(6, 8, 4, 2, 64, 64, 2, 999, skip=0.0)
+    kc = torch.zeros(nb, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    f, a, s = torch.from_numpy(freq).cuda(), torch.from_numpy(of).cuda(), \
+        torch.from_numpy(slots).cuda()
+
+    def flagged(f=f, a=a, s=s):
+        out = ops.rotary_reshape_and_cache(q, k, v, pos, f, kc, vc, s, axes=a)
+        with pytest.raises(ops.PagedAttnError) as e:
+            ops.check_device_errors()
+        assert e.value.code == 4
+        return out
+    bad = s.clone()
+    bad[3] = nb * 16
+    flagged(s=bad)
+    assert (kc.view(-1, 2, 64)[s[3].item()] == 0).all()  # the token was skipped
+    for value in (float("inf"), float("nan"), 2.0 ** 31):
+        g = f.clone()
+        g[1] = value
+        out = flagged(f=g)  # the frequency counts as 0: its pair is unturned
+        assert torch.equal(out[:, :, 1].view(torch.int16), q[:, :, 1].view(torch.int16))
+    for value in (-1, 2):
+        b = a.clone()
+        b[0] = value
+        flagged(a=b)
+    ops.rotary_reshape_and_cache(q, k, v, pos, f, kc, vc, s, axes=a)
+    ops.check_device_errors()
+
+
+def test_not_a_number_stays_in_its_pair():
+    q, k, v, pos, freq, of, slots, nb = _inputs(7, 5, 4, 2, 64, 64, 1, 999, skip=0.0)
+    q[2, 1, 3] = float("nan")
+    k[1, 0, 5] = float("inf")
+    kc = torch.zeros(nb, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out = ops.rotary_reshape_and_cache(q, k, v, pos, torch.from_numpy(freq).cuda(), kc,
+                                       torch.zeros_like(kc), torch.from_numpy(slots).cuda())
+    bad = torch.zeros(5, 4, 64, dtype=torch.bool, device="cuda")
+    bad[2, 1, 3] = bad[2, 1, 35] = True
+    assert torch.equal(~torch.isfinite(out), bad)
+    rows = torch.isfinite(kc.view(-1, 2, 64)[torch.from_numpy(slots).long().cuda()])
+    bad = torch.zeros(5, 2, 64, dtype=torch.bool, device="cuda")
+    bad[1, 0, 5] = bad[1, 0, 37] = True
+    assert torch.equal(~rows, bad)
+
+
+def test_refusals():
+    q, k, v, pos, freq, of, slots, nb = _inputs(8, 6, 4, 2, 64, 64, 2, 999)
+    kc = torch.zeros(nb, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    f, a, s = torch.from_numpy(freq).cuda(), torch.from_numpy(of).cuda(), \
+        torch.from_numpy(slots).cuda()
+    good = dict(q=q, k=k, v=v, positions=pos, inv_freq=f, k_cache=kc, v_cache=kc.clone(),
+                slot_mapping=s, axes=a)
+    for bad in (dict(k=k[:5]), dict(v=v[:, :1]), dict(q=q.transpose(0, 1)),
+                dict(slot_mapping=s[:5]), dict(positions=pos[:, :5]), dict(axes=a[:3]),
+                dict(v_cache=kc[:1]), dict(q_out=q[:5].contiguous()),
+                dict(k=k.repeat(1, 1, 2)[..., :64]), dict(positions=pos.t()),
+                dict(positions=pos[0].expand(2, 6)), dict(q=q.cpu())):
+        with pytest.raises(ValueError):
+            ops.rotary_reshape_and_cache(**{**good, **bad})
+    for bad in (dict(inv_freq=f.float()), dict(positions=pos.long()), dict(q=q.float()),
+                dict(axes=a.long())):
+        with pytest.raises(TypeError):
+            ops.rotary_reshape_and_cache(**{**good, **bad})
+    with pytest.raises(ops.PagedAttnError):  # 24 rotated elements
+        ops.rotary_reshape_and_cache(**{**good, "inv_freq": f[:12].contiguous(),
+                                        "axes": a[:12].contiguous()})
