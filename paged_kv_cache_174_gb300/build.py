@@ -24,7 +24,8 @@ LIB = os.path.join(OUT_DIR, LIB_NAME)
 
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_decode_fp8.cu", "pa_decode_fused.cu",
            "pa_prefill.cu", "pa_prefill_fp8.cu", "pa_graph.cu", "pa_step.cu", "pa_rotary.cu",
-           "pa_window.cu"]
+           "pa_decode_window.cu", "pa_decode_window_fp8.cu", "pa_prefill_window.cu",
+           "pa_prefill_window_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

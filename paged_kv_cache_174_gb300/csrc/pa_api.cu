@@ -686,8 +686,12 @@ int paged_attention_impl(const pa_bf16* q, KvCache kv,
                 need_decode);
   // the prefill key split takes only what the workspace has left
   const size_t left = workspace_bytes - need_decode;
+  // with a window, a query tile's keys are at most the window's and the sinks'
+  // (128 rows of a tile and the edges' pages besides)
+  const int64_t keys = (int64_t)window + num_sinks + 128 + 32;
+  const int32_t plan_len = window > 0 && keys < max_seq_len ? (int32_t)keys : max_seq_len;
   const pa::PrefillPlan plan =
-      pa::prefill_plan(num_tokens, num_q_heads, num_kv_heads, head_dim, max_q_len, max_seq_len,
+      pa::prefill_plan(num_tokens, num_q_heads, num_kv_heads, head_dim, max_q_len, plan_len,
                        sms, left < split_cap ? left : split_cap);
 
   pa::AttnArgs a;
@@ -718,12 +722,6 @@ int paged_attention_impl(const pa_bf16* q, KvCache kv,
   a.no_decode = min_q_len >= 2;
   a.window = window;
   a.num_sinks = num_sinks;
-  if (window > 0) {
-    pa::NvtxRange range("sliding-window attention");
-    cudaError_t e = pa::launch_window(a, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "window attention launch");
-    return PA_OK;
-  }
 
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   if (max_q_len >= 2) {

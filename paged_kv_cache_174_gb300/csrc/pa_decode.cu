@@ -35,9 +35,12 @@ bool decode_supported(int head_dim, int group, int num_kv_heads) {
 
 cudaError_t launch_decode(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
                           cudaStream_t stream) {
+  if (a.window > 0)
+    return a.fp8 ? launch_decode_window_fp8(a, ws, ctas, stream)
+                 : launch_decode_window(a, ws, ctas, stream);
   if (a.fp8) return launch_decode_fp8(a, ws, ctas, stream);
   if (a.fuse_slot_mapping) return launch_decode_fused(a, ws, ctas, stream);
-  return launch_decode_any<false, false>(a, ws, ctas, stream);
+  return launch_decode_any<false, false, false>(a, ws, ctas, stream);
 }
 
 }  // namespace pa

@@ -9,7 +9,7 @@ namespace pa {
 
 cudaError_t launch_decode_fused(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
                                 cudaStream_t stream) {
-  return launch_decode_any<false, true>(a, ws, ctas, stream);
+  return launch_decode_any<false, true, false>(a, ws, ctas, stream);
 }
 
 }  // namespace pa

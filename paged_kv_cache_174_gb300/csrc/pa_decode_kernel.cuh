@@ -75,10 +75,62 @@ struct DecodeParams {
   uint32_t page_bytes;   // one K (or V) page of 16 tokens: 16 * n_kv * head_dim * elem,
                          // F8: the codes, then their 16 * n_kv fp32 scales
   uint32_t row_bytes;    // one token row of one cache: n_kv * head_dim * elem
+  // Sliding window (the WIN instances): a request's pages are those with a
+  // key its row sees, the sinks' pages first, then the window's
+  int32_t window, num_sinks;
 };
+
+// Which pages of a request of length L a windowed decode row reads.
+struct WindowPages {
+  int w0;     // first position in the window
+  int sinks;  // pages before the window's first that hold sinks
+  int skip;   // pages between those and the window's first
+  __device__ __forceinline__ WindowPages(const DecodeParams& p, int L) {
+    w0 = max(0, L - p.window);
+    const int first = w0 / kBlock;
+    sinks = p.num_sinks > first * kBlock ? first : (p.num_sinks + kBlock - 1) / kBlock;
+    skip = first - sinks;
+  }
+  // Logical page of the list's entry j.
+  __device__ __forceinline__ int page(int j) const { return j < sinks ? j : j + skip; }
+};
+
+// Logical page of entry j of the page list of a request of length L.
+template <bool WIN>
+__device__ __forceinline__ int logical_page(const DecodeParams& p, int L, int j) {
+  if constexpr (WIN) return WindowPages(p, L).page(j);
+  return j;
+}
+
+// Which tokens of a page the row sees: their number (the page's first ones), or
+// with a window one bit each.
+template <bool WIN>
+__device__ __forceinline__ int page_limit(const DecodeParams& p, int L, int j) {
+  if constexpr (!WIN) return min(kBlock, L - j * kBlock);
+  const WindowPages w(p, L);
+  const int base = w.page(j) * kBlock;
+  const int n = min(kBlock, L - base);
+  const int lo = min(max(w.w0 - base, 0), kBlock);
+  const int ns = min(max(p.num_sinks - base, 0), kBlock);
+  return ((1 << n) - 1) & (((1 << ns) - 1) | (0xffff << lo));
+}
+template <bool WIN>
+__device__ __forceinline__ bool token_seen(int limit, int tok) {
+  return WIN ? (limit >> tok) & 1 : tok < limit;
+}
+template <bool WIN>
+__device__ __forceinline__ bool all_seen(int limit) {
+  return WIN ? limit == 0xffff : limit == kBlock;
+}
+// A token that is seen.
+template <bool WIN>
+__device__ __forceinline__ int seen_token(int limit) {
+  return WIN ? __ffs(limit) - 1 : 0;
+}
 
 // Pages this kernel processes for request s (0 if it is not a decode request
 // or is invalid; invalid ones flag the error word once, from CTA 0).
+template <bool WIN>
 __device__ __forceinline__ int decode_pages(const DecodeParams& p, int s, bool report) {
   const int a = __ldg(p.qsl + s), b = __ldg(p.qsl + s + 1);
   if (b - a != 1) return 0;
@@ -88,7 +140,9 @@ __device__ __forceinline__ int decode_pages(const DecodeParams& p, int s, bool r
     if (report) flag_error(p.err, DEVERR_BOUNDS);
     return 0;
   }
-  return (L + kBlock - 1) / kBlock;
+  const int pages = (L + kBlock - 1) / kBlock;
+  if constexpr (WIN) return pages - WindowPages(p, L).skip;
+  return pages;
 }
 
 __device__ __forceinline__ int64_t slice_begin(int64_t c, int64_t F, int64_t C) {
@@ -132,6 +186,7 @@ __host__ __device__ constexpr size_t comb_offset() {
 }
 
 // Walks the flat page list of the decode requests: (request s, page j).
+template <bool WIN>
 struct PageCursor {
   int s, j, np;
   __device__ __forceinline__ void next(const DecodeParams& p) {
@@ -139,7 +194,7 @@ struct PageCursor {
       j = 0;
       do {
         ++s;
-      } while (s < p.num_seqs && (np = decode_pages(p, s, false)) == 0);
+      } while (s < p.num_seqs && (np = decode_pages<WIN>(p, s, false)) == 0);
     }
   }
 };
@@ -162,14 +217,21 @@ __device__ __forceinline__ void bulk_g2s_hint(uint32_t dst_smem, const void* src
 
 // Issue the bulk copies of page (c.s, c.j) into a stage.  *fused_slot gets the
 // slot the stage's last row must be stored to (fused scatter), or -1.
-template <bool FUSE, bool F8>
-__device__ __forceinline__ void fetch_page(const DecodeParams& p, const PageCursor& c,
+template <bool FUSE, bool F8, bool WIN>
+__device__ __forceinline__ void fetch_page(const DecodeParams& p, const PageCursor<WIN>& c,
                                            uint32_t stage_smem, uint32_t full_bar,
                                            int* fused_slot) {
   const int L = __ldg(p.seq_lens + c.s);
-  const int ntok = min(kBlock, L - c.j * kBlock);
-  const int phys =
-      __ldg(p.block_tables + (int64_t)c.s * p.max_blocks + (c.j >> p.block_shift));
+  const int lp = logical_page<WIN>(p, L, c.j);
+  // rows [row0, ntok) of the page: with a window from the first seen token to
+  // the last (the others in a page at the window's start are not read)
+  int row0 = 0, ntok = min(kBlock, L - lp * kBlock);
+  if constexpr (WIN && !F8) {
+    const int limit = page_limit<WIN>(p, L, c.j);
+    row0 = __ffs(limit) - 1;
+    ntok = 32 - __clz(limit);
+  }
+  const int phys = __ldg(p.block_tables + (int64_t)c.s * p.max_blocks + (lp >> p.block_shift));
   *fused_slot = -1;
   if (phys < 0 || phys >= p.num_blocks) {
     flag_error(p.err, DEVERR_BOUNDS);
@@ -178,11 +240,12 @@ __device__ __forceinline__ void fetch_page(const DecodeParams& p, const PageCurs
   }
   // the page's rows (F8: the whole page, whose scales follow all 16 rows;
   // rows past ntok are never used)
-  const uint32_t bytes = F8 ? p.page_bytes : (uint32_t)ntok * p.row_bytes;
+  const uint32_t bytes = F8 ? p.page_bytes : (uint32_t)(ntok - row0) * p.row_bytes;
   mbar_arrive_expect_tx(full_bar, 2 * bytes);
   // 16-token page index in the pool: a block of 32 tokens is two pages
-  const size_t page = ((size_t)phys << p.block_shift) + (c.j & ((1 << p.block_shift) - 1));
-  const size_t off = page * p.page_bytes;
+  const size_t page = ((size_t)phys << p.block_shift) + (lp & ((1 << p.block_shift) - 1));
+  const uint32_t skipped = (uint32_t)row0 * p.row_bytes;
+  const size_t off = page * p.page_bytes + skipped;
   // the pages are read once per call: evict-first keeps them from pushing
   // the call's reused data (tables, q, partial results) out of L2 (decode
   // batch on GB300: 91.3 against 93.6 us per call)
@@ -213,10 +276,10 @@ __device__ __forceinline__ void fetch_page(const DecodeParams& p, const PageCurs
     // as with a separate scatter; any other slot breaks the precondition
     if (slot >= 0) flag_error(p.err, DEVERR_BOUNDS);
   }
-  bulk_g2s_hint(stage_smem, reinterpret_cast<const unsigned char*>(p.k_cache) + off, bytes,
-                full_bar, pol);
-  bulk_g2s_hint(stage_smem + p.page_bytes, reinterpret_cast<const unsigned char*>(p.v_cache) + off,
+  bulk_g2s_hint(stage_smem + skipped, reinterpret_cast<const unsigned char*>(p.k_cache) + off,
                 bytes, full_bar, pol);
+  bulk_g2s_hint(stage_smem + p.page_bytes + skipped,
+                reinterpret_cast<const unsigned char*>(p.v_cache) + off, bytes, full_bar, pol);
 }
 
 template <int N>
@@ -267,15 +330,15 @@ __device__ __forceinline__ float reduce_scatter(float (&part)[G], int lane) {
 // predicate.  sc[it] is the base-2 score of token it * TPI + tok_lane for the
 // head this lane holds after the reduce-scatter (-inf past the page's end).
 // (bf16 cache; the 8-bit cache runs on the tensor cores, qk_scores_mma.)
-template <int D, int G, int E_QK, int LPT, uint32_t ROW, bool FULL>
-__device__ __forceinline__ void qk_scores(const unsigned char* kb, int ntok,
+template <int D, int G, int E_QK, int LPT, uint32_t ROW, bool FULL, bool WIN>
+__device__ __forceinline__ void qk_scores(const unsigned char* kb, int limit,
                                           int tok_lane, const float2 (&qf)[G][E_QK / 2],
                                           float (&sc)[kBlock / (32 / LPT)], int lane) {
   constexpr int TPI = 32 / LPT;
   constexpr int NIT = kBlock / TPI;
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
-    const bool valid = FULL || (it * TPI + tok_lane < ntok);
+    const bool valid = FULL || token_seen<WIN>(limit, it * TPI + tok_lane);
     float2 a2[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) a2[h] = make_float2(0.f, 0.f);
@@ -351,8 +414,8 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
 // Scores of one page on the tensor cores (bf16 cache), as qk_scores_mma
 // below but with the cached bf16 values as B directly (two 32-bit words per
 // k-step) and q unscaled in A; the fp32 score takes scale * log2(e).
-template <int D, uint32_t ROW>
-__device__ __forceinline__ void qk_scores_mma_bf16(const unsigned char* kb, int ntok,
+template <int D, uint32_t ROW, bool WIN>
+__device__ __forceinline__ void qk_scores_mma_bf16(const unsigned char* kb, int limit,
                                                    const uint32_t (&qa)[D / 16][2],
                                                    float scale_log2, float (&sc)[4], int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -378,7 +441,7 @@ __device__ __forceinline__ void qk_scores_mma_bf16(const unsigned char* kb, int 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int tok = 8 * T + 2 * t + j;
-      sc[2 * T + j] = tok < ntok ? c[T][j] * scale_log2 : kNegInf;
+      sc[2 * T + j] = token_seen<WIN>(limit, tok) ? c[T][j] * scale_log2 : kNegInf;
     }
 }
 
@@ -390,9 +453,9 @@ __device__ __forceinline__ void qk_scores_mma_bf16(const unsigned char* kb, int 
 // G.. zero), columns the tokens, the reduction head_dim; lane (r, t) takes
 // its k-steps from head_dim chunk [t D/4, (t + 1) D/4) so that one 32-bit
 // word of codes is one k-step.
-template <int D, int NKV, uint32_t ROW>
+template <int D, int NKV, uint32_t ROW, bool WIN>
 __device__ __forceinline__ void qk_scores_mma(const unsigned char* kb, const float* ksc,
-                                              int ntok, const uint32_t (&qa)[D / 16][2],
+                                              int limit, const uint32_t (&qa)[D / 16][2],
                                               float (&sc)[4], int lane) {
   const int g = lane >> 2, t = lane & 3;
   float c[2][4];
@@ -421,22 +484,22 @@ __device__ __forceinline__ void qk_scores_mma(const unsigned char* kb, const flo
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int tok = 8 * T + 2 * t + j;
-      sc[2 * T + j] = tok < ntok ? c[T][j] * ksc[tok * NKV] : kNegInf;
+      sc[2 * T + j] = token_seen<WIN>(limit, tok) ? c[T][j] * ksc[tok * NKV] : kNegInf;
     }
 }
 
 // p * V of one page for one PV warp: vb points at this lane's 16-byte piece of
 // its first token's value row, pp at p[tok_lane][0] of the page's hand-off
 // (bf16 cache).
-template <int D, int G, int LPT, uint32_t ROW, bool FULL>
-__device__ __forceinline__ void pv_accumulate(const unsigned char* vb, const float* pp, int ntok,
+template <int D, int G, int LPT, uint32_t ROW, bool FULL, bool WIN>
+__device__ __forceinline__ void pv_accumulate(const unsigned char* vb, const float* pp, int limit,
                                               int tok_lane,
                                               float2 (&acc)[G][4]) {
   constexpr int TPI = 32 / LPT;
   constexpr int NIT = kBlock / TPI;
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
-    if (FULL || it * TPI + tok_lane < ntok) {
+    if (FULL || token_seen<WIN>(limit, it * TPI + tok_lane)) {
       float2 v2[4];
       const uint4 vw = *reinterpret_cast<const uint4*>(vb + it * TPI * ROW);
       v2[0] = bf16x2_to_float2(vw.x), v2[1] = bf16x2_to_float2(vw.y);
@@ -480,7 +543,9 @@ __host__ __device__ constexpr int decode_threads() {
 //    warps NKV..2*NKV-1 accumulate p * V (PV warps) on the FMA pipe; warp g
 //    and warp NKV + g serve kv head g and hand over p through a
 //    double-buffered slot in shared memory.
-template <int D, int G, int NKV, bool F8, bool FUSE, bool MW>
+//  * WIN: sliding window and sinks; the page list of a request holds only the
+//    pages with a key its row sees, and tokens outside are masked.
+template <int D, int G, int NKV, bool F8, bool FUSE, bool MW, bool WIN>
 __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
     decode_kernel(const DecodeParams p) {
   constexpr bool MMA = F8 || MW;
@@ -517,7 +582,7 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
   // pass 1: total decode pages F (all threads)
   long long mine = 0;
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x)
-    mine += decode_pages(p, s, c == 0);
+    mine += decode_pages<WIN>(p, s, c == 0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) red[warp] = mine;
@@ -539,7 +604,7 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
     int found_s = -1, found_j = 0;
     for (int base = 0; base < p.num_seqs && found_s < 0; base += 32) {
       const int s = base + lane;
-      const int np = s < p.num_seqs ? decode_pages(p, s, false) : 0;
+      const int np = s < p.num_seqs ? decode_pages<WIN>(p, s, false) : 0;
       long long incl = np;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -577,9 +642,9 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
     // the slice's first NST pages, one lane each: each copy waits for two
     // dependent table loads, which then overlap instead of queueing
     if (found_s >= 0 && lane < NST && lane < n_pages) {
-      PageCursor fc{found_s, found_j, decode_pages(p, found_s, false)};
+      PageCursor<WIN> fc{found_s, found_j, decode_pages<WIN>(p, found_s, false)};
       for (int i = 0; i < lane; ++i) fc.next(p);
-      fetch_page<FUSE, F8>(p, fc, smem_addr(stages + (size_t)lane * p.stage_bytes),
+      fetch_page<FUSE, F8, WIN>(p, fc, smem_addr(stages + (size_t)lane * p.stage_bytes),
                            smem_addr(&S.full[lane]), &S.fused_slot[lane]);
       S.last_issued[lane] = lane;
     }
@@ -592,8 +657,8 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
 
   const bool is_qk = warp < NKV;
   const int g = is_qk ? warp : warp - NKV;  // kv head served by this warp
-  PageCursor cur{s_begin, j_begin, decode_pages(p, s_begin, false)};
-  PageCursor fc = cur;  // page to fetch when this warp is the last to release a stage
+  PageCursor<WIN> cur{s_begin, j_begin, decode_pages<WIN>(p, s_begin, false)};
+  PageCursor<WIN> fc = cur;  // page to fetch when this warp is the last to release a stage
   for (int i = 0; i < NST; ++i) fc.next(p);
 
   int L = __ldg(p.seq_lens + cur.s);
@@ -666,16 +731,16 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
         // i + NST is copied only after every reader, this warp among them,
         // released page i.
         mbar_wait(smem_addr(&S.full[st]), st_phase, p.err, abort_flag);
-        const int ntok = min(kBlock, L - cur.j * kBlock);
+        const int limit = page_limit<WIN>(p, L, cur.j);
         const int fslot = FUSE ? S.fused_slot[st] : -1;
         if (FUSE && fslot >= 0 && lane == 0) {
           // fused scatter: this kv head's slices of the new key and value rows
           bulk_s2g(reinterpret_cast<unsigned char*>(const_cast<void*>(p.k_cache)) +
                        (size_t)fslot * ROW + g * D * ES,
-                   smem_addr(stage + (ntok - 1) * ROW + g * D * ES), D * ES);
+                   smem_addr(stage + (limit - 1) * ROW + g * D * ES), D * ES);
           bulk_s2g(reinterpret_cast<unsigned char*>(const_cast<void*>(p.v_cache)) +
                        (size_t)fslot * ROW + g * D * ES,
-                   smem_addr(stage + p.page_bytes + (ntok - 1) * ROW + g * D * ES), D * ES);
+                   smem_addr(stage + p.page_bytes + (limit - 1) * ROW + g * D * ES), D * ES);
           bulk_commit();
           stored = true;
         }
@@ -688,11 +753,11 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
         // exposed instead of overlapping the arithmetic).
         float sc4[4];
         if constexpr (F8)
-          qk_scores_mma<D, NKV, ROW>(
+          qk_scores_mma<D, NKV, ROW, WIN>(
               stage + g * D, reinterpret_cast<const float*>(stage + kBlock * ROW + g * 4),
-              ntok, qa, sc4, lane);
+              limit, qa, sc4, lane);
         else
-          qk_scores_mma_bf16<D, ROW>(stage + g * D * ES, ntok, qa, p.scale_log2, sc4, lane);
+          qk_scores_mma_bf16<D, ROW, WIN>(stage + g * D * ES, limit, qa, p.scale_log2, sc4, lane);
         // online softmax (base 2) of head r: its 16 scores sit in lanes 4r .. 4r + 3
         float mx = fmaxf(fmaxf(sc4[0], sc4[1]), fmaxf(sc4[2], sc4[3]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -709,7 +774,8 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
-            const unsigned char* src = vb + (tok < ntok ? tok : 0) * ROW;
+            const unsigned char* src =
+                vb + (token_seen<WIN>(limit, tok) ? tok : seen_token<WIN>(limit)) * ROW;
             if constexpr (VW % 4 == 0) {
 #pragma unroll
               for (int v = 0; v < VW / 4; ++v) {
@@ -737,7 +803,7 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
           // B = P^T; for codes times the token's value scale and 2^9, which
           // keeps the product in f16's normal range for row maxima from about
           // 1e-3 to 5e4 (the 2^9 comes out exactly when the result is written)
-          pv[k] = tok < ntok ? (F8 ? pr * (vs[k] * 512.f) : pr) : 0.f;
+          pv[k] = token_seen<WIN>(limit, tok) ? (F8 ? pr * (vs[k] * 512.f) : pr) : 0.f;
         }
         l_lane = l_lane * alpha + lsum;
         m_run = m_new;
@@ -801,7 +867,7 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
           if (atomicAdd(&S.released[st], 1) == NKV - 1) {
             S.released[st] = 0;
             if (i + NST < n_pages && !*abort_flag) {
-              fetch_page<FUSE, F8>(p, fc, smem_addr(stage), smem_addr(&S.full[st]),
+              fetch_page<FUSE, F8, WIN>(p, fc, smem_addr(stage), smem_addr(&S.full[st]),
                                &S.fused_slot[st]);
               S.last_issued[st] = i + NST;
             }
@@ -954,13 +1020,13 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
       // page i: every warp reads every page, so this warp waited for page
       // i - NST of the stage; page i + NST is copied after all release page i
       mbar_wait(smem_addr(&S.full[st]), st_phase, p.err, abort_flag);
-      const int ntok = min(kBlock, L - cur.j * kBlock);
+      const int limit = page_limit<WIN>(p, L, cur.j);
       const int fslot = FUSE ? S.fused_slot[st] : -1;
       if (FUSE && fslot >= 0 && lane == 0) {
         // fused scatter: this kv head's slice of the new key row to its slot
         bulk_s2g(reinterpret_cast<unsigned char*>(const_cast<void*>(p.k_cache)) +
                      (size_t)fslot * ROW + g * D * ES,
-                 smem_addr(stage + (ntok - 1) * ROW + g * D * ES), D * ES);
+                 smem_addr(stage + (limit - 1) * ROW + g * D * ES), D * ES);
         bulk_commit();
         stored = true;
       }
@@ -968,10 +1034,10 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
       const bool seg_end = seq_done || (i + 1 == n_pages);
       PBuf<G>& pb = S.pb[g][b];
       float sc[NIT_QK];
-      if (ntok == kBlock)
-        qk_scores<D, G, E_QK, LPT_QK, ROW, true>(stage + k_off, ntok, tok_lane, qf, sc, lane);
+      if (all_seen<WIN>(limit))
+        qk_scores<D, G, E_QK, LPT_QK, ROW, true, WIN>(stage + k_off, limit, tok_lane, qf, sc, lane);
       else
-        qk_scores<D, G, E_QK, LPT_QK, ROW, false>(stage + k_off, ntok, tok_lane, qf, sc, lane);
+        qk_scores<D, G, E_QK, LPT_QK, ROW, false, WIN>(stage + k_off, limit, tok_lane, qf, sc, lane);
       // online softmax (base 2) for head my_h over the page's 16 tokens
       float mx = sc[0];
 #pragma unroll
@@ -1010,7 +1076,7 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
         if (atomicAdd(&S.released[st], 1) == NW - 1) {
           S.released[st] = 0;
           if (i + NST < n_pages && !*abort_flag) {
-            fetch_page<FUSE, F8>(p, fc, smem_addr(stage), smem_addr(&S.full[st]),
+            fetch_page<FUSE, F8, WIN>(p, fc, smem_addr(stage), smem_addr(&S.full[st]),
                              &S.fused_slot[st]);
             S.last_issued[st] = i + NST;
           }
@@ -1046,13 +1112,13 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
       const int b = i & 1;
       // page i: as for the QK warps (every warp reads every page)
       mbar_wait(smem_addr(&S.full[st]), st_phase, p.err, abort_flag);
-      const int ntok = min(kBlock, L - cur.j * kBlock);
+      const int limit = page_limit<WIN>(p, L, cur.j);
       const int fslot = FUSE ? S.fused_slot[st] : -1;
       if (FUSE && fslot >= 0 && lane == 0) {
         // fused scatter: this kv head's slice of the new value row to its slot
         bulk_s2g(reinterpret_cast<unsigned char*>(const_cast<void*>(p.v_cache)) +
                      (size_t)fslot * ROW + g * D * ES,
-                 smem_addr(stage + p.page_bytes + (ntok - 1) * ROW + g * D * ES), D * ES);
+                 smem_addr(stage + p.page_bytes + (limit - 1) * ROW + g * D * ES), D * ES);
         bulk_commit();
         stored = true;
       }
@@ -1070,10 +1136,10 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
         for (int e = 0; e < 4; ++e) acc[h][e] = __fmul2_rn(acc[h][e], a2);
       }
       const float* pp = &pb.p[tok_lane][0];
-      if (ntok == kBlock)
-        pv_accumulate<D, G, LPT_PV, ROW, true>(stage + v_off, pp, ntok, tok_lane, acc);
+      if (all_seen<WIN>(limit))
+        pv_accumulate<D, G, LPT_PV, ROW, true, WIN>(stage + v_off, pp, limit, tok_lane, acc);
       else
-        pv_accumulate<D, G, LPT_PV, ROW, false>(stage + v_off, pp, ntok, tok_lane, acc);
+        pv_accumulate<D, G, LPT_PV, ROW, false, WIN>(stage + v_off, pp, limit, tok_lane, acc);
       const bool seq_done = (cur.j + 1 == cur.np);
       const bool seg_end = seq_done || (i + 1 == n_pages);
       float m_fin[G], l_fin[G];
@@ -1088,7 +1154,7 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
         if (atomicAdd(&S.released[st], 1) == NW - 1) {
           S.released[st] = 0;
           if (i + NST < n_pages && !*abort_flag) {
-            fetch_page<FUSE, F8>(p, fc, smem_addr(stage), smem_addr(&S.full[st]),
+            fetch_page<FUSE, F8, WIN>(p, fc, smem_addr(stage), smem_addr(&S.full[st]),
                              &S.fused_slot[st]);
             S.last_issued[st] = i + NST;
           }
@@ -1197,7 +1263,7 @@ constexpr int kMergeWarps = 4;
 // eight per lane); past it, it reads the record the decode kernel wrote.
 constexpr int kMergeScanMax = 256;
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool WIN>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const DecodeParams p) {
   __shared__ float w_m[kMergeWarps], w_l[kMergeWarps];
   __shared__ float4 w_o[kMergeWarps][32];
@@ -1208,7 +1274,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
   // the request's shape and output row come from the call's inputs, which
   // are complete before the decode grid starts: read them before waiting for
   // it (with SPLIT every early return below is the same for the whole CTA)
-  const int np_s = decode_pages(p, s, false);
+  const int np_s = decode_pages<WIN>(p, s, false);
   if (np_s == 0) return;  // not a (valid) decode request
   const int a_row = __ldg(p.qsl + s);
   const int C = p.ctas;
@@ -1223,7 +1289,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
 #pragma unroll
     for (int i = 0; i < kMergeScanMax / 32; ++i) {  // all loads in flight at once
       const int s2 = lane + 32 * i;
-      const int n = s2 < p.num_seqs ? decode_pages(p, s2, false) : 0;
+      const int n = s2 < p.num_seqs ? decode_pages<WIN>(p, s2, false) : 0;
       tot += n;
       if (s2 < s) before += n;
     }
@@ -1336,7 +1402,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
 constexpr size_t kSmemBudget = 220 * 1024;
 constexpr size_t kSmemBudgetF8 = 226 * 1024;  // below the 227 KB opt-in limit per block
 
-template <int D, int G, int NKV, bool F8, bool FUSE, bool MW>
+template <int D, int G, int NKV, bool F8, bool FUSE, bool MW, bool WIN>
 cudaError_t launch_decode_t(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
                             cudaStream_t stream) {
   DecodeParams p;
@@ -1362,6 +1428,8 @@ cudaError_t launch_decode_t(const AttnArgs& a, const DecodeWorkspace& ws, int ct
   p.n_kv = a.num_kv_heads;
   p.max_seq_len = a.max_seq_len;
   p.block_shift = a.block_shift;
+  p.window = a.window;
+  p.num_sinks = a.num_sinks;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.ctas = ctas;
   p.row_bytes = (uint32_t)NKV * D * (F8 ? 1 : 2);
@@ -1384,7 +1452,7 @@ cudaError_t launch_decode_t(const AttnArgs& a, const DecodeWorkspace& ws, int ct
   if (nst < 2) return cudaErrorInvalidConfiguration;
   p.nstages = nst;
   const size_t smem = (size_t)nst * p.stage_bytes + fixed;
-  auto kern = decode_kernel<D, G, NKV, F8, FUSE, MW>;
+  auto kern = decode_kernel<D, G, NKV, F8, FUSE, MW, WIN>;
   constexpr int threads = decode_threads<NKV, F8, MW>();
   static int configured_device = -1;  // one attribute set per process and device
   int dev = 0;
@@ -1429,8 +1497,8 @@ cudaError_t launch_decode_t(const AttnArgs& a, const DecodeWorkspace& ws, int ct
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return split ? cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, true>, p)
-               : cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, false>, p);
+  return split ? cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, true, WIN>, p)
+               : cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, false, WIN>, p);
 }
 
 // Tensor-core warps for the 8-bit cache always; for a bf16 cache when the
@@ -1440,33 +1508,33 @@ constexpr bool decode_uses_mma() {
   return F8 || G == 8;
 }
 
-template <int D, int G, bool F8, bool FUSE>
+template <int D, int G, bool F8, bool FUSE, bool WIN>
 cudaError_t launch_decode_dg(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
                              cudaStream_t stream) {
   constexpr bool MW = decode_uses_mma<F8, G>();
   switch (a.num_kv_heads) {
-    case 1: return launch_decode_t<D, G, 1, F8, FUSE, MW>(a, ws, ctas, stream);
-    case 2: return launch_decode_t<D, G, 2, F8, FUSE, MW>(a, ws, ctas, stream);
-    case 4: return launch_decode_t<D, G, 4, F8, FUSE, MW>(a, ws, ctas, stream);
-    case 8: return launch_decode_t<D, G, 8, F8, FUSE, MW>(a, ws, ctas, stream);
+    case 1: return launch_decode_t<D, G, 1, F8, FUSE, MW, WIN>(a, ws, ctas, stream);
+    case 2: return launch_decode_t<D, G, 2, F8, FUSE, MW, WIN>(a, ws, ctas, stream);
+    case 4: return launch_decode_t<D, G, 4, F8, FUSE, MW, WIN>(a, ws, ctas, stream);
+    case 8: return launch_decode_t<D, G, 8, F8, FUSE, MW, WIN>(a, ws, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }
 
-template <bool F8, bool FUSE>
+template <bool F8, bool FUSE, bool WIN>
 cudaError_t launch_decode_any(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
                               cudaStream_t stream) {
   const int group = a.num_q_heads / a.num_kv_heads;
   if (a.head_dim == 128) {
-    if (group == 1) return launch_decode_dg<128, 1, F8, FUSE>(a, ws, ctas, stream);
-    if (group == 2) return launch_decode_dg<128, 2, F8, FUSE>(a, ws, ctas, stream);
-    if (group == 4) return launch_decode_dg<128, 4, F8, FUSE>(a, ws, ctas, stream);
-    if (group == 8) return launch_decode_dg<128, 8, F8, FUSE>(a, ws, ctas, stream);
+    if (group == 1) return launch_decode_dg<128, 1, F8, FUSE, WIN>(a, ws, ctas, stream);
+    if (group == 2) return launch_decode_dg<128, 2, F8, FUSE, WIN>(a, ws, ctas, stream);
+    if (group == 4) return launch_decode_dg<128, 4, F8, FUSE, WIN>(a, ws, ctas, stream);
+    if (group == 8) return launch_decode_dg<128, 8, F8, FUSE, WIN>(a, ws, ctas, stream);
   } else if (a.head_dim == 64) {
-    if (group == 1) return launch_decode_dg<64, 1, F8, FUSE>(a, ws, ctas, stream);
-    if (group == 2) return launch_decode_dg<64, 2, F8, FUSE>(a, ws, ctas, stream);
-    if (group == 4) return launch_decode_dg<64, 4, F8, FUSE>(a, ws, ctas, stream);
-    if (group == 8) return launch_decode_dg<64, 8, F8, FUSE>(a, ws, ctas, stream);
+    if (group == 1) return launch_decode_dg<64, 1, F8, FUSE, WIN>(a, ws, ctas, stream);
+    if (group == 2) return launch_decode_dg<64, 2, F8, FUSE, WIN>(a, ws, ctas, stream);
+    if (group == 4) return launch_decode_dg<64, 4, F8, FUSE, WIN>(a, ws, ctas, stream);
+    if (group == 8) return launch_decode_dg<64, 8, F8, FUSE, WIN>(a, ws, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }

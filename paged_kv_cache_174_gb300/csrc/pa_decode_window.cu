@@ -1,0 +1,13 @@
+// pa_decode_window.cu -- the sliding-window instantiations of the split-KV decode kernel
+// (pa_decode_kernel.cuh) over the bf16 cache.  A translation unit of its own
+// so that the instantiations compile in parallel.
+#include "pa_decode_kernel.cuh"
+
+namespace pa {
+
+cudaError_t launch_decode_window(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
+                                 cudaStream_t stream) {
+  return launch_decode_any<false, false, true>(a, ws, ctas, stream);
+}
+
+}  // namespace pa

@@ -103,6 +103,11 @@ cudaError_t launch_decode_fp8(const AttnArgs& a, const DecodeWorkspace& ws, int 
 cudaError_t launch_decode_fused(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
                                 cudaStream_t stream);
 
+cudaError_t launch_decode_window(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
+                                 cudaStream_t stream);
+cudaError_t launch_decode_window_fp8(const AttnArgs& a, const DecodeWorkspace& ws, int ctas,
+                                     cudaStream_t stream);
+
 bool prefill_supported(int head_dim, int group, int num_kv_heads);
 // How the prefill kernel splits the keys of each query-tile pair, and the
 // workspace bytes the pieces take (0 when nsplit == 1).
@@ -183,9 +188,6 @@ struct RotaryArgs {
   bool fp8;
 };
 cudaError_t launch_rotary_cache(const RotaryArgs& p, cudaStream_t stream);
-
-// Attention with a sliding window (AttnArgs.window > 0; pa_window.cu).
-cudaError_t launch_window(const AttnArgs& a, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, unsigned* err,
                                          cudaStream_t stream);

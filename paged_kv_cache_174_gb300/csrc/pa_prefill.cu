@@ -56,14 +56,17 @@ size_t prefill_workspace_bound(int num_tokens, int num_q_heads, int num_kv_heads
 cudaError_t launch_prefill(const AttnArgs& a, const PrefillPlan& plan, void* ws, int sm_count,
                            cudaStream_t stream) {
   const int group = a.num_q_heads / a.num_kv_heads;
+  if (a.window > 0)
+    return a.fp8 ? launch_prefill_window_fp8(a, plan, ws, sm_count, stream)
+                 : launch_prefill_window(a, plan, ws, sm_count, stream);
   if (a.fp8) return launch_prefill_fp8(a, plan, ws, sm_count, stream);
   // the fused step's instance loads new rows from k_new / v_new and stores
   // them; the plain one reads the cache only
   const bool fuse = a.fuse_slot_mapping != nullptr;
 #define PA_PREFILL_CASE(D_, G_)                                                         \
   if (a.head_dim == D_ && group == G_)                                                  \
-    return fuse ? launch_prefill_t<D_, G_, kKindFused>(a, plan, ws, sm_count, stream) \
-                : launch_prefill_t<D_, G_, kKindPlain>(a, plan, ws, sm_count, stream);
+    return fuse ? launch_prefill_t<D_, G_, kKindFused, false>(a, plan, ws, sm_count, stream) \
+                : launch_prefill_t<D_, G_, kKindPlain, false>(a, plan, ws, sm_count, stream);
   PA_PREFILL_CASE(128, 1)
   PA_PREFILL_CASE(128, 2)
   PA_PREFILL_CASE(128, 4)

@@ -10,7 +10,7 @@ cudaError_t launch_prefill_fp8(const AttnArgs& a, const PrefillPlan& plan, void*
   const int group = a.num_q_heads / a.num_kv_heads;
 #define PA_PREFILL_FP8_CASE(D_, G_)    \
   if (a.head_dim == D_ && group == G_) \
-    return launch_prefill_t<D_, G_, kKindFp8>(a, plan, ws, sm_count, stream);
+    return launch_prefill_t<D_, G_, kKindFp8, false>(a, plan, ws, sm_count, stream);
   PA_PREFILL_FP8_CASE(128, 1)
   PA_PREFILL_FP8_CASE(128, 2)
   PA_PREFILL_FP8_CASE(128, 4)

@@ -114,6 +114,7 @@ struct PrefillParams {
   int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_q, n_kv, max_seq_len, nsplit;
   int32_t block_shift;  // log2(block_size / 16)
   int32_t no_decode;    // a request with one query row is an error (no decode kernel runs)
+  int32_t window, num_sinks;  // sliding window (the WIN instances)
   float scale_log2;
 };
 
@@ -153,14 +154,23 @@ struct Unit {
   int ntok;     // valid query tokens of the tile
   int p_first;  // position of token q0
   int kv_end;   // keys the tile needs: 0 .. kv_end - 1
-  int kt0, kt1; // K/V tiles of this unit (of ceil(kv_end / 128))
+  int kt0, kt1; // K/V tiles of this unit (of ceil(pages / 8))
+  int pages;    // pages the tile reads
+  // Sliding window: the keys are those before num_sinks and those from w0 on;
+  // the pages read are the first sink_pages ones, then skip pages further on
+  int w0, sink_pages, skip;
+  // Logical page of entry e of the pages read.
+  template <bool WIN>
+  __device__ __forceinline__ int page(int e) const {
+    return WIN && e >= sink_pages ? e + skip : e;
+  }
 };
 
 // Walks the unit list: request-major, then query tile, kv head, key split.
 // Requests are found through the block's list of prefill requests (sequence
 // ids and first tile indices, built once per CTA); when a batch holds more
 // than kMaxListed of them the cursor walks the sequences instead.
-template <int TM>
+template <int TM, bool WIN>
 struct UnitCursor {
   const int* seq;   // listed requests, or nullptr
   const int* tbase; // first tile of each listed request; tbase[n] = all tiles
@@ -208,7 +218,16 @@ struct UnitCursor {
     U.ntok = min(TM, ql - first);
     U.p_first = L - ql + first;
     U.kv_end = U.p_first + U.ntok;
-    const int nkt = (U.kv_end + kKeysPerTile - 1) / kKeysPerTile;
+    U.pages = (U.kv_end + kBlock - 1) / kBlock;
+    if constexpr (WIN) {
+      // what the tile's first row sees bounds the window of all of them
+      U.w0 = max(0, U.p_first - p.window + 1);
+      const int wp = U.w0 / kBlock;
+      U.sink_pages = p.num_sinks > wp * kBlock ? wp : (p.num_sinks + kBlock - 1) / kBlock;
+      U.skip = wp - U.sink_pages;
+      U.pages -= U.skip;
+    }
+    const int nkt = (U.pages + kPagesPerTile - 1) / kPagesPerTile;
     U.kt0 = U.ks * nkt / p.nsplit;
     U.kt1 = (U.ks + 1) * nkt / p.nsplit;
     return true;
@@ -401,7 +420,16 @@ __device__ __forceinline__ void fused_store_rows(const PrefillParams& p, const U
   }
 }
 
-template <int D, int G, int KIND>
+// The columns (keys) of a 16-key page at position base that the row at
+// position p sees, one bit each: not past p, in the window or among the sinks.
+__device__ __forceinline__ uint32_t window_bits(int base, int p, int window, int sinks) {
+  const int hi = min(max(p - base, -1), kBlock - 1);            // the last one not past p
+  const int lo = min(max(p - window + 1 - base, 0), kBlock);    // the first one in the window
+  const int ns = min(max(sinks - base, 0), kBlock);             // sinks
+  return ((1u << (hi + 1)) - 1u) & ((0xffffu << lo) | ((1u << ns) - 1u));
+}
+
+template <int D, int G, int KIND, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -553,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t nst = k_warp ? SK : SV;
       const uint32_t patch_bar = smem_addr(&B.patch[warp]);
       uint32_t n_patch = 0;
-      UnitCursor<TM> cur;
+      UnitCursor<TM, WIN> cur;
       cur.init(p, B.list_seq, B.list_base, B.listed);
       int n_out = 0, c = 0;
       Ring pos;
@@ -594,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ++n_out;
-        const int pages = (U.kv_end + kBlock - 1) / kBlock;
         const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
         for (int kt = U.kt0; kt < U.kt1; ++kt, ++c) {
           // per page: -1 (nothing to load), 0 (cached rows: the cache), 1
@@ -604,10 +631,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t bytes = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int lp = kt * kPagesPerTile + pg_lo + i;  // logical page
+            const int e = kt * kPagesPerTile + pg_lo + i;
             phys[i] = -1;
             kind[i] = -1;
-            if (pg_lo + i < pg_hi && lp < pages) {
+            if (pg_lo + i < pg_hi && e < U.pages) {
+              const int lp = U.template page<WIN>(e);  // logical page
               const int pos0 = lp * kBlock;
               if (FUSE && pos0 >= U.c0) {
                 kind[i] = 1;
@@ -785,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (waits spin without the suspend hint: these threads' latency is the
     // tensor pipe's)
     if (lane == 0) {
-      UnitCursor<TM> cur;
+      UnitCursor<TM, WIN> cur;
       cur.init(p, B.list_seq, B.list_base, B.listed);
       int n_out = 0;
       uint32_t ntiles = 0;  // tiles of S (or P V) issued so far, all units
@@ -881,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool pos_scale = sl2 > 0.f;
     const float mul = pos_scale ? 1.f : sl2;
     const float emul = pos_scale ? sl2 : 1.f;
-    UnitCursor<TM> cur;
+    UnitCursor<TM, WIN> cur;
     cur.init(p, B.list_seq, B.list_base, B.listed);
     int n_out = 0;
     Ring sbr, prev, prev2, vr;  // S buffer of this tile, the last one and the one
@@ -915,7 +943,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // causal mask and the max of this half (three-input max, 4 chains)
         const int lim = p_row - (kt * kKeysPerTile + kh * 64);  // keys c <= lim visible
-        if (__all_sync(0xffffffffu, lim >= 63)) {
+        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // with a window: a bit for each key
+        if constexpr (WIN) {
+#pragma unroll
+          for (int g4 = 0; g4 < 4; ++g4) {
+            // (an entry past the pages read lies past the tile's keys)
+            const int e = kt * kPagesPerTile + kh * 4 + g4;
+            const uint32_t bits = window_bits(U.template page<true>(e) * kBlock, p_row, p.window,
+                                              p.num_sinks);
+            if (g4 & 1)
+              seen[g4 >> 1] |= bits << 16;
+            else
+              seen[g4 >> 1] = bits & 0xffffu;
+          }
+        }
+        if (WIN ? __all_sync(0xffffffffu, (seen[0] & seen[1]) == 0xffffffffu)
+                : __all_sync(0xffffffffu, lim >= 63)) {
           if (!pos_scale) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * mul);
@@ -923,7 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            sr[c] = __float_as_uint((c <= lim) ? __uint_as_float(sr[c]) * mul : kNegInf);
+            sr[c] = __float_as_uint((WIN ? (seen[c >> 5] >> (c & 31)) & 1u : c <= lim)
+                                        ? __uint_as_float(sr[c]) * mul
+                                        : kNegInf);
         }
         float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
@@ -1003,8 +1048,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys past the last needed one: V rows there may hold stale or
         // poisoned data; zero them so that P = 0 times V stays 0.  Thread r
         // clears half of the 16-byte chunks of V row 64 kh + r / 2.
+        // (With a window also the rows before the tile's window that are no
+        // sinks, and those of entries past the pages read.)
         const int kv_local = U.kv_end - kt * kKeysPerTile;
-        if (kv_local < kKeysPerTile) {
+        const int key = kh * 64 + (r >> 1);
+        bool unseen = key >= kv_local;
+        if constexpr (WIN) {
+          const int pos = U.template page<true>(kt * kPagesPerTile + (key >> 4)) * kBlock +
+                          (key & 15);
+          unseen = pos >= U.kv_end || (pos >= p.num_sinks && pos < U.w0);
+        }
+        if (WIN ? __any_sync(0xffffffffu, unseen) : kv_local < kKeysPerTile) {
           // A parity wait tells apart only two phases in a row: the stage's
           // barrier must be at this tile's use or the one after, never still
           // at the use SV tiles back (its phase has this tile's parity, and
@@ -1022,8 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_wait(smem_addr(&B.pv_done[prev2.stage]), prev2.phase, p.err, abort_flag);
           }
           mbar_wait(smem_addr(&B.v_full[vr.stage]), vr.phase, p.err, abort_flag);
-          const int key = kh * 64 + (r >> 1);
-          if (key >= kv_local) {
+          if (unseen) {
             unsigned char* vpage = v_s + vr.stage * KV_BYTES + (key >> 4) * V_PAGE;
 #pragma unroll
             for (int h = 0; h < NH; ++h)
@@ -1215,7 +1268,7 @@ size_t split_bytes(int num_tokens, int num_q_heads, int head_dim, int nsplit) {
          ((rows * 2 * sizeof(float) + 255) & ~size_t(255));
 }
 
-template <int D, int G, int KIND>
+template <int D, int G, int KIND, bool WIN>
 cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* ws, int sm_count,
                              cudaStream_t stream) {
   constexpr bool FUSE = KIND == kKindFused;
@@ -1246,6 +1299,8 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
   p.block_shift = a.block_shift;
   p.no_decode = a.no_decode ? 1 : 0;
   p.nsplit = plan.nsplit;
+  p.window = a.window;
+  p.num_sinks = a.num_sinks;
   // the 8-bit instance scales the query tile itself (f16 operands), so its
   // scores arrive in base-2 units
   p.q_mul = a.scale * 1.4426950408889634f;
@@ -1319,7 +1374,7 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
   const int grid = (int)(units_bound < sm_count ? units_bound : sm_count);
   if (grid <= 0) return cudaSuccess;
   const size_t smem = prefill_smem_bytes<D, G>();
-  auto kern = prefill_kernel<D, G, KIND>;
+  auto kern = prefill_kernel<D, G, KIND, WIN>;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1349,8 +1404,13 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
 
 }  // namespace
 
-// The 8-bit cache's instance (pa_prefill_fp8.cu).
+// The 8-bit cache's instance (pa_prefill_fp8.cu), and the sliding window's
+// (pa_prefill_window.cu, pa_prefill_window_fp8.cu).
 cudaError_t launch_prefill_fp8(const AttnArgs& a, const PrefillPlan& plan, void* ws,
                                int sm_count, cudaStream_t stream);
+cudaError_t launch_prefill_window(const AttnArgs& a, const PrefillPlan& plan, void* ws,
+                                  int sm_count, cudaStream_t stream);
+cudaError_t launch_prefill_window_fp8(const AttnArgs& a, const PrefillPlan& plan, void* ws,
+                                      int sm_count, cudaStream_t stream);
 
 }  // namespace pa

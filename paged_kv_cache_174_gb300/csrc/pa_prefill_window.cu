@@ -1,0 +1,26 @@
+// pa_prefill_window.cu -- the chunked-prefill kernel's sliding-window instance for the
+// bf16 cache, in a translation unit of its own so that the instances compile
+// in parallel.
+#include "pa_prefill_kernel.cuh"
+
+namespace pa {
+
+cudaError_t launch_prefill_window(const AttnArgs& a, const PrefillPlan& plan, void* ws,
+                                  int sm_count, cudaStream_t stream) {
+  const int group = a.num_q_heads / a.num_kv_heads;
+#define PA_PREFILL_WINDOW_CASE(D_, G_) \
+  if (a.head_dim == D_ && group == G_)   \
+    return launch_prefill_t<D_, G_, kKindPlain, true>(a, plan, ws, sm_count, stream);
+  PA_PREFILL_WINDOW_CASE(128, 1)
+  PA_PREFILL_WINDOW_CASE(128, 2)
+  PA_PREFILL_WINDOW_CASE(128, 4)
+  PA_PREFILL_WINDOW_CASE(128, 8)
+  PA_PREFILL_WINDOW_CASE(64, 1)
+  PA_PREFILL_WINDOW_CASE(64, 2)
+  PA_PREFILL_WINDOW_CASE(64, 4)
+  PA_PREFILL_WINDOW_CASE(64, 8)
+#undef PA_PREFILL_WINDOW_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa
