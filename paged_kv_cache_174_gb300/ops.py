@@ -551,15 +551,24 @@ def copy_blocks_fp8(k_cache, v_cache, src_dst_pairs: torch.Tensor, *, num_kv_hea
 # current, and allocate what the caller does not pass on the stream they use.
 # ---------------------------------------------------------------------------
 
-def _one_device(named) -> torch.device:
-    """The one CUDA device of the (name, tensor) pairs whose tensor is not None."""
-    device = None
-    for name, t in named:
+def _check_tensors(specs) -> torch.device:
+    """Checks (name, tensor, dtype, dimensions) of a call's tensors: contiguous
+    CUDA tensors of that type, all on one device, which is returned.  None
+    tensors are skipped.  One pass of cheap tests; the error comes from _need."""
+    index = None
+    for name, t, dtype, dim in specs:
         if t is None:
             continue
-        if device is None:
-            device = t.device
-        elif t.device != device:
+        if type(t) is not torch.Tensor or t.dtype is not dtype or t.dim() != dim or \
+                not t.is_contiguous():
+            _need(t, name, dtype, dim)
+        on = t.get_device()  # -1: not a CUDA tensor
+        if index is None:
+            if on < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            index, device = on, t.device
+        elif on != index:
+            _need(t, name, dtype, dim)
             raise ValueError(f"{name} is on {t.device}, other tensors on {device}")
     return device
 
@@ -579,29 +588,34 @@ def _other_device_or_stream(device, stream):
 class _Here:
     """The plain case of _launching: current device, current stream."""
 
+    def __init__(self, index):
+        self.index = index
+
     def __enter__(self):
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         return False
 
 
-_HERE_AND_NOW = _Here()
+# the current stream's handle by device index (current_stream() makes a Stream
+# object for each call: 2.9 us against 0.1 us on the GB300 host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_here: dict = {}
 
 
 def _launching(device, stream):
     """Context with the tensors' device current and the stream's allocator in
     use; its value is the stream's handle."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _HERE_AND_NOW
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return _here.get(index) or _here.setdefault(index, _Here(index))
     return _other_device_or_stream(device, stream)
 
 
-def _int32_out(t, name, shape, device):
-    if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
-    _need(t, name, torch.int32)
-    if tuple(t.shape) != tuple(shape):
+def _shaped(t, name, shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
@@ -625,121 +639,133 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
     [S + 1], slot_mapping [num_tokens], positions [num_axes, num_tokens]); each
     may be passed in to be written (seq_lens may be context_lens itself).
     """
-    L = _load()
-    _need(context_lens, "context_lens", torch.int32, 1)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(free_blocks, "free_blocks", torch.int32, 1)
-    _need(free_count, "free_count", torch.int32)
-    S, T, A = context_lens.shape[0], int(num_tokens), int(num_axes)
-    if new_lens.shape[0] != S or block_tables.shape[0] != S:
-        raise ValueError("context_lens [S], new_lens [S], block_tables [S, max_blocks] disagree")
+    L = _lib or _load()
+    i32 = torch.int32
+    T, A = int(num_tokens), int(num_axes)
     if T < 0 or A < 0:
         raise ValueError(f"num_tokens {T} and num_axes {A} must not be negative")
-    if free_count.numel() != 1:
-        raise ValueError("free_count must hold one value")
+    device = _check_tensors((
+        ("context_lens", context_lens, i32, 1), ("new_lens", new_lens, i32, 1),
+        ("block_tables", block_tables, i32, 2), ("free_blocks", free_blocks, i32, 1),
+        ("free_count", free_count, i32, 1), ("free_count_out", free_count_out, i32, 1),
+        ("position_offsets", position_offsets, i32, 1), ("seq_lens", seq_lens, i32, 1),
+        ("query_start_loc", query_start_loc, i32, 1), ("slot_mapping", slot_mapping, i32, 1),
+        ("positions", positions, i32, 2)))
+    S, width = block_tables.shape
+    lens = (S,)
+    _shaped(context_lens, "context_lens", lens)
+    _shaped(new_lens, "new_lens", lens)
+    _shaped(free_count, "free_count", (1,))
     if free_count_out is None:
         free_count_out = free_count
     else:
-        _need(free_count_out, "free_count_out", torch.int32)
-        if free_count_out.numel() != 1:
-            raise ValueError("free_count_out must hold one value")
+        _shaped(free_count_out, "free_count_out", (1,))
     if position_offsets is not None:
-        _need(position_offsets, "position_offsets", torch.int32, 1)
-        if position_offsets.shape[0] != S:
-            raise ValueError("position_offsets must be [S]")
-    device = _one_device((("context_lens", context_lens), ("new_lens", new_lens),
-                          ("block_tables", block_tables), ("free_blocks", free_blocks),
-                          ("free_count", free_count), ("free_count_out", free_count_out),
-                          ("position_offsets", position_offsets), ("seq_lens", seq_lens),
-                          ("query_start_loc", query_start_loc), ("slot_mapping", slot_mapping),
-                          ("positions", positions)))
+        _shaped(position_offsets, "position_offsets", lens)
     with _launching(device, stream) as handle:
-        seq_lens = _int32_out(seq_lens, "seq_lens", (S,), device)
-        query_start_loc = _int32_out(query_start_loc, "query_start_loc", (S + 1,), device)
-        slot_mapping = _int32_out(slot_mapping, "slot_mapping", (T,), device)
-        positions = _int32_out(positions, "positions", (A, T), device)
-        _check(L.pa_build_step(
+        seq_lens = torch.empty(S, dtype=i32, device=device) if seq_lens is None else \
+            _shaped(seq_lens, "seq_lens", lens)
+        query_start_loc = torch.empty(S + 1, dtype=i32, device=device) \
+            if query_start_loc is None else _shaped(query_start_loc, "query_start_loc", (S + 1,))
+        slot_mapping = torch.empty(T, dtype=i32, device=device) if slot_mapping is None else \
+            _shaped(slot_mapping, "slot_mapping", (T,))
+        positions = torch.empty(A, T, dtype=i32, device=device) if positions is None else \
+            _shaped(positions, "positions", (A, T))
+        code = L.pa_build_step(
             context_lens.data_ptr(), new_lens.data_ptr(),
             None if position_offsets is None else position_offsets.data_ptr(), S, T, A,
-            block_tables.data_ptr(), block_tables.shape[1], int(block_size),
-            free_blocks.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
-            free_blocks.shape[0], seq_lens.data_ptr(), query_start_loc.data_ptr(),
-            slot_mapping.data_ptr(), positions.data_ptr(), handle))
+            block_tables.data_ptr(), width, block_size, free_blocks.data_ptr(),
+            free_count.data_ptr(), free_count_out.data_ptr(), free_blocks.shape[0],
+            seq_lens.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
+            positions.data_ptr(), handle)
+    if code:
+        _check(code)
     return seq_lens, query_start_loc, slot_mapping, positions
 
 
-def _token_rows(t, name):
-    """A bf16 CUDA tensor [T, heads, d] whose tokens may be strided: (T, heads,
-    d, token stride)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _token_rows(t, name, index, T, d):
+    """Checks a bf16 CUDA tensor [T, heads, d] whose tokens may be strided;
+    returns (heads, token stride)."""
+    if type(t) is not torch.Tensor or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
-    T, heads, d = t.shape
+    n, heads, dt = t.shape
+    if n != T or dt != d:
+        raise ValueError("q [T, n_q, d], k and v [T, n_kv, d] disagree")
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"{name}'s heads must be contiguous within a token")
-    if T > 1 and (st < heads * d or st % 8):
+    if T <= 1:
+        return heads, heads * d
+    if st < heads * d or st % 8:
         raise ValueError(f"{name}'s tokens must not overlap, at a stride of a multiple of 8")
-    return T, heads, d, st if T > 1 else heads * d
+    return heads, st
 
 
 def _rotary(fp8, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, axes, interleaved,
             q_out, stream):
-    L = _load()
-    T, nq, d, q_stride = _token_rows(q, "q")
-    Tk, nkv, dk, k_stride = _token_rows(k, "k")
-    Tv, nv, dv, v_stride = _token_rows(v, "v")
-    if (Tk, Tv) != (T, T) or nv != nkv or (dk, dv) != (d, d):
-        raise ValueError("q [T, n_q, d], k and v [T, n_kv, d] disagree")
+    L = _lib or _load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [T, n_q, d]")
+    T, _, d = q.shape
+    index = q.get_device()
+    nq, q_stride = _token_rows(q, "q", index, T, d)
+    nkv, k_stride = _token_rows(k, "k", index, T, d)
+    nv, v_stride = _token_rows(v, "v", index, T, d)
+    kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
+    device = _check_tensors((
+        ("k_cache", k_cache, kind, dims), ("v_cache", v_cache, kind, dims),
+        ("slot_mapping", slot_mapping, torch.int32, 1),
+        ("inv_freq", inv_freq, torch.float64, 1), ("axes", axes, torch.int32, 1),
+        ("q_out", q_out, torch.bfloat16, 3)))
+    if device.index != index:
+        raise ValueError(f"q is on {q.device}, other tensors on {device}")
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be alike")
+    if nv != nkv:
+        raise ValueError("k and v [T, n_kv, d] disagree")
     if fp8:
         nb, bs = _fp8_geometry(k_cache, v_cache, nkv, d)
     else:
-        _need(k_cache, "k_cache", torch.bfloat16, 4)
-        _need(v_cache, "v_cache", torch.bfloat16, 4)
-        nb, bs, n, dc = k_cache.shape
-        if v_cache.shape != k_cache.shape or (n, dc) != (nkv, d):
-            raise ValueError("caches must be alike, [num_blocks, block_size, n_kv, d]")
-    _need(slot_mapping, "slot_mapping", torch.int32, 1)
-    _need(inv_freq, "inv_freq", torch.float64, 1)
+        nb, bs, n, dc = shape
+        if n != nkv or dc != d:
+            raise ValueError("caches must be [num_blocks, block_size, n_kv, d]")
     half = inv_freq.shape[0]
     if slot_mapping.shape[0] != T:
         raise ValueError("slot_mapping must be [T]")
-    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+    if type(positions) is not torch.Tensor or positions.dtype is not torch.int32:
         raise TypeError("positions must be a torch.int32 tensor")
-    if not positions.is_cuda:
-        raise ValueError("positions must be a CUDA tensor")
-    if positions.dim() not in (1, 2) or positions.shape[-1] != T or \
-            (T > 1 and positions.stride(-1) != 1):
+    if positions.get_device() != index:
+        raise ValueError("positions must be a CUDA tensor on the other tensors' device")
+    A, p_stride = 1, T
+    if positions.dim() == 2:
+        A = positions.shape[0]
+        p_stride = max(positions.stride(0), T) if A > 0 else T
+        if A > 1 and positions.stride(0) < T:
+            raise ValueError("the rows of positions overlap")
+    elif positions.dim() != 1:
+        raise ValueError("positions must be [T] or [num_axes, T]")
+    if positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
         raise ValueError("positions must be [T] or [num_axes, T] with contiguous rows")
-    A = 1 if positions.dim() == 1 else positions.shape[0]
-    p_stride = T if positions.dim() == 1 else max(positions.stride(0), T)
-    if A > 1 and positions.stride(0) < T:
-        raise ValueError("the rows of positions overlap")
-    if axes is not None:
-        _need(axes, "axes", torch.int32, 1)
-        if axes.shape[0] != half:
-            raise ValueError("axes must name an axis for each entry of inv_freq")
-    device = _one_device((("q", q), ("k", k), ("v", v), ("positions", positions),
-                          ("inv_freq", inv_freq), ("k_cache", k_cache), ("v_cache", v_cache),
-                          ("slot_mapping", slot_mapping), ("axes", axes), ("q_out", q_out)))
+    if axes is not None and axes.shape[0] != half:
+        raise ValueError("axes must name an axis for each entry of inv_freq")
+    if q_out is not None and q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
     with _launching(device, stream) as handle:
         if q_out is None:
             q_out = torch.empty(T, nq, d, dtype=torch.bfloat16, device=device)
-        _need(q_out, "q_out", torch.bfloat16, 3)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
         fn = L.pa_rotary_reshape_and_cache_fp8 if fp8 else L.pa_rotary_reshape_and_cache
-        _check(fn(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, T,
+        code = fn(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, T,
                   positions.data_ptr(), p_stride, A, inv_freq.data_ptr(),
-                  None if axes is None else axes.data_ptr(), 2 * half, int(bool(interleaved)),
+                  None if axes is None else axes.data_ptr(), 2 * half, 1 if interleaved else 0,
                   q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
-                  slot_mapping.data_ptr(), handle))
+                  slot_mapping.data_ptr(), handle)
+    if code:
+        _check(code)
     return q_out
 
 
@@ -778,46 +804,45 @@ def rotary_reshape_and_cache_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
 def _window_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
                       window, num_sinks, min_q_len, max_q_len, max_seq_len, out, workspace,
                       stream):
-    L = _load()
-    _need(q, "q", torch.bfloat16, 3)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(query_start_loc, "query_start_loc", torch.int32, 1)
-    T, nq, d = q.shape
+    L = _lib or _load()
+    kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
+    device = _check_tensors((
+        ("q", q, torch.bfloat16, 3), ("k_cache", k_cache, kind, dims),
+        ("v_cache", v_cache, kind, dims), ("block_tables", block_tables, torch.int32, 2),
+        ("seq_lens", seq_lens, torch.int32, 1),
+        ("query_start_loc", query_start_loc, torch.int32, 1), ("out", out, torch.bfloat16, 3),
+        ("workspace", workspace, torch.uint8, 1)))
+    shape, cache = q.shape, k_cache.shape
+    T, nq, d = shape
+    if v_cache.shape != cache:
+        raise ValueError("k_cache and v_cache must be alike")
     if fp8:
-        _need(k_cache, "k_cache", torch.uint8, 3)
-        nkv = k_cache.shape[2] // fp8_page_bytes(1, d)
+        nkv = cache[2] // fp8_page_bytes(1, d)
         nb, bs = _fp8_geometry(k_cache, v_cache, nkv, d)
-        if nkv <= 0 or nq % nkv != 0:
-            raise ValueError(f"num_q_heads {nq} must be a multiple of num_kv_heads {nkv}")
-        S = seq_lens.shape[0]
-        if block_tables.shape[0] != S or query_start_loc.shape[0] != S + 1:
-            raise ValueError("block_tables [S, max_blocks], seq_lens [S], "
-                             "query_start_loc [S + 1] disagree")
-        if out is not None and out.shape != q.shape:
-            raise ValueError("out must have q's shape")
     else:
-        _need(k_cache, "k_cache", torch.bfloat16, 4)
-        _need(v_cache, "v_cache", torch.bfloat16, 4)
-        T, nq, d, nb, bs, nkv, S = _attention_shapes(q, k_cache, v_cache, block_tables, seq_lens,
-                                                     query_start_loc, out)
-    device = _one_device((("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                          ("block_tables", block_tables), ("seq_lens", seq_lens),
-                          ("query_start_loc", query_start_loc), ("out", out),
-                          ("workspace", workspace)))
+        nb, bs, nkv, dc = cache
+        if dc != d:
+            raise ValueError("q / k_cache / v_cache head_dim disagree")
+    if nkv <= 0 or nq % nkv != 0:
+        raise ValueError(f"num_q_heads {nq} must be a multiple of num_kv_heads {nkv}")
+    S, width = block_tables.shape
+    if seq_lens.shape[0] != S or query_start_loc.shape[0] != S + 1:
+        raise ValueError("seq_lens [S], query_start_loc [S+1], block_tables [S, maxb] disagree")
+    if out is not None and out.shape != shape:
+        raise ValueError("out must have q's shape")
     with _launching(device, stream) as handle:
         if out is None:
             out = torch.empty_like(q)
-        _need(out, "out", torch.bfloat16, 3)
         if workspace is None:
             workspace = alloc_workspace(S, T, nq, nkv, d, max_q_len, max_seq_len, device)
-        _need_workspace(workspace)
         fn = L.pa_paged_attention_window_fp8 if fp8 else L.pa_paged_attention_window
-        _check(fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
-                  block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-                  query_start_loc.data_ptr(), S, T, int(min_q_len), int(max_q_len),
-                  int(max_seq_len), int(window), int(num_sinks), float(scale), out.data_ptr(),
-                  workspace.data_ptr(), workspace.numel(), handle))
+        code = fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
+                  block_tables.data_ptr(), width, seq_lens.data_ptr(),
+                  query_start_loc.data_ptr(), S, T, min_q_len, max_q_len, max_seq_len, window,
+                  num_sinks, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                  handle)
+    if code:
+        _check(code)
     return out
 
 
