@@ -16,9 +16,11 @@
 // top 32 bits, as a signed fraction of a half turn, feed sincospif, which
 // reduces nothing further.
 //
-// Bytes: q, k and v are read once and written once (HBM-bound); a lane holds
-// the same 16 elements of every head it handles, so it needs the same eight
-// (cos, sin) pairs for all of them.
+// Bytes: q, k and v are read once and written once (HBM-bound).  A warp works
+// on one token by itself: its lanes compute the token's cosines and sines, two
+// each, into shared memory while the first heads' loads are in flight, and a
+// lane then holds the same 16 elements of every head it handles, so it keeps
+// the same eight (cos, sin) pairs in registers for all of them.
 #include <cstdint>
 
 #include "pa_common.cuh"
@@ -28,6 +30,12 @@ namespace pa {
 namespace {
 
 constexpr int kRotThreads = 128;
+constexpr int kRotWarps = kRotThreads / 32;
+// Up to this many tokens the four warps of a CTA share a token's heads (64
+// tokens of 32 + 8 heads of 128: 3.1 us, 5.1 with a warp for each token); past
+// it the angles, which each of them computes, cost more than the wait for the
+// heads (2048 tokens: 12.0 us a warp each, 12.7 shared).
+constexpr int kRotSplitTokens = 1024;
 
 // frac(f / 2 pi) * 2^64 of a finite f with |f| < 2^31: the 53-bit mantissa times
 // 2^66 / (2 pi), shifted by the exponent; below 2^-64 of a turn exact.
@@ -64,145 +72,226 @@ __device__ __forceinline__ float2 pair_cos_sin(const RotaryArgs& p, int64_t t, i
   return cs;
 }
 
-// 16 elements of a head (two 8-element chunks) in fp32.
+// 16 elements of a head (two 8-element chunks) in fp32, as neighbouring pairs.
 struct Piece {
-  float a[8], b[8];
+  float2 a[4], b[4];
 };
 
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
-  const float2 p0 = bf16x2_to_float2(w.x), p1 = bf16x2_to_float2(w.y);
-  const float2 p2 = bf16x2_to_float2(w.z), p3 = bf16x2_to_float2(w.w);
-  x[0] = p0.x, x[1] = p0.y, x[2] = p1.x, x[3] = p1.y;
-  x[4] = p2.x, x[5] = p2.y, x[6] = p3.x, x[7] = p3.y;
+__device__ __forceinline__ void widen(const uint4& w, float2 (&x)[4]) {
+  x[0] = bf16x2_to_float2(w.x), x[1] = bf16x2_to_float2(w.y);
+  x[2] = bf16x2_to_float2(w.z), x[3] = bf16x2_to_float2(w.w);
 }
 
-__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow(const float2 (&x)[4]) {
+  return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                    pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
 }
+
+// Cosines and sines of a lane's eight pairs.
+struct Angles {
+  float2 c[4], s[4];
+};
 
 // Turn the lane's eight pairs: chunk a with chunk b, or neighbours inside each.
-__device__ __forceinline__ void turn(Piece& x, const float2 (&cs)[8], bool interleaved) {
-  if (!interleaved) {
+template <bool INTER>
+__device__ __forceinline__ void turn(Piece& x, const Angles& t) {
+  if constexpr (!INTER) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float u = x.a[e], w = x.b[e];
-      x.a[e] = u * cs[e].x - w * cs[e].y;
-      x.b[e] = w * cs[e].x + u * cs[e].y;
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = x.a[e], b = x.b[e];
+      x.a[e] = __ffma2_rn(b, make_float2(-t.s[e].x, -t.s[e].y), __fmul2_rn(a, t.c[e]));
+      x.b[e] = __ffma2_rn(a, t.s[e], __fmul2_rn(b, t.c[e]));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float u = x.a[2 * e], w = x.a[2 * e + 1];
-      x.a[2 * e] = u * cs[e].x - w * cs[e].y;
-      x.a[2 * e + 1] = w * cs[e].x + u * cs[e].y;
-      const float y = x.b[2 * e], z = x.b[2 * e + 1];
-      x.b[2 * e] = y * cs[4 + e].x - z * cs[4 + e].y;
-      x.b[2 * e + 1] = z * cs[4 + e].x + y * cs[4 + e].y;
+      const float2 a = x.a[e], b = x.b[e];
+      const float ca = e & 1 ? t.c[e >> 1].y : t.c[e >> 1].x;
+      const float sa = e & 1 ? t.s[e >> 1].y : t.s[e >> 1].x;
+      const float cb = e & 1 ? t.c[2 + (e >> 1)].y : t.c[2 + (e >> 1)].x;
+      const float sb = e & 1 ? t.s[2 + (e >> 1)].y : t.s[2 + (e >> 1)].x;
+      x.a[e] = make_float2(a.x * ca - a.y * sa, a.y * ca + a.x * sa);
+      x.b[e] = make_float2(b.x * cb - b.y * sb, b.y * cb + b.x * sb);
     }
   }
+}
+
+// x / d rounded to nearest, given r = 1 / d rounded to nearest: the residual of
+// x * r is exact in one FMA, and adding it times r gives the correctly rounded
+// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), as long as no product leaves the normal range.
+__device__ __forceinline__ float2 quotient(float2 x, float2 minus_d, float2 r) {
+  const float2 y = __fmul2_rn(x, r);
+  return __ffma2_rn(__ffma2_rn(y, minus_d, x), r, y);
 }
 
 // Store a row's piece to the 8-bit cache: scale = row max / 448 (1 for an
 // all-zero row) over the row's LPR lanes, codes e4m3(x / scale), as
 // pa_reshape_and_cache_fp8 defines them, from the fp32 values (a rotated key
-// is rounded once, to its code).
+// is rounded once, to its code).  codes_at, scale_at: the row's.
 template <int D>
-__device__ __forceinline__ void store_fp8(unsigned char* cache, int64_t slot, int n_kv, int h,
-                                          int ca, int cb, int l, const Piece& x, bool on) {
+__device__ __forceinline__ void store_fp8(unsigned char* codes_at, float* scale_at, int ca, int cb,
+                                          int l, const Piece& x, bool on) {
   constexpr int LPR = D / 16;
-  float amax = 0.f;
+  float m4[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x.a[e]), fabsf(x.b[e])));
+  for (int e = 0; e < 4; ++e)
+    m4[e] = fmaxf(fmaxf(fabsf(x.a[e].x), fabsf(x.a[e].y)), fmaxf(fabsf(x.b[e].x), fabsf(x.b[e].y)));
+  float amax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 #pragma unroll
   for (int m = LPR / 2; m >= 1; m >>= 1)
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
   if (!on) return;
   const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-  unsigned char* page = cache + (slot / kFp8PageTokens) * fp8_page_bytes(n_kv, D);
-  const int64_t row = (slot % kFp8PageTokens) * n_kv + h;
-  auto codes = [&](const float (&v)[8]) {
-    uint32_t w[4];
+  const float inv = __frcp_rn(sc);
+  const float2 d2 = make_float2(-sc, -sc), r2 = make_float2(inv, inv);
+  float2 y[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = e4m3x2_from_floats(__fdiv_rn(v[2 * e], sc), __fdiv_rn(v[2 * e + 1], sc));
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-  };
-  *reinterpret_cast<uint2*>(page + row * D + ca * 8) = codes(x.a);
-  *reinterpret_cast<uint2*>(page + row * D + cb * 8) = codes(x.b);
-  if (l == 0) *reinterpret_cast<float*>(page + fp8_scales_offset(n_kv, D) + row * 4) = sc;
+  for (int e = 0; e < 4; ++e) {
+    y[e] = quotient(x.a[e], d2, r2);
+    y[4 + e] = quotient(x.b[e], d2, r2);
+  }
+  // a divider near the ends of fp32's range takes the plain division; elements
+  // so small that their residual underflows have the code 0 either way
+  if (!(amax >= 1e-18f && amax <= 1e18f)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = make_float2(__fdiv_rn(x.a[e].x, sc), __fdiv_rn(x.a[e].y, sc));
+      y[4 + e] = make_float2(__fdiv_rn(x.b[e].x, sc), __fdiv_rn(x.b[e].y, sc));
+    }
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = e4m3x2_from_floats(y[e].x, y[e].y);
+  *reinterpret_cast<uint2*>(codes_at + ca * 8) =
+      make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  *reinterpret_cast<uint2*>(codes_at + cb * 8) =
+      make_uint2(w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+  if (l == 0) *scale_at = sc;
 }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(kRotThreads) rotary_cache_kernel(const RotaryArgs p) {
-  constexpr int LPR = D / 16;  // lanes of a head: 16 elements each
-  __shared__ float2 cs_s[D / 2];
-  const int64_t t = blockIdx.x;
-  const int half = p.rotary_dim / 2;
-  bool bad = false;
-  for (int i = threadIdx.x; i < half; i += kRotThreads) cs_s[i] = pair_cos_sin(p, t, i, bad);
-  __syncthreads();
-  int64_t slot = p.slot_mapping[t];
-  if (slot >= p.num_slots) bad = true, slot = -1;
-  const int l = threadIdx.x % LPR;
+// Warps of a token: `split` of them share its heads (1, or 4 with few tokens).
+// DEPTH passes of a warp have their loads in flight together.  The bf16 cache
+// takes three with 80 registers a thread (4099 tokens of 16 + 4 heads of 64,
+// half rotated: 5.9 us, 4.3 TB/s; two: 6.2), the 8-bit cache, whose codes cost
+// more instructions, two with 64 registers (8191 tokens of 32 +
+// 8 heads of 128: 35.0 us, 5.3 TB/s; three: 36.6).
+template <int D, bool F8, bool INTER>
+__global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
+    rotary_cache_kernel(const RotaryArgs p, int split) {
+  constexpr int DEPTH = F8 ? 2 : 3;
+  constexpr int LPR = D / 16;      // lanes of a head: 16 elements each
+  constexpr int HEADS = 32 / LPR;  // heads of a pass of the warp
+  __shared__ float2 cs_s[kRotWarps][D / 2];
+  // (read from lane 0, so that what follows from it is known to be the warp's)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * kRotWarps + warp;
+  const int64_t t = split == 1 ? unit : unit / kRotWarps;
+  if (t >= p.num_tokens) return;
+  const int step = HEADS * split;
+  const int l = lane % LPR;
+  const int h_lane = (split == 1 ? 0 : warp * HEADS) + lane / LPR;  // head of the first pass
   const bool rot = l < p.rotary_dim / 16;
   // this lane's two chunks of 8 elements
   int ca = 2 * l, cb = 2 * l + 1;
-  float2 cs[8];
-  if (rot) {
-    if (!p.interleaved) ca = l, cb = l + p.rotary_dim / 16;
+  if (rot && !INTER) ca = l, cb = l + p.rotary_dim / 16;
+  // the passes over the token's heads: queries, then keys, then values
+  const int nq = (p.n_q + step - 1) / step, nk = (p.n_kv + step - 1) / step;
+  const int passes = nq + 2 * nk;
+  const uint16_t* q = p.q + t * p.q_stride;
+  const uint16_t* k = p.k + t * p.k_stride;
+  const uint16_t* v = p.v + t * p.v_stride;
+  uint4 wa[DEPTH], wb[DEPTH];
+  auto load = [&](int i, int pass) {
+    const bool is_q = pass < nq, is_v = pass >= nq + nk;
+    const int h = h_lane + (is_q ? pass : is_v ? pass - nq - nk : pass - nq) * step;
+    wa[i] = wb[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (pass < passes && h < (is_q ? p.n_q : p.n_kv)) {
+      const uint16_t* src = (is_q ? q : is_v ? v : k) + h * D;
+      wa[i] = *reinterpret_cast<const uint4*>(src + ca * 8);
+      wb[i] = *reinterpret_cast<const uint4*>(src + cb * 8);
+    }
+  };
+  // the first passes' loads; their wait covers the angles' arithmetic
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = cs_s[8 * l + e];
+  for (int i = 0; i < DEPTH; ++i) load(i, i);
+  int64_t slot = p.slot_mapping[t];
+  bool bad = false;
+  for (int i = lane; i < p.rotary_dim / 2; i += 32) cs_s[warp][i] = pair_cos_sin(p, t, i, bad);
+  __syncwarp();
+  if (slot >= p.num_slots) bad = true, slot = -1;
+  Angles cs;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 u = rot ? cs_s[warp][8 * l + 2 * e] : make_float2(1.f, 0.f);
+    const float2 w = rot ? cs_s[warp][8 * l + 2 * e + 1] : make_float2(1.f, 0.f);
+    cs.c[e] = make_float2(u.x, w.x), cs.s[e] = make_float2(u.y, w.y);
   }
-  const int rows = p.n_q + 2 * p.n_kv;
-  for (int r0 = 0; r0 < rows; r0 += kRotThreads / LPR) {
-    const int r = r0 + threadIdx.x / LPR;
-    const bool on = r < rows;
-    const uint16_t* src = p.q + t * p.q_stride + (int64_t)r * D;
-    int h = r;
-    if (r >= p.n_q) h = r - p.n_q, src = p.k + t * p.k_stride + (int64_t)h * D;
-    const bool is_v = r >= p.n_q + p.n_kv;
-    if (is_v) h -= p.n_kv, src = p.v + t * p.v_stride + (int64_t)h * D;
-    const bool needed = on && (r < p.n_q || slot >= 0);
-    uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
-    if (needed) {
-      wa = *reinterpret_cast<const uint4*>(src + ca * 8);
-      wb = *reinterpret_cast<const uint4*>(src + cb * 8);
+  uint16_t* q_out = p.q_out + t * p.n_q * D;
+  // the token's row in the caches: of values, or (8-bit) of codes and scales
+  int64_t row = slot * p.n_kv * (int64_t)(2 * D), scales = 0;
+  if (F8) {
+    row = (slot / kFp8PageTokens) * fp8_page_bytes(p.n_kv, D);
+    const int r = (int)(slot % kFp8PageTokens) * p.n_kv;
+    scales = row + fp8_scales_offset(p.n_kv, D) + r * 4;
+    row += r * D;
+  }
+  for (int p0 = 0; p0 < passes; p0 += DEPTH) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      const int pass = p0 + i;
+      if (pass >= passes) break;
+      const bool is_q = pass < nq, is_v = pass >= nq + nk;
+      const int h = h_lane + (is_q ? pass : is_v ? pass - nq - nk : pass - nq) * step;
+      unsigned char* cache = static_cast<unsigned char*>(is_v ? p.v_cache : p.k_cache);
+      if (F8 && !is_q) {
+        // from fp32 (a turned key is rounded once, to its code); every lane of
+        // the warp takes part in the row maximum's shuffles
+        Piece x;
+        widen(wa[i], x.a);
+        widen(wb[i], x.b);
+        if (rot && !is_v) turn<INTER>(x, cs);
+        store_fp8<D>(cache + row + h * D, reinterpret_cast<float*>(cache + scales) + h, ca, cb, l,
+                     x, slot >= 0 && h < p.n_kv);
+      } else if (is_q ? h < p.n_q : slot >= 0 && h < p.n_kv) {
+        if (rot && !is_v) {
+          Piece x;
+          widen(wa[i], x.a);
+          widen(wb[i], x.b);
+          turn<INTER>(x, cs);
+          wa[i] = narrow(x.a);
+          wb[i] = narrow(x.b);
+        }
+        uint16_t* dst = is_q ? q_out + h * D : reinterpret_cast<uint16_t*>(cache + row) + h * D;
+        *reinterpret_cast<uint4*>(dst + ca * 8) = wa[i];
+        *reinterpret_cast<uint4*>(dst + cb * 8) = wb[i];
+      }
+      load(i, pass + DEPTH);
     }
-    Piece x;
-    widen(wa, x.a);
-    widen(wb, x.b);
-    if (rot && !is_v) turn(x, cs, p.interleaved);
-    if (F8) {
-      // every lane takes part in the row maximum's shuffles
-      store_fp8<D>(is_v ? static_cast<unsigned char*>(p.v_cache)
-                        : static_cast<unsigned char*>(p.k_cache),
-                   slot, p.n_kv, h, ca, cb, l, x, needed && r >= p.n_q);
-    }
-    if (!needed || (F8 && r >= p.n_q)) continue;
-    uint16_t* dst = r < p.n_q ? p.q_out + (t * p.n_q + r) * D
-                              : static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) +
-                                    (slot * p.n_kv + h) * D;
-    *reinterpret_cast<uint4*>(dst + ca * 8) = narrow(x.a);
-    *reinterpret_cast<uint4*>(dst + cb * 8) = narrow(x.b);
   }
   if (bad) flag_error(p.err, DEVERR_BOUNDS);
 }
 
 }  // namespace
 
-cudaError_t launch_rotary_cache(const RotaryArgs& p, cudaStream_t stream) {
-  if (p.head_dim == 128 && !p.fp8)
-    rotary_cache_kernel<128, false><<<p.num_tokens, kRotThreads, 0, stream>>>(p);
-  else if (p.head_dim == 64 && !p.fp8)
-    rotary_cache_kernel<64, false><<<p.num_tokens, kRotThreads, 0, stream>>>(p);
-  else if (p.head_dim == 128)
-    rotary_cache_kernel<128, true><<<p.num_tokens, kRotThreads, 0, stream>>>(p);
-  else if (p.head_dim == 64)
-    rotary_cache_kernel<64, true><<<p.num_tokens, kRotThreads, 0, stream>>>(p);
+template <int D, bool F8>
+static cudaError_t launch_rotary_t(const RotaryArgs& p, cudaStream_t stream) {
+  const int split = p.num_tokens <= kRotSplitTokens ? kRotWarps : 1;
+  const int64_t warps = (int64_t)p.num_tokens * split;
+  const unsigned grid = (unsigned)((warps + kRotWarps - 1) / kRotWarps);
+  if (p.interleaved)
+    rotary_cache_kernel<D, F8, true><<<grid, kRotThreads, 0, stream>>>(p, split);
   else
-    return cudaErrorInvalidValue;
+    rotary_cache_kernel<D, F8, false><<<grid, kRotThreads, 0, stream>>>(p, split);
   return cudaGetLastError();
+}
+
+cudaError_t launch_rotary_cache(const RotaryArgs& p, cudaStream_t stream) {
+  if (p.head_dim == 128)
+    return p.fp8 ? launch_rotary_t<128, true>(p, stream) : launch_rotary_t<128, false>(p, stream);
+  if (p.head_dim == 64)
+    return p.fp8 ? launch_rotary_t<64, true>(p, stream) : launch_rotary_t<64, false>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

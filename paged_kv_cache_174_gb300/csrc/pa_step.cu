@@ -13,10 +13,12 @@
 // new block is free[count - 1 - (B_s + k)] (last in, first out, as the host
 // allocator hands blocks out), and its i-th new token is row T_s + i.
 //
-// Kilobytes move, so a launch's latency is all there is: one CTA scans the
-// lengths into shared memory, then its threads walk the flat lists of new
-// blocks and of token rows, each finding its request by a binary search of the
-// prefix sums.
+// Kilobytes move, so latency is all there is.  Every CTA scans all the lengths
+// into its shared memory (cheaper than handing the sums over), then the CTAs'
+// threads walk the flat lists of new blocks and of token rows, each finding its
+// request by a binary search of the prefix sums.  The grid is one cluster, so
+// that its barrier can keep every write behind every CTA's reads: seq_lens may
+// be context_lens, and free_count_out free_count.
 #include <cstdint>
 
 #include "pa_common.cuh"
@@ -25,8 +27,10 @@
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanWarps = 32;  // at most
+// Up to this many token rows one CTA of 512 threads does the step; past it a
+// cluster of eight of 1024.
+constexpr int kPlanOneCta = 1024;
 
 // The last index s in [0, n) with pre[s] <= x (pre[0] = 0 <= x, non-decreasing).
 __device__ __forceinline__ int owner_of(const int* pre, int n, int x) {
@@ -41,7 +45,22 @@ __device__ __forceinline__ int owner_of(const int* pre, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) build_step_kernel(const StepPlanArgs p) {
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepPlanArgs p) {
   extern __shared__ int smem_i[];
   int* ctx_s = smem_i;                     // [num_seqs]
   int* tok_s = ctx_s + p.num_seqs;         // [num_seqs + 1] exclusive prefix of new tokens
@@ -49,96 +68,97 @@ __global__ void __launch_bounds__(kPlanThreads) build_step_kernel(const StepPlan
   __shared__ long long warp_t[kPlanWarps], warp_b[kPlanWarps];
   __shared__ int served_t, served_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int threads = blockDim.x, warps = threads >> 5;
+  const int me = blockIdx.x * threads + tid, all = gridDim.x * threads;
   const int bs = p.block_size;
 
   const int raw_count = *p.free_count;
   const bool count_ok = raw_count >= 0 && raw_count <= p.num_blocks;
   const int count = count_ok ? raw_count : 0;
   bool bad = !count_ok;
-  if (tid == 0) served_t = 0, served_b = 0;
+  if (tid == 0) served_t = 0, served_b = 0, tok_s[0] = 0, blk_s[0] = 0;
 
+  bool cut = false;                // a request of this thread was not served
   long long run_t = 0, run_b = 0;  // totals of the chunks before this one
-  for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+  for (int s0 = 0; s0 < p.num_seqs; s0 += threads) {
     const int s = s0 + tid;
     long long nt = 0, nb = 0;
-    bool ok = false;
     if (s < p.num_seqs) {
       const int c = p.context_lens[s], n = p.new_lens[s];
       ctx_s[s] = c;
-      ok = c >= 0 && n >= 0 && (long long)c + n <= (long long)p.max_blocks * bs;
-      if (ok) {
+      if (c >= 0 && n >= 0 && (long long)c + n <= (long long)p.max_blocks * bs) {
+        // (at most 2^31 - 1 positions: no overflow in 32 bits, unsigned)
         nt = n;
-        nb = ((long long)c + n + bs - 1) / bs - ((long long)c + bs - 1) / bs;
+        nb = ((unsigned)c + n + bs - 1) / (unsigned)bs - ((unsigned)c + bs - 1) / (unsigned)bs;
       } else {
         bad = true;  // a length out of range: no rows, no blocks
       }
     }
-    long long it = nt, ib = nb;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, it, o);
-      const long long b = __shfl_up_sync(0xffffffffu, ib, o);
-      if (lane >= o) it += a, ib += b;
-    }
-    __syncthreads();  // the last chunk's warp totals have been read
+    long long it = warp_scan(nt, lane), ib = warp_scan(nb, lane);
+    if (s0) __syncthreads();  // the last chunk's warp totals have been read
     if (lane == 31) warp_t[warp] = it, warp_b[warp] = ib;
     __syncthreads();
-    long long bt = run_t, bb = run_b;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      if (w < warp) bt += warp_t[w], bb += warp_b[w];
-      run_t += warp_t[w], run_b += warp_b[w];
-    }
-    it += bt, ib += bb;
-    if (s < p.num_seqs) {
-      const bool served = it <= p.num_tokens && ib <= count;
-      // inclusive sums at s + 1; past the served prefix a mark, replaced below
-      tok_s[s + 1] = served ? (int)it : -1;
-      blk_s[s + 1] = served ? (int)ib : -1;
-      if (served) {
+    const long long wt = warp_scan(lane < warps ? warp_t[lane] : 0, lane);
+    const long long wb = warp_scan(lane < warps ? warp_b[lane] : 0, lane);
+    const int before = warp > 0 ? warp - 1 : 0;
+    const long long pt = __shfl_sync(0xffffffffu, wt, before);
+    const long long pb = __shfl_sync(0xffffffffu, wb, before);
+    it += run_t + (warp > 0 ? pt : 0), ib += run_b + (warp > 0 ? pb : 0);
+    run_t += __shfl_sync(0xffffffffu, wt, 31), run_b += __shfl_sync(0xffffffffu, wb, 31);
+    const bool mine = s < p.num_seqs;
+    const bool served = mine && it <= p.num_tokens && ib <= count;
+    const unsigned ball = __ballot_sync(0xffffffffu, served);
+    if (served) {
+      tok_s[s + 1] = (int)it;
+      blk_s[s + 1] = (int)ib;
+      if ((ball >> lane) == 1u) {  // the warp's last served request
         atomicMax(&served_t, (int)it);
         atomicMax(&served_b, (int)ib);
-      } else {
-        bad = true;
       }
+    } else if (mine) {
+      tok_s[s + 1] = -1;  // past the served prefix: the totals, below
+      cut = true;
     }
   }
-  if (tid == 0) tok_s[0] = 0, blk_s[0] = 0;
-  __syncthreads();
+  const int any_cut = __syncthreads_or(cut);
   const int total_t = served_t, total_b = served_b;
-  for (int s = tid; s < p.num_seqs; s += kPlanThreads) {
-    if (tok_s[s + 1] < 0) tok_s[s + 1] = total_t, blk_s[s + 1] = total_b;
+  if (any_cut) {
+    bad |= cut;
+    for (int s = tid; s < p.num_seqs; s += threads)
+      if (tok_s[s + 1] < 0) tok_s[s + 1] = total_t, blk_s[s + 1] = total_b;
+    __syncthreads();
   }
-  __syncthreads();
+  if (gridDim.x > 1) cluster_barrier();
 
-  for (int s = tid; s <= p.num_seqs; s += kPlanThreads) {
+  for (int s = me; s <= p.num_seqs; s += all) {
     p.query_start_loc[s] = tok_s[s];
     if (s < p.num_seqs) p.seq_lens[s] = ctx_s[s] + (tok_s[s + 1] - tok_s[s]);
   }
-  if (tid == 0) *p.free_count_out = raw_count - total_b;
+  if (me == 0) *p.free_count_out = raw_count - total_b;
 
   // new blocks, in the order of the requests
-  for (int k = tid; k < total_b; k += kPlanThreads) {
+  for (int k = me; k < total_b; k += all) {
     const int s = owner_of(blk_s, p.num_seqs, k);
-    const int col = (int)(((long long)ctx_s[s] + bs - 1) / bs) + (k - blk_s[s]);
+    const int col = (int)(((unsigned)ctx_s[s] + bs - 1) / (unsigned)bs) + (k - blk_s[s]);
     int id = p.free_blocks[count - 1 - k];
     if (id < 0 || id >= p.num_blocks) bad = true, id = -1;
     p.block_tables[(int64_t)s * p.max_blocks + col] = id;
   }
   // token rows; those past the last new token are padding
-  for (int t = tid; t < p.num_tokens; t += kPlanThreads) {
+  for (int t = me; t < p.num_tokens; t += all) {
     int slot = -1, pos = 0;
     if (t < total_t) {
       const int s = owner_of(tok_s, p.num_seqs, t);
       const int c = ctx_s[s];
       const int at = c + (t - tok_s[s]);
-      const int col = at / bs;
-      const int first = (int)(((long long)c + bs - 1) / bs);
+      const int col = (unsigned)at / (unsigned)bs;
+      const int first = (int)(((unsigned)c + bs - 1) / (unsigned)bs);
       const int id = col >= first ? p.free_blocks[count - 1 - (blk_s[s] + col - first)]
                                   : p.block_tables[(int64_t)s * p.max_blocks + col];
       if (id < 0 || id >= p.num_blocks)
         bad = true;
       else
-        slot = id * bs + at % bs;
+        slot = id * bs + (at - col * bs);
       pos = at + (p.position_offsets ? p.position_offsets[s] : 0);
     }
     p.slot_mapping[t] = slot;
@@ -158,8 +178,20 @@ cudaError_t launch_build_step(const StepPlanArgs& p, cudaStream_t stream) {
                                          (int)((3 * kMaxPlanSeqs + 2) * sizeof(int)));
     if (e != cudaSuccess) return e;
   }
-  build_step_kernel<<<1, kPlanThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  const bool one = p.num_tokens <= kPlanOneCta;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(one ? 1 : 8);
+  cfg.blockDim = dim3(one ? 512 : kPlanWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = one ? 1 : 8;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, build_step_kernel, p);
 }
 
 }  // namespace pa
