@@ -74,6 +74,7 @@ constexpr int kStagesK = 3;        // K tile stages (bf16 cache)
 constexpr int kStagesV = 2;        // V tile stages (bf16 cache)
 constexpr int kStagesMax = 3;      // the most stages of one kind in any instance
 constexpr int kSBufs = 3;          // S / P buffers in TMEM
+constexpr int kSBufsMax = 4;       // the most in any instance (a pair's, of half the size)
 constexpr int kSoftmaxWarps = 8;   // two per TMEM lane quarter
 constexpr int kKWarps = 3;         // warp 0 (which also loads Q) and warps 10-11
 constexpr int kVWarps = 3;         // warps 12-14
@@ -83,6 +84,7 @@ constexpr int kThreads = 512;
 constexpr float kNegInf = -INFINITY;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxSplit = 4;
+constexpr double kPairCost = 1.7, kPairCostFp8 = 1.1;  // see pair_query_tiles
 constexpr int kMaxListed = 1024;   // prefill requests the shared-memory unit list holds
 
 // Instances of the kernel: the plain one reads the bf16 cache; the fused
@@ -239,11 +241,12 @@ struct PrefillShared {
   uint64_t q_land;  // 8-bit cache: the bf16 query tile has landed (then rewritten)
   uint64_t k_full[kStagesMax], k_empty[kStagesMax];
   uint64_t v_full[kStagesMax], v_empty[kStagesMax];
-  uint64_t s_full[kSBufs], p_full[kSBufs], pv_done[kSBufs];
-  uint64_t o_full, o_empty;
-  uint64_t s_done, pv_done_all;  // each issuer's last products, before TMEM is freed
+  uint64_t s_full[kSBufsMax], p_full[kSBufsMax], pv_done[kSBufsMax];
+  uint64_t o_full[2], o_empty[2];  // of each query tile of the unit
+  uint64_t s_done[2], pv_done_all[2];  // each issuer's last products, before TMEM is freed
   uint64_t patch[kThreads / 32];  // per producer warp: a page to patch has landed
   uint32_t tmem_slot;
+  uint32_t v_landed[2];  // V tiles each P V issuer of a pair has waited for
   int abort_flag;
   long long total_units;
   float xmax[2][2][kRows];  // partial row maxima: [tile parity][key half][row]
@@ -429,7 +432,17 @@ __device__ __forceinline__ uint32_t window_bits(int base, int p, int window, int
   return ((1u << (hi + 1)) - 1u) & ((0xffffu << lo) | ((1u << ns) - 1u));
 }
 
-template <int D, int G, int KIND, bool WIN>
+}  // namespace
+}  // namespace pa
+
+#include "pa_prefill_pair.cuh"
+
+namespace pa {
+namespace {
+
+// QT: query tiles of a unit, 1 or (sliding window) 2; with two, the products
+// and the softmax are the pair's (pa_prefill_pair.cuh).
+template <int D, int G, int KIND, bool WIN, int QT>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -441,10 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Stages: the 8-bit instance's V copies wait for a product two tiles
   // earlier with two V stages, and its producers take longer per page (code
   // conversion), so it trades a K stage for a V stage (same shared memory).
-  constexpr int SK = F8 ? 2 : kStagesK;
-  constexpr int SV = F8 ? 3 : kStagesV;
-  static_assert(SK + SV == kStagesK + kStagesV && SK <= kStagesMax && SV <= kStagesMax,
-                "shared memory holds kStagesK + kStagesV tiles");
+  // With two query tiles the second takes a stage's place.
+  constexpr int SK = F8 || QT == 2 ? 2 : kStagesK;
+  constexpr int SV = F8 && QT == 1 ? 3 : kStagesV;
+  static_assert(QT + SK + SV == 1 + kStagesK + kStagesV && SK <= kStagesMax && SV <= kStagesMax,
+                "shared memory holds a query tile and kStagesK + kStagesV tiles");
+  // producer warps of K and of V, and the pages of a tile that each brings
+  constexpr int KW = QT == 1 ? kKWarps : 2, VW = QT == 1 ? kVWarps : 2;
+  constexpr int PG = QT == 1 ? 3 : 4;
   constexpr int TM = kRows / G;            // query tokens per tile
   constexpr int NH = D / 64;               // 64-element halves of head_dim
   constexpr uint32_t HALF = kRows * 128;   // bytes of one [128 rows][64] block
@@ -459,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* q_s = base;
-  unsigned char* k_s = q_s + Q_BYTES;
+  unsigned char* k_s = q_s + QT * Q_BYTES;
   unsigned char* v_s = k_s + SK * KV_BYTES;
   PrefillShared& B = *reinterpret_cast<PrefillShared*>(v_s + SV * KV_BYTES);
 
@@ -482,26 +499,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(smem_addr(&B.q_full), 1);
     mbar_init(smem_addr(&B.q_land), 1);
-    mbar_init(smem_addr(&B.q_empty), 1);
+    mbar_init(smem_addr(&B.q_empty), QT);
     for (int i = 0; i < SK; ++i) {
-      mbar_init(smem_addr(&B.k_full[i]), kKWarps);
-      mbar_init(smem_addr(&B.k_empty[i]), 1);
+      mbar_init(smem_addr(&B.k_full[i]), KW);
+      mbar_init(smem_addr(&B.k_empty[i]), QT);
     }
     for (int i = 0; i < SV; ++i) {
-      mbar_init(smem_addr(&B.v_full[i]), kVWarps);
-      mbar_init(smem_addr(&B.v_empty[i]), 1);
+      mbar_init(smem_addr(&B.v_full[i]), VW);
+      mbar_init(smem_addr(&B.v_empty[i]), QT);
     }
-    for (int i = 0; i < kSBufs; ++i) {
+    for (int i = 0; i < (QT == 1 ? kSBufs : kSBufsMax); ++i) {
       mbar_init(smem_addr(&B.s_full[i]), 1);
-      mbar_init(smem_addr(&B.p_full[i]), kSoftmaxWarps);
+      mbar_init(smem_addr(&B.p_full[i]), kSoftmaxWarps / QT);
       mbar_init(smem_addr(&B.pv_done[i]), 1);
     }
-    mbar_init(smem_addr(&B.o_full), 1);
-    mbar_init(smem_addr(&B.o_empty), kSoftmaxWarps);
-    mbar_init(smem_addr(&B.s_done), 1);
-    mbar_init(smem_addr(&B.pv_done_all), 1);
+    for (int i = 0; i < QT; ++i) {
+      mbar_init(smem_addr(&B.o_full[i]), 1);
+      mbar_init(smem_addr(&B.o_empty[i]), kSoftmaxWarps / QT);
+    }
+    for (int i = 0; i < QT; ++i) {
+      mbar_init(smem_addr(&B.s_done[i]), 1);
+      mbar_init(smem_addr(&B.pv_done_all[i]), 1);
+    }
     for (int w = 0; w < kThreads / 32; ++w) mbar_init(smem_addr(&B.patch[w]), 1);
     B.abort_flag = 0;
+    B.v_landed[0] = B.v_landed[1] = 0;
     fence_mbar_init();
   }
   {
@@ -510,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int listed = 0, tiles_so_far = 0;
     for (int s0 = 0; s0 < p.num_seqs; s0 += kThreads) {
       const int s = s0 + (int)threadIdx.x;
-      const int t = s < p.num_seqs ? prefill_tiles<TM>(p, s, blockIdx.x == 0) : 0;
+      const int t = s < p.num_seqs ? prefill_tiles<QT * TM>(p, s, blockIdx.x == 0) : 0;
       const unsigned has = __ballot_sync(0xffffffffu, t > 0);
       int incl = t;  // inclusive scan of tiles over the warp
 #pragma unroll
@@ -560,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long total_units = B.total_units;
   volatile int* abort_flag = &B.abort_flag;
 
-  const bool k_warp = warp == 0 || (warp >= kWarpK1 && warp < kWarpK1 + kKWarps - 1);
-  const bool v_warp = warp >= kWarpV0 && warp < kWarpV0 + kVWarps;
+  const bool k_warp = warp == 0 || (warp >= kWarpK1 && warp < kWarpK1 + KW - 1);
+  const bool v_warp = warp >= kWarpV0 && warp < kWarpV0 + VW;
   if (k_warp || v_warp) {
     // ============================================================ producers
     // (lane 0 issues and waits; in the fused step the whole warp runs along
@@ -570,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K warp k and V warp k load pages 3k .. 3k+2 of each tile (the last
       // two): 96 rows of 128 bytes per warp and tile either way
       const int idx = k_warp ? (warp == 0 ? 0 : warp - kWarpK1 + 1) : warp - kWarpV0;
-      const int pg_lo = 3 * idx;
-      const int pg_hi = min(pg_lo + 3, kPagesPerTile);
+      // (with two query tiles two warps each, four pages)
+      const int pg_lo = PG * idx;
+      const int pg_hi = min(pg_lo + PG, kPagesPerTile);
       const CUtensorMap* map = k_warp ? &kmap : &vmap;
       const CUtensorMap* nmap = k_warp ? &knmap : &vnmap;
       const uint16_t* newrows = k_warp ? p.k_new : p.v_new;
@@ -581,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t nst = k_warp ? SK : SV;
       const uint32_t patch_bar = smem_addr(&B.patch[warp]);
       uint32_t n_patch = 0;
-      UnitCursor<TM, WIN> cur;
+      UnitCursor<QT * TM, WIN> cur;
       cur.init(p, B.list_seq, B.list_base, B.listed);
       int n_out = 0, c = 0;
       Ring pos;
@@ -595,10 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the S products of the Q loaded below
           if (n_out > 0) mbar_wait(smem_addr(&B.q_empty), (n_out - 1) & 1, p.err, abort_flag);
           const uint32_t qbar = smem_addr(F8 ? &B.q_land : &B.q_full);
-          mbar_arrive_expect_tx(qbar, Q_BYTES);
+          const bool two = QT == 2 && U.ntok > TM;
+          mbar_arrive_expect_tx(qbar, two ? 2 * Q_BYTES : Q_BYTES);
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
+          for (int h = 0; h < NH; ++h) {
             tc::tma_load_3d(smem_addr(q_s + h * HALF), &qmap, h * 64, U.g * G, U.q0, qbar);
+            if (two)
+              tc::tma_load_3d(smem_addr(q_s + Q_BYTES + h * HALF), &qmap, h * 64, U.g * G,
+                              U.q0 + TM, qbar);
+          }
         }
         if constexpr (F8) {
           if (warp == 0) {
@@ -607,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // in place as f16(q * scale * log2 e) for the f16 products
             if (lane == 0) mbar_wait(smem_addr(&B.q_land), n_out & 1, p.err, abort_flag);
             __syncwarp();
-            for (int e = lane; e < (int)(Q_BYTES / 16); e += 32) {
+            const int chunks = (QT == 2 && U.ntok > TM ? 2 : 1) * (int)(Q_BYTES / 16);
+            for (int e = lane; e < chunks; e += 32) {
               uint4* qp = reinterpret_cast<uint4*>(q_s + e * 16);
               uint4 v = *qp;
               v.x = f16x2_from_bf16x2_mul(v.x, p.q_mul);
@@ -658,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // plain loads issued before the stage is free (their latency
             // overlaps the wait); lane j-th chunk: 16 codes of one row
             constexpr int CPR = D / 16;                  // chunks per row
-            constexpr int NJ = 3 * kBlock * CPR / 32;    // chunks per lane
+            constexpr int NJ = PG * kBlock * CPR / 32;   // chunks per lane
             const uint8_t* pages = k_warp ? p.k_codes : p.v_codes;
             const int64_t page_bytes = fp8_page_bytes(p.n_kv, D);
             const int64_t scales_at = fp8_scales_offset(p.n_kv, D);
@@ -808,12 +837,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(smem_addr(&B.q_full), (n_out - 1) & 1, p.err, abort_flag);
       }
     }
-  } else if (warp == 1 || warp == kWarpPV) {
+  } else if (warp == 1 || warp == kWarpPV || (QT == 2 && (warp == 11 || warp == 14))) {
     // ============================================================ MMA issuers
     // (waits spin without the suspend hint: these threads' latency is the
     // tensor pipe's)
-    if (lane == 0) {
-      UnitCursor<TM, WIN> cur;
+    if constexpr (QT == 2) {
+      if (lane == 0) {
+        UnitCursor<QT * TM, WIN> cur;
+        cur.init(p, B.list_seq, B.list_base, B.listed);
+        // S of the two query tiles from warps 1 and 11, P V from 14 and 15
+        if (warp == 1 || warp == 11)
+          pair_issue_s<D, TM, F8>(p, B, cur, total_units, tmem, smem_addr(q_s), smem_addr(k_s),
+                                  warp == 1 ? 0 : 1);
+        else
+          pair_issue_pv<D, TM, F8>(p, B, cur, total_units, tmem, smem_addr(v_s),
+                                   warp == 14 ? 0 : 1);
+      }
+    } else if (lane == 0) {
+      UnitCursor<QT * TM, WIN> cur;
       cur.init(p, B.list_seq, B.list_base, B.listed);
       int n_out = 0;
       uint32_t ntiles = 0;  // tiles of S (or P V) issued so far, all units
@@ -853,8 +894,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n_out;
         }
         if (ntiles > 0) {
-          tc::commit(smem_addr(&B.s_done));  // its only use: phase 0
-          mbar_wait_spin(smem_addr(&B.s_done), 0, p.err, abort_flag);
+          tc::commit(smem_addr(&B.s_done[0]));  // its only use: phase 0
+          mbar_wait_spin(smem_addr(&B.s_done[0]), 0, p.err, abort_flag);
         }
       } else {
         // O += P V with P in the S buffer at sb and V at kv; the first tile of
@@ -875,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the last unit's O read out: the release before was waited for
             // here, and the next needs this unit's O (o_full)
             if (first && n_out > 0)
-              mbar_wait_spin(smem_addr(&B.o_empty), (n_out - 1) & 1, p.err, abort_flag);
+              mbar_wait_spin(smem_addr(&B.o_empty[0]), (n_out - 1) & 1, p.err, abort_flag);
             tc::fence_after_sync();
             issue_pv_mma<D, F8>(tmem + O_COL, tmem + sb.stage * kKeysPerTile,
                                 tc::Desc{vd0.lo + kv.stage * (KV_BYTES >> 4), vd0.hi},
@@ -885,17 +926,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             kv.next(SV);
             sb.next(kSBufs);
           }
-          tc::commit(smem_addr(&B.o_full));
+          tc::commit(smem_addr(&B.o_full[0]));
           ++n_out;
         }
         if (ntiles > 0) {
-          tc::commit(smem_addr(&B.pv_done_all));  // its only use: phase 0
-          mbar_wait_spin(smem_addr(&B.pv_done_all), 0, p.err, abort_flag);
+          tc::commit(smem_addr(&B.pv_done_all[0]));  // its only use: phase 0
+          mbar_wait_spin(smem_addr(&B.pv_done_all[0]), 0, p.err, abort_flag);
         }
       }
     }
   } else {
     // ============================================================ softmax
+    if constexpr (QT == 2) {
+      UnitCursor<QT * TM, WIN> cur;
+      cur.init(p, B.list_seq, B.list_base, B.listed);
+      pair_softmax<D, G, F8>(p, B, cur, total_units, tmem, v_s, warp, lane);
+    } else {
     const int quarter = warp & 3;    // TMEM lanes 32*quarter .. +31
     const int kh = (warp - 2) >> 2;  // key half of each tile: 64*kh .. 64*kh + 63
     const int r = quarter * 32 + lane;
@@ -909,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool pos_scale = sl2 > 0.f;
     const float mul = pos_scale ? 1.f : sl2;
     const float emul = pos_scale ? sl2 : 1.f;
-    UnitCursor<TM, WIN> cur;
+    UnitCursor<QT * TM, WIN> cur;
     cur.init(p, B.list_seq, B.list_base, B.listed);
     int n_out = 0;
     Ring sbr, prev, prev2, vr;  // S buffer of this tile, the last one and the one
@@ -1106,7 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = ltot > 0.f ? 1.f / ltot : 0.f;
       // this unit's O: the last unit's was waited for here, and the next
       // unit's first P V waits for o_empty, which these warps arrive on
-      mbar_wait(smem_addr(&B.o_full), upar, p.err, abort_flag);
+      mbar_wait(smem_addr(&B.o_full[0]), upar, p.err, abort_flag);
       tc::fence_after_sync();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -1139,8 +1185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             make_float2(ltot > 0.f ? m_ref : kNegInf, ltot);
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&B.o_empty));
+      if (lane == 0) mbar_arrive(smem_addr(&B.o_empty[0]));
       ++n_out;
+    }
     }
   }
 
@@ -1268,7 +1315,7 @@ size_t split_bytes(int num_tokens, int num_q_heads, int head_dim, int nsplit) {
          ((rows * 2 * sizeof(float) + 255) & ~size_t(255));
 }
 
-template <int D, int G, int KIND, bool WIN>
+template <int D, int G, int KIND, bool WIN, int QT = 1>
 cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* ws, int sm_count,
                              cudaStream_t stream) {
   constexpr bool FUSE = KIND == kKindFused;
@@ -1369,12 +1416,12 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
     }
   }
   // upper bound of the number of units; the kernel reads the exact count
-  const long long tiles_bound = (long long)a.num_tokens / TM + a.num_seqs;
+  const long long tiles_bound = (long long)a.num_tokens / (QT * TM) + a.num_seqs;
   const long long units_bound = tiles_bound * a.num_kv_heads * plan.nsplit;
   const int grid = (int)(units_bound < sm_count ? units_bound : sm_count);
   if (grid <= 0) return cudaSuccess;
   const size_t smem = prefill_smem_bytes<D, G>();
-  auto kern = prefill_kernel<D, G, KIND, WIN>;
+  auto kern = prefill_kernel<D, G, KIND, WIN, QT>;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1400,6 +1447,24 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p);
+}
+
+// Whether a sliding-window call takes two query tiles per unit.  It halves the
+// units, so it pays when they fill the SMs for more rounds than the longer
+// units cost: kPairCost* is a pair's time over a single tile's.
+template <int D, int G, int KIND>
+bool pair_query_tiles(const AttnArgs& a, const PrefillPlan& plan, int sm_count) {
+  constexpr int TM = kRows / G;
+  constexpr double cost = KIND == kKindFp8 ? kPairCostFp8 : kPairCost;
+  if (plan.nsplit > 1) return false;
+  // (num_tokens counts decode rows too: leave room for some before taking the
+  // units for a second round)
+  if ((long long)a.num_tokens * a.num_kv_heads * 4 <= (long long)TM * sm_count * 5) return false;
+  const auto rounds = [&](int tm) {
+    const long long units = (long long)((a.num_tokens + tm - 1) / tm) * a.num_kv_heads;
+    return (double)((units + sm_count - 1) / sm_count);
+  };
+  return rounds(2 * TM) * cost < rounds(TM);
 }
 
 }  // namespace

@@ -133,6 +133,19 @@ def test_chunks(lens, q_lens, window, sinks, fp8):
 
 
 @BOTH
+@pytest.mark.parametrize("window,sinks", [(40, 4), (150, 0), (129, 140), (2000, 3)])
+@pytest.mark.parametrize("group,d", [(1, 64), (1, 128), (2, 128), (4, 64), (4, 128), (8, 64),
+                                     (8, 128)])
+def test_many_query_tiles(group, d, window, sinks, fp8):
+    """Calls with more query tiles than SMs (pairs of tiles), requests of odd
+    numbers of tiles, one row, a row more than a tile and a row less among them."""
+    tm = 128 // group
+    q_lens = [tm, 5 * tm, 1, 2, tm + 1, 2 * tm - 1, 2 * tm, 2 * tm + 1, 6 * tm, 3 * tm + 5]
+    lens = [n + x for n, x in zip(q_lens, (0, 700, 300, 0, 33, 128, 1000, 15, 64, 0))]
+    Batch(20 + group, lens, q_lens, 8 * group, 8, d, window, sinks, fp8=fp8).check()
+
+
+@BOTH
 @pytest.mark.parametrize("seed", range(24))
 def test_random(seed, fp8):
     rng = np.random.default_rng(500 + seed)
