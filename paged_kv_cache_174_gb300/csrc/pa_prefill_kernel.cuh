@@ -989,22 +989,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // causal mask and the max of this half (three-input max, 4 chains)
         const int lim = p_row - (kt * kKeysPerTile + kh * 64);  // keys c <= lim visible
-        uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // with a window: a bit for each key
+        // With a window: does every row of the query tile see every key of this
+        // half?  Then there is nothing to mask, and no V row to clear below.
+        bool plain = false;
+        uint32_t seen[2];  // else a bit for each key that the row sees
         if constexpr (WIN) {
+          const int e0 = kt * kPagesPerTile + kh * (kPagesPerTile / 2);
+          const int pos0 = U.template page<true>(e0) * kBlock;
+          const int pos1 = U.template page<true>(e0 + kPagesPerTile / 2 - 1) * kBlock + kBlock - 1;
+          plain = pos1 <= U.p_first &&
+                  (pos0 > U.p_first + TM - 1 - p.window || pos1 < p.num_sinks);
+          if (!plain) {
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            // (an entry past the pages read lies past the tile's keys)
-            const int e = kt * kPagesPerTile + kh * 4 + g4;
-            const uint32_t bits = window_bits(U.template page<true>(e) * kBlock, p_row, p.window,
-                                              p.num_sinks);
-            if (g4 & 1)
-              seen[g4 >> 1] |= bits << 16;
-            else
-              seen[g4 >> 1] = bits & 0xffffu;
+            for (int g4 = 0; g4 < 4; ++g4) {
+              // (an entry past the pages read lies past the tile's keys)
+              const uint32_t bits = window_bits(U.template page<true>(e0 + g4) * kBlock, p_row,
+                                                p.window, p.num_sinks);
+              if (g4 & 1)
+                seen[g4 >> 1] |= bits << 16;
+              else
+                seen[g4 >> 1] = bits;
+            }
           }
         }
-        if (WIN ? __all_sync(0xffffffffu, (seen[0] & seen[1]) == 0xffffffffu)
-                : __all_sync(0xffffffffu, lim >= 63)) {
+        if (WIN ? plain : __all_sync(0xffffffffu, lim >= 63)) {
           if (!pos_scale) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * mul);
@@ -1104,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           (key & 15);
           unseen = pos >= U.kv_end || (pos >= p.num_sinks && pos < U.w0);
         }
-        if (WIN ? __any_sync(0xffffffffu, unseen) : kv_local < kKeysPerTile) {
+        if (WIN ? !plain && __any_sync(0xffffffffu, unseen) : kv_local < kKeysPerTile) {
           // A parity wait tells apart only two phases in a row: the stage's
           // barrier must be at this tile's use or the one after, never still
           // at the use SV tiles back (its phase has this tile's parity, and

@@ -237,6 +237,7 @@ __device__ __forceinline__ void pair_softmax(const PrefillParams& p, PrefillShar
     }
     const bool row_valid = tl < U.ntok;
     const int p_row = row_valid ? U.p_first + tl : U.kv_end - 1;
+    const int p_tile = U.p_first + q * TM;  // position of the tile's first row
     float m_ref = kNegInf, l = 0.f;
     for (int kt = U.kt0; kt < U.kt1; ++kt) {
       const int steps = pair_steps(U, kt);
@@ -251,21 +252,27 @@ __device__ __forceinline__ void pair_softmax(const PrefillParams& p, PrefillShar
         uint32_t sr[64];
         tc::tmem_ld32(s_cols, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tc::tmem_ld32(s_cols + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        // which keys the row sees, one bit each (an entry past the pages read
-        // lies past the unit's keys)
-        uint32_t seen[2];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int e = kt * kPagesPerTile + half * 4 + g;
-          const uint32_t bits =
-              window_bits(U.template page<true>(e) * kBlock, p_row, p.window, p.num_sinks);
-          if (g & 1)
-            seen[g >> 1] |= bits << 16;
-          else
-            seen[g >> 1] = bits;
-        }
+        // Does every row of this query tile see every key of the step?  Then
+        // there is nothing to mask, and no V row to clear.
+        const int e0 = kt * kPagesPerTile + half * (kPagesPerTile / 2);
+        const int pos0 = U.template page<true>(e0) * kBlock;
+        const int pos1 = U.template page<true>(e0 + kPagesPerTile / 2 - 1) * kBlock + kBlock - 1;
+        const bool plain =
+            pos1 <= p_tile && (pos0 > p_tile + TM - 1 - p.window || pos1 < p.num_sinks);
         tc::tmem_wait_ld();
-        if (!pos_scale || !__all_sync(0xffffffffu, (seen[0] & seen[1]) == 0xffffffffu)) {
+        if (!plain || !pos_scale) {
+          // which keys the row sees, one bit each (an entry past the pages read
+          // lies past the unit's keys)
+          uint32_t seen[2];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t bits =
+                window_bits(U.template page<true>(e0 + g) * kBlock, p_row, p.window, p.num_sinks);
+            if (g & 1)
+              seen[g >> 1] |= bits << 16;
+            else
+              seen[g >> 1] = bits;
+          }
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             sr[c] = __float_as_uint(
@@ -342,7 +349,7 @@ __device__ __forceinline__ void pair_softmax(const PrefillParams& p, PrefillShar
         const int pos =
             U.template page<true>(kt * kPagesPerTile + (key >> 4)) * kBlock + (key & 15);
         const bool unseen = pos >= U.kv_end || (pos >= p.num_sinks && pos < U.w0);
-        if (__any_sync(0xffffffffu, unseen)) {
+        if (!plain && __any_sync(0xffffffffu, unseen)) {
           // V tile kt must have landed.  These warps may have left out the tiles
           // of units without their query tile, so a parity wait on the stage
           // could not tell its uses apart; the issuer of this query tile's
