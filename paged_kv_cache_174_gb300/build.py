@@ -1,18 +1,22 @@
-"""Build libpagedattn.so (hand-written CUDA for sm_103a) in-tree.
+"""Build libpagedattn.so (hand-written CUDA for sm_103a) and the Python
+extension that calls it (pa_binding.so) in-tree.
 
     python -m paged_kv_cache_174_gb300.build [--force] [--verbose]
 
 Each translation unit is compiled with nvcc in parallel, then linked into a
 shared library with the CUDA runtime linked statically, so the library needs
-only the NVIDIA driver at run time.  Output: paged_kv_cache_174_gb300/_build/.
+only the NVIDIA driver at run time.  The extension is host code on torch's and
+Python's headers, linked to the library beside it.  Output: paged_kv_cache_174_gb300/_build/.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,9 @@ SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_decode_fp8.cu", "pa_d
            "pa_prefill.cu", "pa_prefill_fp8.cu", "pa_graph.cu", "pa_step.cu", "pa_rotary.cu",
            "pa_decode_window.cu", "pa_decode_window_fp8.cu", "pa_prefill_window.cu",
            "pa_prefill_window_fp8.cu"]
+BINDING_SOURCE = "pa_binding.cpp"
+BINDING_NAME = "pa_binding.so"
+BINDING = os.path.join(OUT_DIR, BINDING_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -56,6 +63,14 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    """torch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
 def _run(cmd, verbose: bool):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or r.returncode != 0:
@@ -79,13 +94,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             cmd = [cc] + ARCH + CFLAGS + (["-Xptxas", "-v"] if ptxas_verbose else []) + [
                 "-c", path, "-o", obj]
             jobs.append(cmd)
+    binding_src = os.path.join(CSRC, BINDING_SOURCE)
+    binding_obj = os.path.join(OUT_DIR, BINDING_SOURCE.replace(".cpp", ".o"))
+    torch_dir = _torch_dir()
+    if force or _stale(binding_obj, [binding_src, os.path.join(INCLUDE, "pagedattn.h")]):
+        inc = os.path.join(torch_dir, "include")
+        jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I", INCLUDE, "-I", inc, "-I",
+                     os.path.join(inc, "torch", "csrc", "api", "include"), "-I",
+                     os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))),
+                                  "include"),
+                     "-I", sysconfig.get_paths()["include"], "-c", binding_src, "-o",
+                     binding_obj])
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(lambda c: _run(c, verbose or ptxas_verbose), jobs))
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
-        _run([cc] + ARCH + ["-shared", "-o", tmp] + objs, verbose)
+        _run([cc] + ARCH + ["-shared", "-Xlinker", "-soname=" + LIB_NAME, "-o", tmp] + objs,
+             verbose)
         os.replace(tmp, LIB)
+    if force or jobs or _stale(BINDING, [binding_obj, LIB]):
+        tmp = BINDING + ".tmp"
+        torch_lib = os.path.join(torch_dir, "lib")
+        _run(["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L", torch_lib, "-ltorch_python",
+              "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN",
+              "-Wl,-rpath," + torch_lib], verbose)
+        os.replace(tmp, BINDING)
     return LIB
 
 

@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 from typing import Optional
@@ -20,6 +22,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpagedattn.so")
+BINDING_PATH = os.path.join(_HERE, "_build", "pa_binding.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "pagedattn.h")
 
 PA_OK = 0
@@ -34,6 +37,7 @@ class PagedAttnError(RuntimeError):
 
 
 _lib = None
+_binding = None  # the extension module of the calls around a step (csrc/pa_binding.cpp)
 
 
 class StepBuffers(ctypes.Structure):
@@ -124,6 +128,22 @@ def _load() -> ctypes.CDLL:
     L.pa_step_graph_destroy.restype = ctypes.c_int
     _lib = L
     return L
+
+
+def _load_binding():
+    """The extension module that takes the plain calls around a step."""
+    global _binding
+    _load()
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("pa_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("pa_binding", BINDING_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+    except (ImportError, OSError) as e:
+        raise PagedAttnError(-1, f"cannot load {BINDING_PATH}: {e}; build it with "
+                                 "`python -m paged_kv_cache_174_gb300.build`") from e
+    _binding = module
+    return module
 
 
 def lib() -> ctypes.CDLL:
@@ -549,6 +569,9 @@ def copy_blocks_fp8(k_cache, v_cache, src_dst_pairs: torch.Tensor, *, num_kv_hea
 # rotary positions with the slot scatter, attention with a sliding window.
 # These run on the device of their tensors (all on one), whichever device is
 # current, and allocate what the caller does not pass on the stream they use.
+# The plain case (contiguous tensors on the current device, the current stream)
+# goes through the extension module, which checks the tensors itself; it answers
+# None for anything else, and the checks here then name what is wrong.
 # ---------------------------------------------------------------------------
 
 def _check_tensors(specs) -> torch.device:
@@ -639,6 +662,15 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
     [S + 1], slot_mapping [num_tokens], positions [num_axes, num_tokens]); each
     may be passed in to be written (seq_lens may be context_lens itself).
     """
+    if stream is None:
+        r = (_binding or _load_binding()).build_step(
+            context_lens, new_lens, block_tables, free_blocks, free_count, free_count_out,
+            position_offsets, seq_lens, query_start_loc, slot_mapping, positions, block_size,
+            num_tokens, num_axes)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
     L = _lib or _load()
     i32 = torch.int32
     T, A = int(num_tokens), int(num_axes)
@@ -707,6 +739,13 @@ def _token_rows(t, name, index, T, d):
 
 def _rotary(fp8, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, axes, interleaved,
             q_out, stream):
+    if stream is None:
+        r = (_binding or _load_binding()).rotary(fp8, q, k, v, positions, inv_freq, k_cache,
+                                                 v_cache, slot_mapping, axes, interleaved, q_out)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
     L = _lib or _load()
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [T, n_q, d]")
@@ -804,6 +843,14 @@ def rotary_reshape_and_cache_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
 def _window_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
                       window, num_sinks, min_q_len, max_q_len, max_seq_len, out, workspace,
                       stream):
+    if stream is None:
+        r = (_binding or _load_binding()).window(
+            fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, window,
+            num_sinks, min_q_len, max_q_len, max_seq_len, out, workspace)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
     L = _lib or _load()
     kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
     device = _check_tensors((
