@@ -652,7 +652,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_out;
         const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
+        // 8-bit cache: the tile's table entries are fetched a tile ahead
+        auto table_entry = [&](int kt, int i) {
+          const int e = kt * kPagesPerTile + pg_lo + i;
+          if (pg_lo + i >= pg_hi || e >= U.pages) return 0;
+          return __ldg(table + (U.template page<WIN>(e) >> p.block_shift));
+        };
+        int next[4];
+        if constexpr (F8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next[i] = table_entry(U.kt0, i);
+        }
         for (int kt = U.kt0; kt < U.kt1; ++kt, ++c) {
+          int entry[4];
+          if constexpr (F8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              entry[i] = next[i];
+              next[i] = kt + 1 < U.kt1 ? table_entry(kt + 1, i) : 0;
+            }
+          }
           // per page: -1 (nothing to load), 0 (cached rows: the cache), 1
           // (new rows only: k_new / v_new), 2 (both: the cache, then the new
           // rows copied over)
@@ -671,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bytes += NH * (kBlock * 128);
                 continue;
               }
-              const int b = __ldg(table + (lp >> p.block_shift));
+              const int b = F8 ? entry[i] : __ldg(table + (lp >> p.block_shift));
               if (b < 0 || b >= p.num_blocks) {
                 if (lane == 0) flag_error(p.err, DEVERR_BOUNDS);
               } else {
@@ -687,54 +706,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             // plain loads issued before the stage is free (their latency
             // overlaps the wait); lane j-th chunk: 16 codes of one row
             constexpr int CPR = D / 16;                  // chunks per row
-            constexpr int NJ = PG * kBlock * CPR / 32;   // chunks per lane
+            constexpr int RPJ = 32 / CPR;                // rows per load of the warp
+            constexpr int JPP = kBlock / RPJ;            // loads per page
+            constexpr int NJ = PG * JPP;                 // chunks per lane
             const uint8_t* pages = k_warp ? p.k_codes : p.v_codes;
             const int64_t page_bytes = fp8_page_bytes(p.n_kv, D);
-            const int64_t scales_at = fp8_scales_offset(p.n_kv, D);
+            // this lane's chunk of the page's first rows, and the scale of the
+            // page's row lane % 16 (handed to the row's lanes by a shuffle)
+            const uint8_t* lane_codes =
+                pages + ((lane / CPR) * p.n_kv + U.g) * D + (lane % CPR) * 16;
+            const uint8_t* lane_scales =
+                pages + fp8_scales_offset(p.n_kv, D) + ((lane % kBlock) * p.n_kv + U.g) * 4;
             uint4 w8[NJ];
-            float sc[NJ];
+            float sc[PG];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const int pi = (32 * j) / D;  // page of the warp (D rows x chunks per page)
-              const int rem = (32 * j) % D + lane;
-              w8[j] = make_uint4(0u, 0u, 0u, 0u);
-              sc[j] = 0.f;
-              if (phys[pi] >= 0) {
-                const uint8_t* page = pages + (int64_t)phys[pi] * page_bytes;
-                const int row = (rem / CPR) * p.n_kv + U.g;  // (token row, head) in the page
-                w8[j] = __ldg(reinterpret_cast<const uint4*>(page + (int64_t)row * D) + rem % CPR);
-                sc[j] = __ldg(reinterpret_cast<const float*>(page + scales_at) + row);
+            for (int i = 0; i < PG; ++i) {
+              const int64_t page = (int64_t)phys[i] * page_bytes;
+              sc[i] = 0.f;
+              if (phys[i] >= 0) sc[i] = __ldg(reinterpret_cast<const float*>(lane_scales + page));
+#pragma unroll
+              for (int j = 0; j < JPP; ++j) {
+                w8[i * JPP + j] = make_uint4(0u, 0u, 0u, 0u);
+                if (phys[i] >= 0)
+                  w8[i * JPP + j] = __ldg(reinterpret_cast<const uint4*>(
+                      lane_codes + page + j * RPJ * p.n_kv * D));
               }
             }
             // the stage's last reader released it (as below)
             if (lane == 0 && c >= (int)nst)
               mbar_wait(smem_addr(&empty[st]), pos.phase ^ 1u, p.err, abort_flag);
             __syncwarp();
-            unsigned char* stage = ring + st * KV_BYTES;
+            // where the chunk's 16 values go, as elements 16 c16 .. +15 of row r:
+            // half c16 / 4, 16-byte chunks 2 (c16 % 4) and the next of that half's
+            // 128-byte row (the next is the first's address with bit 4 flipped)
+            const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
+            unsigned char* lane_at =
+                ring + st * KV_BYTES + (c16 >> 2) * (k_warp ? HALF : kBlock * 128);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-              const int pi = (32 * j) / D;
+              const int pi = j / JPP;
               if (phys[pi] < 0) continue;  // no page there: nothing is read from it
-              const int rem = (32 * j) % D + lane;
-              const int r = rem / CPR, c16 = rem % CPR;
-              const int pg = pg_lo + pi;
+              const int r = (j % JPP) * RPJ + lane / CPR;
               uint32_t h[8];  // the chunk's 16 values, f16
-              const uint32_t sc2 = f16x2_from_floats(sc[j], sc[j]);
+              const float row_scale = __shfl_sync(0xffffffffu, sc[pi], r);
+              const uint32_t sc2 = f16x2_from_floats(row_scale, row_scale);
               f16x4_from_e4m3x4_scaled(w8[j].x, sc2, h[0], h[1]);
               f16x4_from_e4m3x4_scaled(w8[j].y, sc2, h[2], h[3]);
               f16x4_from_e4m3x4_scaled(w8[j].z, sc2, h[4], h[5]);
               f16x4_from_e4m3x4_scaled(w8[j].w, sc2, h[6], h[7]);
-              // elements 16 c16 .. +15: half c16 / 4, 16-byte chunks 2 (c16 % 4)
-              // and the next of that half's 128-byte row
-              const int hh = c16 >> 2, c8 = (c16 & 3) * 2;
-              unsigned char* d0 =
-                  k_warp ? stage + hh * HALF + sw128_chunk(pg * kBlock + r, c8)
-                         : stage + pg * V_PAGE + hh * (kBlock * 128) + sw128_chunk(r, c8);
-              unsigned char* d1 =
-                  k_warp ? stage + hh * HALF + sw128_chunk(pg * kBlock + r, c8 + 1)
-                         : stage + pg * V_PAGE + hh * (kBlock * 128) + sw128_chunk(r, c8 + 1);
-              *reinterpret_cast<uint4*>(d0) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(d1) = make_uint4(h[4], h[5], h[6], h[7]);
+              const uint32_t at = sw128_chunk(r, c8);
+              unsigned char* page_at = lane_at + (pg_lo + pi) * (k_warp ? kBlock * 128 : V_PAGE);
+              *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
+                  make_uint4(h[4], h[5], h[6], h[7]);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
