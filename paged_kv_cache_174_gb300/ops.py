@@ -582,7 +582,7 @@ def _check_tensors(specs) -> torch.device:
     for name, t, dtype, dim in specs:
         if t is None:
             continue
-        if type(t) is not torch.Tensor or t.dtype is not dtype or t.dim() != dim or \
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dim or \
                 not t.is_contiguous():
             _need(t, name, dtype, dim)
         on = t.get_device()  # -1: not a CUDA tensor
@@ -706,7 +706,7 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
         code = L.pa_build_step(
             context_lens.data_ptr(), new_lens.data_ptr(),
             None if position_offsets is None else position_offsets.data_ptr(), S, T, A,
-            block_tables.data_ptr(), width, block_size, free_blocks.data_ptr(),
+            block_tables.data_ptr(), width, int(block_size), free_blocks.data_ptr(),
             free_count.data_ptr(), free_count_out.data_ptr(), free_blocks.shape[0],
             seq_lens.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
             positions.data_ptr(), handle)
@@ -718,7 +718,7 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
 def _token_rows(t, name, index, T, d):
     """Checks a bf16 CUDA tensor [T, heads, d] whose tokens may be strided;
     returns (heads, token stride)."""
-    if type(t) is not torch.Tensor or t.dtype is not torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a torch.bfloat16 tensor")
     if t.get_device() != index or index < 0:
         raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
@@ -776,7 +776,7 @@ def _rotary(fp8, q, k, v, positions, inv_freq, k_cache, v_cache, slot_mapping, a
     half = inv_freq.shape[0]
     if slot_mapping.shape[0] != T:
         raise ValueError("slot_mapping must be [T]")
-    if type(positions) is not torch.Tensor or positions.dtype is not torch.int32:
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32:
         raise TypeError("positions must be a torch.int32 tensor")
     if positions.get_device() != index:
         raise ValueError("positions must be a CUDA tensor on the other tensors' device")
@@ -885,9 +885,9 @@ def _window_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_st
         fn = L.pa_paged_attention_window_fp8 if fp8 else L.pa_paged_attention_window
         code = fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
                   block_tables.data_ptr(), width, seq_lens.data_ptr(),
-                  query_start_loc.data_ptr(), S, T, min_q_len, max_q_len, max_seq_len, window,
-                  num_sinks, scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                  handle)
+                  query_start_loc.data_ptr(), S, T, int(min_q_len), int(max_q_len),
+                  int(max_seq_len), int(window), int(num_sinks), float(scale), out.data_ptr(),
+                  workspace.data_ptr(), workspace.numel(), handle)
     if code:
         _check(code)
     return out

@@ -198,3 +198,15 @@ def test_refusals():
         ops.build_step(a[0], _i32([1]), *a[2:], **kw)
     with pytest.raises(ValueError):
         ops.build_step(*a[:4], _i32([1, 2]), **kw)
+
+
+def test_either_way_into_the_library():
+    """The extension module's call and the binding's own checks (taken for a
+    given stream, other number types) write the same values."""
+    ctx, new, tables, free, count, off = _case(7, 20, 100, 30, 16)
+    T = int(new.sum()) + 3
+    want = R.build_step(ctx, new, tables, free, count, 16, T, 2, off)
+    for kw in (dict(), dict(stream=torch.cuda.current_stream())):
+        for num in (int, np.int64):
+            _compare(_run(ctx, new, tables, free, count, off, num(16), num(T), num(2), **kw), want)
+    ops.check_device_errors()

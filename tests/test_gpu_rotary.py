@@ -214,3 +214,44 @@ def test_refusals():
     with pytest.raises(ops.PagedAttnError):  # 24 rotated elements
         ops.rotary_reshape_and_cache(**{**good, "inv_freq": f[:12].contiguous(),
                                         "axes": a[:12].contiguous()})
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_either_way_into_the_library(fp8):
+    """The extension module's call and the binding's own checks (taken for a
+    given stream and for a tensor subclass) write the same bits."""
+    q, k, v, pos, freq, of, slots, nb = _inputs(9, 50, 8, 2, 64, 64, 3, 9999, packed=True)
+    f, a, s = torch.from_numpy(freq).cuda(), torch.from_numpy(of).cuda(), \
+        torch.from_numpy(slots).cuda()
+    call = ops.rotary_reshape_and_cache_fp8 if fp8 else ops.rotary_reshape_and_cache
+    seen = []
+    for kw in (dict(), dict(stream=torch.cuda.current_stream()),
+               dict(axes=torch.nn.Parameter(a, requires_grad=False))):
+        kc, vc = ops.empty_fp8_cache(nb, 16, 2, 64) if fp8 else \
+            (torch.zeros(nb, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        out = call(q, k, v, pos, f, kc, vc, s, **{"axes": a, **kw})
+        seen.append([x.view(torch.uint8) for x in (out, kc, vc)])
+    for other in seen[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(seen[0], other))
+    ops.check_device_errors()
+
+
+def test_quotients_are_those_of_the_plain_scatter():
+    """Values whose row maxima cover fp32's range, elements down to nothing:
+    every code as the plain 8-bit scatter's division gives it."""
+    g = torch.Generator().manual_seed(11)
+    T, nkv, d = 2048, 2, 128
+    x = torch.randn(T, nkv, d, generator=g)
+    x = x * torch.exp2(torch.randint(-126, 120, (T, nkv, 1), generator=g).float())
+    x = x * torch.exp2(-torch.randint(0, 30, (T, nkv, d), generator=g).float())
+    v = x.bfloat16().cuda()
+    q = torch.zeros(T, 2, d, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")  # no turn: keys as they are
+    f = torch.ones(d // 2, dtype=torch.float64, device="cuda")
+    a, b = ops.empty_fp8_cache(T // 16, 16, nkv, d)
+    c, e = ops.empty_fp8_cache(T // 16, 16, nkv, d)
+    ops.rotary_reshape_and_cache_fp8(q, v, v, pos, f, a, b, slots)
+    ops.reshape_and_cache_fp8(v, v, c, e, slots)
+    ops.check_device_errors()
+    assert torch.equal(b, e) and torch.equal(a, c)

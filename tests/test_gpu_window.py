@@ -345,3 +345,19 @@ def test_refusals():
     b.dt = keep.long()
     with pytest.raises(TypeError):
         b.run()
+
+
+@BOTH
+def test_either_way_into_the_library(fp8):
+    """The extension module's calls and the binding's own checks (taken for a
+    given stream, other number types, a workspace to allocate, a tensor
+    subclass) give the same bits."""
+    b = Batch(18, [300, 90, 513], [1, 40, 70], 8, 2, 64, 75, 5, fp8=fp8)
+    ws = ops.alloc_workspace(3, 111, 8, 2, 64, 70, 513)
+    want = b.run(workspace=ws)
+    here = torch.cuda.current_stream()
+    for kw in (dict(workspace=ws, stream=here), dict(), dict(workspace=ws, max_q_len=np.int64(70)),
+               dict(workspace=torch.nn.Parameter(ws, requires_grad=False))):
+        assert torch.equal(b.run(**kw).view(torch.int16), want.view(torch.int16))
+    assert b.run(workspace=ws, out=want) is want
+    ops.check_device_errors()

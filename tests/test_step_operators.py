@@ -149,6 +149,18 @@ def test_window_refusals(lib, form):
         assert call(**bad) == "PA_ERR_UNSUPPORTED", bad
 
 
+def test_extension_module_leaves_what_is_not_plain(lib):
+    """It answers None, and the binding's own checks decide."""
+    m = ops._load_binding()
+    assert m.build_step() is None and m.rotary(1, 2) is None and m.window() is None
+    i32 = torch.zeros(4, dtype=torch.int32)
+    assert m.build_step(i32, i32, i32.view(2, 2), i32, i32[:1], *[None] * 6, 16, 4, 1) is None
+    assert m.rotary(False, *[i32] * 9, False, None) is None
+    assert m.rotary(False, *[3] * 9, False, None) is None
+    assert m.window(False, *[i32] * 6, 0.5, 1, 0, 0, 1, 4, None, i32) is None
+    assert m.window(False, *[None] * 6, 0.5, 1, 0, 0, 1, 4, None, None) is None
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types(lib):
     i32 = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
