@@ -17,6 +17,14 @@ __device__ __forceinline__ void flag_error(unsigned* err, unsigned bits) {
   atomicOr(err, bits);
 }
 
+// For a kernel launched with launch_early(): waits until the kernels before it
+// on the stream are complete, and then lets the next one that was launched so
+// be scheduled.  Before this call it may read nothing that they write.
+__device__ __forceinline__ void after_prior_kernels() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ unsigned long long global_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

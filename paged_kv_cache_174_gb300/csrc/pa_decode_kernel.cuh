@@ -78,6 +78,7 @@ struct DecodeParams {
   // Sliding window (the WIN instances): a request's pages are those with a
   // key its row sees, the sinks' pages first, then the window's
   int32_t window, num_sinks;
+  int32_t early;  // launched with launch_early (WIN, and no prefill before it)
 };
 
 // Which pages of a request of length L a windowed decode row reads.
@@ -576,6 +577,11 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
   const int c = blockIdx.x;
   const int NST = p.nstages;
   // the merge kernel waits for this whole grid anyway; let it be scheduled
+  // (with a window the kernel itself may start before the call's inputs are
+  // complete: only after them, since the merge reads them before its wait)
+  if constexpr (WIN) {
+    if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   asm volatile("griddepcontrol.launch_dependents;");
 
   // ---------------------------------------------------------------- plan
@@ -1430,6 +1436,7 @@ cudaError_t launch_decode_t(const AttnArgs& a, const DecodeWorkspace& ws, int ct
   p.block_shift = a.block_shift;
   p.window = a.window;
   p.num_sinks = a.num_sinks;
+  p.early = WIN && !a.after_prefill ? 1 : 0;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.ctas = ctas;
   p.row_bytes = (uint32_t)NKV * D * (F8 ? 1 : 2);
@@ -1478,6 +1485,8 @@ cudaError_t launch_decode_t(const AttnArgs& a, const DecodeWorkspace& ws, int ct
     pcfg.attrs = pattr;
     pcfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&pcfg, kern, p);
+  } else if (WIN) {
+    e = launch_early(kern, dim3(ctas), dim3(threads), smem, stream, 1, p);
   } else {
     kern<<<ctas, threads, smem, stream>>>(p);
     e = cudaGetLastError();

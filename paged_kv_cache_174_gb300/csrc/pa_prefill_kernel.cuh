@@ -481,7 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   PrefillShared& B = *reinterpret_cast<PrefillShared*>(v_s + SV * KV_BYTES);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the merge grid of split keys may start launching now
+  // the merge grid of split keys may start launching now, and so may the decode
+  // grid, which reads the call's inputs without a wait of its own: with a window
+  // this kernel may be early itself, so only once they are complete
+  if constexpr (WIN) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   // fetch the tensor maps this instance uses ahead of their first copy
   if (threadIdx.x == 32) {
@@ -1479,8 +1482,13 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  kern<<<grid, kThreads, smem, stream>>>(p, qm, km, vm, knm, vnm);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (WIN) {
+    e = launch_early(kern, dim3(grid), dim3(kThreads), smem, stream, 1, p, qm, km, vm, knm, vnm);
+  } else {
+    kern<<<grid, kThreads, smem, stream>>>(p, qm, km, vm, knm, vnm);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || plan.nsplit == 1) return e;
   // the merge may launch while the prefill grid runs; it waits for that grid
   // with griddepcontrol.wait before reading a piece

@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kRotWarps + warp;
   const int64_t t = split == 1 ? unit : unit / kRotWarps;
+  after_prior_kernels();
   if (t >= p.num_tokens) return;
   const int step = HEADS * split;
   const int l = lane % LPR;
@@ -279,11 +280,9 @@ static cudaError_t launch_rotary_t(const RotaryArgs& p, cudaStream_t stream) {
   const int split = p.num_tokens <= kRotSplitTokens ? kRotWarps : 1;
   const int64_t warps = (int64_t)p.num_tokens * split;
   const unsigned grid = (unsigned)((warps + kRotWarps - 1) / kRotWarps);
-  if (p.interleaved)
-    rotary_cache_kernel<D, F8, true><<<grid, kRotThreads, 0, stream>>>(p, split);
-  else
-    rotary_cache_kernel<D, F8, false><<<grid, kRotThreads, 0, stream>>>(p, split);
-  return cudaGetLastError();
+  return launch_early(p.interleaved ? rotary_cache_kernel<D, F8, true>
+                                    : rotary_cache_kernel<D, F8, false>,
+                      dim3(grid), dim3(kRotThreads), 0, stream, 1, p, split);
 }
 
 cudaError_t launch_rotary_cache(const RotaryArgs& p, cudaStream_t stream) {

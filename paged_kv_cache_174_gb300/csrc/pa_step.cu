@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
   const int me = blockIdx.x * threads + tid, all = gridDim.x * threads;
   const int bs = p.block_size;
 
+  after_prior_kernels();
   const int raw_count = *p.free_count;
   const bool count_ok = raw_count >= 0 && raw_count <= p.num_blocks;
   const int count = count_ok ? raw_count : 0;
@@ -179,19 +180,8 @@ cudaError_t launch_build_step(const StepPlanArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const bool one = p.num_tokens <= kPlanOneCta;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(one ? 1 : 8);
-  cfg.blockDim = dim3(one ? 512 : kPlanWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = one ? 1 : 8;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, build_step_kernel, p);
+  return launch_early(build_step_kernel, dim3(one ? 1 : 8), dim3(one ? 512 : kPlanWarps * 32), smem,
+                      stream, one ? 1 : 8, p);
 }
 
 }  // namespace pa
