@@ -84,7 +84,7 @@ constexpr int kThreads = 512;
 constexpr float kNegInf = -INFINITY;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxSplit = 4;
-constexpr double kPairCost = 1.8, kPairCostFp8 = 1.45;  // see pair_query_tiles
+constexpr double kPairCost = 1.7, kPairCostFp8 = 1.4;  // see pair_query_tiles
 constexpr int kMaxListed = 1024;   // prefill requests the shared-memory unit list holds
 
 // Instances of the kernel: the plain one reads the bf16 cache; the fused
@@ -190,8 +190,16 @@ struct UnitCursor {
   }
   __device__ __forceinline__ bool locate(const PrefillParams& p, long long u, Unit& U) {
     const long long per = (long long)p.n_kv * p.nsplit;
-    const long long tile = u / per;
-    const int rem = (int)(u % per);
+    // (a 64-bit division takes several times a 32-bit one)
+    long long tile;
+    int rem;
+    if (u < 0x7fffffffll && per < 0x7fffffffll) {
+      tile = (unsigned)u / (unsigned)per;
+      rem = (int)((unsigned)u % (unsigned)per);
+    } else {
+      tile = u / per;
+      rem = (int)(u % per);
+    }
     int s;
     if (seq) {
       while (i < n && tile >= tbase[i + 1]) ++i;
@@ -236,7 +244,7 @@ struct UnitCursor {
   }
 };
 
-struct PrefillShared {
+struct alignas(16) PrefillShared {
   uint64_t q_full, q_empty;
   uint64_t q_land;  // 8-bit cache: the bf16 query tile has landed (then rewritten)
   uint64_t k_full[kStagesMax], k_empty[kStagesMax];
@@ -289,6 +297,39 @@ __device__ __forceinline__ void f16x4_from_e4m3x4_scaled(uint32_t w, uint32_t sc
   f16x2x2_from_e4m3x4(w, a, b);
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(sc2));
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(sc2));
+}
+
+// Output rows through shared memory (sliding window).  A thread holds 32 values
+// of a row of its own; stored straight, each instruction of a warp would touch
+// 32 rows, and the SM's store path takes a row at a time (128 rows of 128 values
+// took 5500 cycles of two softmax groups, 1700 this way).  The warp's 32 rows of
+// 64 bytes go through its staging block, the four 16-byte pieces of a row
+// rotated by the row's number so that neither side has bank conflicts, and
+// come out four lanes to a row.
+constexpr uint32_t kOutStage = 32 * 64;
+// o: 32 fp32 values of this lane's row, times inv, as bf16 to column col of the
+// row; row: the lane's output row, or -1.  Whole warp.
+template <int D>
+__device__ __forceinline__ void store_rows(uint16_t* out, int64_t row, int col, unsigned char* stage,
+                                           const uint32_t (&o)[32], float inv, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 w;
+    w.x = pack_bf16x2(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
+    w.y = pack_bf16x2(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
+    w.z = pack_bf16x2(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
+    w.w = pack_bf16x2(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((j + (lane >> 1)) & 3) * 16) = w;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 8 * k + (lane >> 2), piece = lane & 3;
+    const int64_t to = __shfl_sync(0xffffffffu, row, r);
+    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece + (r >> 1)) & 3) * 16);
+    if (to >= 0) *reinterpret_cast<uint4*>(out + to * D + col + piece * 8) = w;
+  }
+  __syncwarp();
 }
 
 // Byte offset of 16-byte chunk c (0..7) of row r inside a [rows][64 x bf16]
@@ -479,6 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* k_s = q_s + QT * Q_BYTES;
   unsigned char* v_s = k_s + SK * KV_BYTES;
   PrefillShared& B = *reinterpret_cast<PrefillShared*>(v_s + SV * KV_BYTES);
+  static_assert(sizeof(PrefillShared) % 16 == 0, "the output staging follows it");
+  unsigned char* out_s = v_s + SV * KV_BYTES + sizeof(PrefillShared);  // (sliding window)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the merge grid of split keys may start launching now, and so may the decode
@@ -983,7 +1026,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (QT == 2) {
       UnitCursor<QT * TM, WIN> cur;
       cur.init(p, B.list_seq, B.list_base, B.listed);
-      pair_softmax<D, G, F8>(p, B, cur, total_units, tmem, v_s, warp, lane);
+      pair_softmax<D, G, F8>(p, B, cur, total_units, tmem, v_s, out_s + (warp - 2) * kOutStage,
+                             warp, lane);
     } else {
     const int quarter = warp & 3;    // TMEM lanes 32*quarter .. +31
     const int kh = (warp - 2) >> 2;  // key half of each tile: 64*kh .. 64*kh + 63
@@ -1210,6 +1254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tc::tmem_ld32(tmem + lane_addr + O_COL + kh * (D / 2) + c * 32, o);
         tc::tmem_wait_ld();
+        if constexpr (WIN) {
+          if (p.nsplit == 1) {
+            store_rows<D>(p.out, row_valid ? row : -1, kh * (D / 2) + c * 32,
+                          out_s + (warp - 2) * kOutStage, o, inv, lane);
+            continue;
+          }
+        }
         if (!row_valid) continue;
         if (p.nsplit == 1) {
           uint16_t* orow = p.out + row * D + kh * (D / 2) + c * 32;
@@ -1353,10 +1404,11 @@ cudaError_t make_map(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int G>
+template <int D, int G, bool WIN>
 size_t prefill_smem_bytes() {
   constexpr size_t half = kRows * 128;
-  return 1024 + (size_t)(D / 64) * half * (1 + kStagesK + kStagesV) + sizeof(PrefillShared);
+  return 1024 + (size_t)(D / 64) * half * (1 + kStagesK + kStagesV) + sizeof(PrefillShared) +
+         (WIN ? kSoftmaxWarps * kOutStage : 0);
 }
 
 size_t split_bytes(int num_tokens, int num_q_heads, int head_dim, int nsplit) {
@@ -1471,7 +1523,7 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
   const long long units_bound = tiles_bound * a.num_kv_heads * plan.nsplit;
   const int grid = (int)(units_bound < sm_count ? units_bound : sm_count);
   if (grid <= 0) return cudaSuccess;
-  const size_t smem = prefill_smem_bytes<D, G>();
+  const size_t smem = prefill_smem_bytes<D, G, WIN>();
   auto kern = prefill_kernel<D, G, KIND, WIN, QT>;
   static int configured_device = -1;
   int dev = 0;
@@ -1509,9 +1561,9 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
 // units, so it pays when they fill the SMs for more rounds than the longer
 // units cost: kPairCost* is a pair's time over a single tile's, measured with
 // one round of each (32 q / 8 kv heads of 128, a 4096-token window: 512 rows in
-// single tiles 42.4 us, 1024 in pairs 76.1, 1024 in single tiles 79.5; the 8-bit
-// cache 67.9, 98.1, 139.7).  At 8192 rows: 512 against 526 us, 8-bit 672
-// against 976; heads of 64: 434 against 500 and 556 against 643.
+// single tiles 42.5 us, 1024 in pairs 72.3, 1024 in single tiles 79.5; the 8-bit
+// cache 69.7, 96.4, 139.7).  At 8192 rows: 480 against 526 us, 8-bit 664
+// against 976; heads of 64: 444 against 500 and 510 against 643.
 template <int D, int G, int KIND>
 bool pair_query_tiles(const AttnArgs& a, const PrefillPlan& plan, int sm_count) {
   constexpr int TM = kRows / G;

@@ -23,10 +23,12 @@
 //    thread spends as long on the wait before and the commit after a product
 //    as on its issue, so the four products of a step now have an issuer for
 //    each query tile, 492 us;
-//  * no key bits where a whole step is seen by every row, 477 us.
-// Without any exponential it would take 452 us, so what paces it now is the
-// products' hand-offs, not the softmax's arithmetic.  With the 8-bit cache the
-// producers' conversion paces it.
+//  * no key bits where a whole step is seen by every row, 477 us (without any
+//    exponential it would then have taken 452 us, so the products' hand-offs
+//    pace it more than the softmax's arithmetic);
+//  * output rows through shared memory, and the unit's place found with 32-bit
+//    divisions: 451 us, 1143 TFLOP/s.
+// With the 8-bit cache the producers' conversion paces it.
 //
 // Buffer b = 2 * half + query tile.  A half is one "step"; with one query tile
 // in the unit (an odd number of them) the other's buffers rest.
@@ -219,7 +221,8 @@ __device__ __forceinline__ void pair_issue_pv(const PrefillParams& p, PrefillSha
 template <int D, int G, bool F8, class Cursor>
 __device__ __forceinline__ void pair_softmax(const PrefillParams& p, PrefillShared& B, Cursor& cur,
                                              long long total_units, uint32_t tmem,
-                                             unsigned char* v_s, int warp, int lane) {
+                                             unsigned char* v_s, unsigned char* out_s, int warp,
+                                             int lane) {
   constexpr int TM = kRows / G;
   constexpr int NH = D / 64;
   constexpr uint32_t V_PAGE = NH * kBlock * 128;
@@ -395,22 +398,13 @@ __device__ __forceinline__ void pair_softmax(const PrefillParams& p, PrefillShar
     // first P V waits for o_empty, which these warps arrive on
     mbar_wait(smem_addr(&B.o_full[q]), n_out & 1, p.err, abort_flag);
     tc::fence_after_sync();
-    uint16_t* orow = p.out + ((int64_t)(U.q0 + tl) * p.n_q + U.g * G + hl) * D;
+    const int64_t row = row_valid ? (int64_t)(U.q0 + tl) * p.n_q + U.g * G + hl : -1;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       tc::tmem_ld32(o_cols + c * 32, o);
       tc::tmem_wait_ld();
-      if (!row_valid) continue;
-#pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint4 w;
-        w.x = pack_bf16x2(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-        w.y = pack_bf16x2(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
-        w.z = pack_bf16x2(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
-        w.w = pack_bf16x2(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-        *reinterpret_cast<uint4*>(orow + c * 32 + j) = w;
-      }
+      store_rows<D>(p.out, row, c * 32, out_s, o, inv, lane);
     }
     tc::fence_before_sync();
     __syncwarp();
