@@ -470,7 +470,7 @@ int pa_rotary_reshape_and_cache_fp8(const pa_bf16 *q, int64_t q_stride, const pa
  * reused (a rolling cache).  Cached rows outside every row's view have no
  * effect, whatever they hold; within a request's prompt chunk, a key or value
  * that is not finite reaches the rows that see it and, for values, may reach
- * the rows computed with them (128 / group consecutive tokens).
+ * the rows computed with them (up to 256 / group consecutive tokens).
  *
  *   window        >= 1; a window of max_seq_len or more is
  *                 pa_paged_attention_qrange

@@ -32,7 +32,7 @@ namespace {
 constexpr int kRotThreads = 128;
 constexpr int kRotWarps = kRotThreads / 32;
 // Up to this many tokens the four warps of a CTA share a token's heads (64
-// tokens of 32 + 8 heads of 128: 3.1 us, 5.1 with a warp for each token); past
+// tokens of 32 + 8 heads of 128: 3.2 us, 5.1 with a warp for each token); past
 // it the angles, which each of them computes, cost more than the wait for the
 // heads (2048 tokens: 12.0 us a warp each, 12.7 shared).
 constexpr int kRotSplitTokens = 1024;
@@ -174,8 +174,8 @@ __device__ __forceinline__ void store_fp8(unsigned char* codes_at, float* scale_
 // DEPTH passes of a warp have their loads in flight together.  The bf16 cache
 // takes three with 80 registers a thread (4099 tokens of 16 + 4 heads of 64,
 // half rotated: 5.9 us, 4.3 TB/s; two: 6.2), the 8-bit cache, whose codes cost
-// more instructions, two with 64 registers (8191 tokens of 32 +
-// 8 heads of 128: 35.0 us, 5.3 TB/s; three: 36.6).
+// more instructions, two with 64 registers (8191 tokens of 32 + 8 heads of 128:
+// 34.7 us, 5.3 TB/s; three: 36.6).
 template <int D, bool F8, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
     rotary_cache_kernel(const RotaryArgs p, int split) {

@@ -186,6 +186,7 @@ def test_many_requests(fp8):
     lens = [17 + i % 40 for i in range(n)]
     Batch(6, lens, [1] * n, 2, 1, 64, 20, 2, fp8=fp8).check()
     Batch(7, lens, [2 + i % 3 for i in range(n)], 2, 1, 64, 20, 2, fp8=fp8).check()
+    Batch(7, lens, [2 + i % 16 for i in range(n)], 8, 1, 64, 20, 2, fp8=fp8).check()
 
 
 @BOTH
