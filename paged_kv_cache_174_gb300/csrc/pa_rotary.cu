@@ -31,11 +31,14 @@ namespace {
 
 constexpr int kRotThreads = 128;
 constexpr int kRotWarps = kRotThreads / 32;
-// Up to this many tokens the four warps of a CTA share a token's heads (64
-// tokens of 32 + 8 heads of 128: 3.2 us, 5.1 with a warp for each token); past
-// it the angles, which each of them computes, cost more than the wait for the
-// heads (2048 tokens: 12.0 us a warp each, 12.7 shared).
-constexpr int kRotSplitTokens = 1024;
+// Warps that share a token's heads: more of them wait less for the heads, but
+// each computes the token's angles.  A token of at least kRotLong passes (a pass
+// is 32 lanes' heads) is shared by two warps, by four in a call of at most
+// kRotFew tokens; a shorter one by two in such a call.  32 + 8 heads of 128 (12
+// passes), 1 / 2 / 4 warps: 128 tokens 5.1 / 3.6 / 3.1 us, 2048 tokens 11.6 /
+// 10.7 / 12.2 us, 8192 tokens 33.6 / 33.2 / 37.7 us; 16 + 4 heads of 64 (4
+// passes): 2.7 / 2.4 / 2.4, 3.5 / 4.4 / 6.2 and 11.3 / 14.6 / 21.9 us.
+constexpr int kRotLong = 8, kRotFew = 512;
 
 // frac(f / 2 pi) * 2^64 of a finite f with |f| < 2^31: the 53-bit mantissa times
 // 2^66 / (2 pi), shifted by the exponent; below 2^-64 of a turn exact.
@@ -170,15 +173,14 @@ __device__ __forceinline__ void store_fp8(unsigned char* codes_at, float* scale_
   if (l == 0) *scale_at = sc;
 }
 
-// Warps of a token: `split` of them share its heads (1, or 4 with few tokens).
-// DEPTH passes of a warp have their loads in flight together.  The bf16 cache
-// takes three with 80 registers a thread (4099 tokens of 16 + 4 heads of 64,
-// half rotated: 5.9 us, 4.3 TB/s; two: 6.2), the 8-bit cache, whose codes cost
-// more instructions, two with 64 registers (8191 tokens of 32 + 8 heads of 128:
-// 34.7 us, 5.3 TB/s; three: 36.6).
+// 2^split_log2 warps share a token's heads.  DEPTH passes of a warp have their
+// loads in flight together: three with the bf16 cache (4099 tokens of 16 + 4
+// heads of 64, half rotated: 5.9 us, 4.3 TB/s; two: 6.2), two with the 8-bit
+// cache, whose codes cost more instructions, at eight CTAs an SM (8191 tokens of
+// 32 + 8 heads of 128: 34.7 us, 5.3 TB/s; three: 36.6).
 template <int D, bool F8, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
-    rotary_cache_kernel(const RotaryArgs p, int split) {
+    rotary_cache_kernel(const RotaryArgs p, int split_log2) {
   constexpr int DEPTH = F8 ? 2 : 3;
   constexpr int LPR = D / 16;      // lanes of a head: 16 elements each
   constexpr int HEADS = 32 / LPR;  // heads of a pass of the warp
@@ -186,12 +188,13 @@ __global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
   // (read from lane 0, so that what follows from it is known to be the warp's)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kRotWarps + warp;
-  const int64_t t = split == 1 ? unit : unit / kRotWarps;
+  const int64_t t = unit >> split_log2;
+  const int split = 1 << split_log2;
   after_prior_kernels();
   if (t >= p.num_tokens) return;
   const int step = HEADS * split;
   const int l = lane % LPR;
-  const int h_lane = (split == 1 ? 0 : warp * HEADS) + lane / LPR;  // head of the first pass
+  const int h_lane = (int)(unit & (split - 1)) * HEADS + lane / LPR;  // head of the first pass
   const bool rot = l < p.rotary_dim / 16;
   // this lane's two chunks of 8 elements
   int ca = 2 * l, cb = 2 * l + 1;
@@ -277,8 +280,10 @@ __global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
 
 template <int D, bool F8>
 static cudaError_t launch_rotary_t(const RotaryArgs& p, cudaStream_t stream) {
-  const int split = p.num_tokens <= kRotSplitTokens ? kRotWarps : 1;
-  const int64_t warps = (int64_t)p.num_tokens * split;
+  constexpr int HEADS = 32 / (D / 16);
+  const int passes = (p.n_q + HEADS - 1) / HEADS + 2 * ((p.n_kv + HEADS - 1) / HEADS);
+  const int split = (passes >= kRotLong ? 1 : 0) + (p.num_tokens <= kRotFew ? 1 : 0);
+  const int64_t warps = (int64_t)p.num_tokens << split;
   const unsigned grid = (unsigned)((warps + kRotWarps - 1) / kRotWarps);
   return launch_early(p.interleaved ? rotary_cache_kernel<D, F8, true>
                                     : rotary_cache_kernel<D, F8, false>,

@@ -53,6 +53,9 @@ CASES = [
     (257, 5, 5, 64, 48, 3, False, 2 ** 31 - 1, False, 32),
     (31, 1, 1, 128, 16, 1, False, 100, True, 48),
     (9, 8, 8, 64, 0, 1, False, 100, False, 16),
+    (601, 32, 8, 128, 128, 3, False, 1 << 20, True, 16),
+    (703, 5, 1, 64, 64, 2, True, 9999, False, 16),
+    (1, 64, 8, 128, 64, 2, True, 9999, True, 32),
 ]
 
 
