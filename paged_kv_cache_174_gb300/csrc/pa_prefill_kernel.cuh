@@ -707,12 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_out;
         const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
-        if constexpr (F8) {
-          // 8-bit cache: lane i holds the tile's page i (the pool's page, -1 for
-          // none), looked up a tile ahead; a page's codes and row scales come by
-          // plain loads while the page before it is converted.  (One page's code,
-          // looped: all of a tile's unrolled would crowd the other warps out of
-          // the instruction cache.)
+        if constexpr (F8 && QT == 2) {
+          // 8-bit cache, two query tiles: lane i holds the tile's page i (the pool's page, -1 for
+          // none), looked up a tile ahead; pages come by plain loads.
           constexpr int CPR = D / 16;        // 16-code chunks per row
           constexpr int RPJ = 32 / CPR;      // rows per load of the warp
           constexpr int JPP = kBlock / RPJ;  // loads per page
@@ -747,8 +744,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             return (b << p.block_shift) +
                    (U.template page<WIN>(e) & ((1 << p.block_shift) - 1));
           };
-          uint4 w8[JPP], n8[JPP];
-          float sc = 0.f, nsc = 0.f;
           auto load = [&](int page, uint4 (&w)[JPP], float& scale) {
             if (page < 0) return;
             const int64_t at = (int64_t)page * page_bytes;
@@ -757,6 +752,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < JPP; ++j)
               w[j] = __ldg(reinterpret_cast<const uint4*>(lane_codes + at + j * row_step));
           };
+          // page i of the tile into stage st, as f16(code * f16(scale))
+          auto convert = [&](uint32_t st, int i, const uint4 (&w)[JPP], float scale) {
+            unsigned char* page_at =
+                ring + st * KV_BYTES + lane_at + i * (k_warp ? kBlock * 128 : V_PAGE);
+#pragma unroll
+            for (int j = 0; j < JPP; ++j) {
+              const int r = j * RPJ + lane / CPR;
+              uint32_t h[8];  // the chunk's 16 values, f16
+              const float row_scale = __shfl_sync(0xffffffffu, scale, r);
+              const uint32_t sc2 = f16x2_from_floats(row_scale, row_scale);
+              f16x4_from_e4m3x4_scaled(w[j].x, sc2, h[0], h[1]);
+              f16x4_from_e4m3x4_scaled(w[j].y, sc2, h[2], h[3]);
+              f16x4_from_e4m3x4_scaled(w[j].z, sc2, h[4], h[5]);
+              f16x4_from_e4m3x4_scaled(w[j].w, sc2, h[6], h[7]);
+              const uint32_t at = sw128_chunk(r, c8);
+              *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
+                  make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          };
+          // the stage's last reader released it (as below)
+          auto wait_stage = [&]() {
+            if (lane == 0 && c >= (int)nst)
+              mbar_wait(smem_addr(&empty[pos.stage]), pos.phase ^ 1u, p.err, abort_flag);
+            __syncwarp();
+          };
+          // A page at a time, the next one's loads in flight while one is converted,
+          // in a loop of one page's code: with all of a tile's unrolled the softmax
+          // warps waited for instructions (1024 rows, a 4096-token window: 122 us,
+          // 96 this way; two pages ahead 105).  A single query tile's producers
+          // load a tile's pages at once, below: they have more of their time to
+          // wait in, and a cold cache costs them less that way (a 512-row chunk at
+          // 3584, L2 flushed: 77 us, a page at a time 89; L2 warm 68 and 68).
+          uint4 w8[JPP], n8[JPP];
+          float sc = 0.f, nsc = 0.f;
 #pragma unroll
           for (int j = 0; j < JPP; ++j) w8[j] = n8[j] = make_uint4(0u, 0u, 0u, 0u);
           int phys = page_of(U.kt0, entry_of(U.kt0));
@@ -767,34 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             entry = entry_of(kt + 2);
             const uint32_t st = pos.stage;
 #pragma unroll 1
-            for (int i = 0; i < npg; ++i) {
-              load(__shfl_sync(0xffffffffu, i + 1 < npg ? phys : phys_next, i + 1 < npg ? i + 1 : 0),
-                   n8, nsc);
-              if (i == 0) {
-                // the stage's last reader released it (as below)
-                if (lane == 0 && c >= (int)nst)
-                  mbar_wait(smem_addr(&empty[st]), pos.phase ^ 1u, p.err, abort_flag);
-                __syncwarp();
-              }
-              if (__shfl_sync(0xffffffffu, phys, i) >= 0) {  // else there is no page
-                unsigned char* page_at =
-                    ring + st * KV_BYTES + lane_at + i * (k_warp ? kBlock * 128 : V_PAGE);
-#pragma unroll
-                for (int j = 0; j < JPP; ++j) {
-                  const int r = j * RPJ + lane / CPR;
-                  uint32_t h[8];  // the chunk's 16 values, f16
-                  const float row_scale = __shfl_sync(0xffffffffu, sc, r);
-                  const uint32_t sc2 = f16x2_from_floats(row_scale, row_scale);
-                  f16x4_from_e4m3x4_scaled(w8[j].x, sc2, h[0], h[1]);
-                  f16x4_from_e4m3x4_scaled(w8[j].y, sc2, h[2], h[3]);
-                  f16x4_from_e4m3x4_scaled(w8[j].z, sc2, h[4], h[5]);
-                  f16x4_from_e4m3x4_scaled(w8[j].w, sc2, h[6], h[7]);
-                  const uint32_t at = sw128_chunk(r, c8);
-                  *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                  *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
-                      make_uint4(h[4], h[5], h[6], h[7]);
-                }
-              }
+            for (int i = 0; i < PG; ++i) {
+              load(__shfl_sync(0xffffffffu, i + 1 < PG ? phys : phys_next, (i + 1) % PG), n8, nsc);
+              if (i == 0) wait_stage();
+              if (__shfl_sync(0xffffffffu, phys, i) >= 0) convert(st, i, w8, sc);
 #pragma unroll
               for (int j = 0; j < JPP; ++j) w8[j] = n8[j];
               sc = nsc;
@@ -807,7 +813,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+        // 8-bit cache: the tile's table entries are fetched a tile ahead
+        auto table_entry = [&](int kt, int i) {
+          const int e = kt * kPagesPerTile + pg_lo + i;
+          if (pg_lo + i >= pg_hi || e >= U.pages) return 0;
+          return __ldg(table + (U.template page<WIN>(e) >> p.block_shift));
+        };
+        int next[4];
+        if constexpr (F8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next[i] = table_entry(U.kt0, i);
+        }
         for (int kt = U.kt0; kt < U.kt1; ++kt, ++c) {
+          int entry[4];
+          if constexpr (F8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              entry[i] = next[i];
+              next[i] = kt + 1 < U.kt1 ? table_entry(kt + 1, i) : 0;
+            }
+          }
           // per page: -1 (nothing to load), 0 (cached rows: the cache), 1
           // (new rows only: k_new / v_new), 2 (both: the cache, then the new
           // rows copied over)
@@ -826,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bytes += NH * (kBlock * 128);
                 continue;
               }
-              const int b = __ldg(table + (lp >> p.block_shift));
+              const int b = F8 ? entry[i] : __ldg(table + (lp >> p.block_shift));
               if (b < 0 || b >= p.num_blocks) {
                 if (lane == 0) flag_error(p.err, DEVERR_BOUNDS);
               } else {
@@ -837,6 +862,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const uint32_t st = pos.stage;
+          if constexpr (F8) {
+            // 8-bit cache: this warp's pages as codes and row scales, by
+            // plain loads issued before the stage is free (their latency
+            // overlaps the wait); lane j-th chunk: 16 codes of one row
+            constexpr int CPR = D / 16;                  // chunks per row
+            constexpr int RPJ = 32 / CPR;                // rows per load of the warp
+            constexpr int JPP = kBlock / RPJ;            // loads per page
+            constexpr int NJ = PG * JPP;                 // chunks per lane
+            const uint8_t* pages = k_warp ? p.k_codes : p.v_codes;
+            const int64_t page_bytes = fp8_page_bytes(p.n_kv, D);
+            // this lane's chunk of the page's first rows, and the scale of the
+            // page's row lane % 16 (handed to the row's lanes by a shuffle)
+            const uint8_t* lane_codes =
+                pages + ((lane / CPR) * p.n_kv + U.g) * D + (lane % CPR) * 16;
+            const uint8_t* lane_scales =
+                pages + fp8_scales_offset(p.n_kv, D) + ((lane % kBlock) * p.n_kv + U.g) * 4;
+            uint4 w8[NJ];
+            float sc[PG];
+#pragma unroll
+            for (int i = 0; i < PG; ++i) {
+              const int64_t page = (int64_t)phys[i] * page_bytes;
+              sc[i] = 0.f;
+              if (phys[i] >= 0) sc[i] = __ldg(reinterpret_cast<const float*>(lane_scales + page));
+#pragma unroll
+              for (int j = 0; j < JPP; ++j) {
+                w8[i * JPP + j] = make_uint4(0u, 0u, 0u, 0u);
+                if (phys[i] >= 0)
+                  w8[i * JPP + j] = __ldg(reinterpret_cast<const uint4*>(
+                      lane_codes + page + j * RPJ * p.n_kv * D));
+              }
+            }
+            // the stage's last reader released it (as below)
+            if (lane == 0 && c >= (int)nst)
+              mbar_wait(smem_addr(&empty[st]), pos.phase ^ 1u, p.err, abort_flag);
+            __syncwarp();
+            // where the chunk's 16 values go, as elements 16 c16 .. +15 of row r:
+            // half c16 / 4, 16-byte chunks 2 (c16 % 4) and the next of that half's
+            // 128-byte row (the next is the first's address with bit 4 flipped)
+            const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
+            unsigned char* lane_at =
+                ring + st * KV_BYTES + (c16 >> 2) * (k_warp ? HALF : kBlock * 128);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const int pi = j / JPP;
+              if (phys[pi] < 0) continue;  // no page there: nothing is read from it
+              const int r = (j % JPP) * RPJ + lane / CPR;
+              uint32_t h[8];  // the chunk's 16 values, f16
+              const float row_scale = __shfl_sync(0xffffffffu, sc[pi], r);
+              const uint32_t sc2 = f16x2_from_floats(row_scale, row_scale);
+              f16x4_from_e4m3x4_scaled(w8[j].x, sc2, h[0], h[1]);
+              f16x4_from_e4m3x4_scaled(w8[j].y, sc2, h[2], h[3]);
+              f16x4_from_e4m3x4_scaled(w8[j].z, sc2, h[4], h[5]);
+              f16x4_from_e4m3x4_scaled(w8[j].w, sc2, h[6], h[7]);
+              const uint32_t at = sw128_chunk(r, c8);
+              unsigned char* page_at = lane_at + (pg_lo + pi) * (k_warp ? kBlock * 128 : V_PAGE);
+              *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
+                  make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&full[st]));
+            pos.next(nst);
+            continue;
+          }
           // the stage's last reader released it: one commit per use, and the
           // next commit needs this load, so never two completions behind
           if (lane == 0 && c >= (int)nst)
