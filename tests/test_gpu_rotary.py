@@ -263,3 +263,29 @@ def test_quotients_are_those_of_the_plain_scatter():
     a, c = (ops.fp8_cache_views(x, nkv, d) for x in (a, c))
     assert torch.equal(a[1], c[1])
     assert torch.equal(torch.where(a[0] == 0x80, 0, a[0]), torch.where(c[0] == 0x80, 0, c[0]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_zeros_and_non_finite_values_as_the_plain_scatter(d):
+    """Signed zeros, infinities and NaN among the values, and among keys that no
+    rotation touches: the plain 8-bit scatter's bytes."""
+    g = torch.Generator().manual_seed(5)
+    T, nkv = 333, 3
+    x = torch.randn(T, nkv, d, generator=g)
+    pick = torch.rand(T, nkv, d, generator=g)
+    x[pick < 0.3] = 0.0
+    x[pick < 0.15] = -0.0
+    x[5, 0], x[6, 1] = -0.0, 0.0  # rows of zeros alone
+    x[100:200][pick[100:200] > 0.99] = float("nan")
+    x[200:300][pick[200:300] > 0.99] = -float("inf")
+    x = x.bfloat16().cuda()
+    q = torch.zeros(T, 3, d, dtype=torch.bfloat16, device="cuda")
+    slots = torch.randperm(352, generator=g)[:T].int().cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    a, b = ops.empty_fp8_cache(22, 16, nkv, d)
+    c, e = ops.empty_fp8_cache(22, 16, nkv, d)
+    ops.rotary_reshape_and_cache_fp8(
+        q, x, x, pos, torch.ones(0, dtype=torch.float64, device="cuda"), a, b, slots)
+    ops.reshape_and_cache_fp8(x, x, c, e, slots)
+    ops.check_device_errors()
+    assert torch.equal(a, c) and torch.equal(b, e)
