@@ -164,3 +164,36 @@ def test_captured_decode_steps(fp8):
         for name in ("tables_d", "count_d", "lens_d"):
             assert torch.equal(getattr(cap, name), getattr(eager, name))
     ops.check_device_errors()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_captured_after_copies_and_other_streams(fp8):
+    """A captured step whose inputs come by copies on its own stream and by
+    kernels on another that it joins: replayed, it gives what it gave eagerly."""
+    a, b = Loop(5, window=50, sinks=3, fp8=fp8, seed=7), Loop(5, window=50, sinks=3, fp8=fp8, seed=7)
+    for l in (a, b):
+        l.step([20, 1, 300, 16, 47])
+    new = torch.tensor([1, 3, 70, 0, 2], dtype=torch.int32, device="cuda")
+    T = 76
+    source = a.qkv(T)
+    want = a.layer(new, T, 70, source, 400)[-1]
+    held, into, half = torch.empty_like(new), torch.empty_like(source), source * 0.5
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    start = [x.clone() for x in (b.lens_d, b.tables_d, b.count_d, b.kc, b.vc)]
+    with torch.cuda.graph(graph):
+        held.copy_(new)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.add(half, half, out=into)
+        for x, y in zip((b.lens_d, b.tables_d, b.count_d, b.kc, b.vc), start):
+            x.copy_(y)
+        here.wait_stream(side)
+        got = b.layer(held, T, 70, into, 400)[-1]
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        ops.check_device_errors()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(b.lens_d, a.lens_d) and torch.equal(b.count_d, a.count_d)
