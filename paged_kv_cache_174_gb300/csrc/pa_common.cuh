@@ -25,6 +25,14 @@ __device__ __forceinline__ void after_prior_kernels() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// For a kernel that may overlap the one before it and has no need of its results:
+// called by a thread of its first block before that block ends, it keeps the grid
+// from completing before the earlier one has, so that whoever waits for this
+// grid has waited for both.
+__device__ __forceinline__ void complete_after_prior() {
+  asm volatile("griddepcontrol.wait;");
+}
+
 __device__ __forceinline__ unsigned long long global_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
