@@ -123,13 +123,11 @@ __device__ __forceinline__ void turn(Piece& x, const Angles& t) {
 // x * r is exact in one FMA, and adding it times r gives the correctly rounded
 // quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990), as long as no product leaves the normal range.
-// The residual is taken as y d - x, whose zero keeps the sign of x = -0 through
-// the last step (as x - y d it would come out +0); negating x is free in an FMA
-// of one value, not of a pair.
-__device__ __forceinline__ float2 quotient(float2 x, float2 d, float2 r, float2 minus_r) {
+// The residual is rounded down, which being exact it only notices as the sign of a
+// zero: -0 leaves the zero it is added to as it is, where +0 would turn -0 to +0.
+__device__ __forceinline__ float2 quotient(float2 x, float2 minus_d, float2 r) {
   const float2 y = __fmul2_rn(x, r);
-  const float2 over = make_float2(__fmaf_rn(y.x, d.x, -x.x), __fmaf_rn(y.y, d.y, -x.y));
-  return __ffma2_rn(over, minus_r, y);
+  return __ffma2_rn(__ffma2_rd(y, minus_d, x), r, y);
 }
 
 // Store a row's piece to the 8-bit cache: scale = row max / 448 (1 for an
@@ -151,13 +149,12 @@ __device__ __forceinline__ void store_fp8(unsigned char* codes_at, float* scale_
   if (!on) return;
   const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
   const float inv = __frcp_rn(sc);
-  const float2 d2 = make_float2(sc, sc), r2 = make_float2(inv, inv);
-  const float2 m2 = make_float2(-inv, -inv);
+  const float2 d2 = make_float2(-sc, -sc), r2 = make_float2(inv, inv);
   float2 y[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    y[e] = quotient(x.a[e], d2, r2, m2);
-    y[4 + e] = quotient(x.b[e], d2, r2, m2);
+    y[e] = quotient(x.a[e], d2, r2);
+    y[4 + e] = quotient(x.b[e], d2, r2);
   }
   // a divider near the ends of fp32's range takes the plain division; elements
   // so small that their residual underflows have the code 0 either way
