@@ -660,7 +660,8 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
     block of the pool), ``free_count`` [1] is updated in place unless
     ``free_count_out`` is given.  Returns (seq_lens [S], query_start_loc
     [S + 1], slot_mapping [num_tokens], positions [num_axes, num_tokens]); each
-    may be passed in to be written (seq_lens may be context_lens itself).
+    may be passed in to be written (seq_lens may be context_lens itself); those
+    made here may share one allocation.
     """
     if stream is None:
         r = (_binding or _load_binding()).build_step(

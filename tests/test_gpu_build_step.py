@@ -210,3 +210,37 @@ def test_either_way_into_the_library():
         for num in (int, np.int64):
             _compare(_run(ctx, new, tables, free, count, off, num(16), num(T), num(2), **kw), want)
     ops.check_device_errors()
+
+
+@pytest.mark.parametrize("given", [(), (0,), (1, 3), (0, 1, 2, 3)])
+def test_outputs_made_by_the_call_are_apart(given):
+    """Whichever outputs the caller passes, the others are contiguous tensors
+    that writing to one, and dropping the rest, leaves as they are."""
+    ctx, new, tables, free, count, offsets = _case(4, 7, 90, 30, 16)
+    T, axes = int(new.sum()) + 3, 3
+    want = R.build_step(ctx, new, tables, free, count, 16, T, axes, offsets)
+    names = ("seq_lens", "query_start_loc", "slot_mapping", "positions")
+    shapes = ((7,), (8,), (T,), (axes, T))
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            mine = {names[i]: torch.full(shapes[i], -9, dtype=torch.int32, device="cuda")
+                    for i in given}
+            args = (_i32(ctx), _i32(new), _i32(tables), _i32(free), _i32([count]))
+            out = ops.build_step(*args, block_size=16, num_tokens=T, num_axes=axes,
+                                 position_offsets=_i32(offsets), **mine)
+            ops.check_device_errors()
+            for i, x in enumerate(out):
+                assert x.is_contiguous() and x.dtype is torch.int32 and tuple(x.shape) == shapes[i]
+                assert (x is mine[names[i]]) if i in given else x.data_ptr() % 16 == 0
+            for i, x in enumerate(out):
+                kept = [y.clone() for y in out]
+                x.fill_(-5)
+                for j, y in enumerate(out):
+                    assert j == i or torch.equal(y, kept[j])
+                x.copy_(kept[i])
+            last = out[3]
+            rest = [x.cpu().numpy() for x in out[:3]]
+            del out, mine, x, y
+            torch.empty(1 << 16, dtype=torch.int32, device="cuda").fill_(77)
+            for got, w in zip(rest + [last.cpu().numpy()], want[1:5]):
+                assert np.array_equal(got, w)
