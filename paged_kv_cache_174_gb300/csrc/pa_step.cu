@@ -33,6 +33,16 @@ constexpr int kPlanWarps = 32;  // at most
 // cluster of eight of 1024.
 constexpr int kPlanOneCta = 1024;
 
+// What a block holds in shared memory beside the requests' words.
+struct PlanShared {
+  long long warp_t[kPlanWarps], warp_b[kPlanWarps];
+  int served_t, served_b;
+};
+// Dynamic shared memory that a launch may take without asking for more: a block's
+// 48 KB hold its static part and the padding between the two as well.
+constexpr size_t kPlanSmemPlain = 47 * 1024;
+static_assert(sizeof(PlanShared) + 128 <= 48 * 1024 - kPlanSmemPlain, "");
+
 // The last index s in [0, n) with pre[s] <= x (pre[0] = 0 <= x, non-decreasing).
 __device__ __forceinline__ int owner_of(const int* pre, int n, int x) {
   int lo = 0, hi = n;
@@ -66,8 +76,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
   int* ctx_s = smem_i;                     // [num_seqs]
   int* tok_s = ctx_s + p.num_seqs;         // [num_seqs + 1] exclusive prefix of new tokens
   int* blk_s = tok_s + p.num_seqs + 1;     // [num_seqs + 1] exclusive prefix of new blocks
-  __shared__ long long warp_t[kPlanWarps], warp_b[kPlanWarps];
-  __shared__ int served_t, served_b;
+  __shared__ PlanShared B;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int threads = blockDim.x, warps = threads >> 5;
   const int me = blockIdx.x * threads + tid, all = gridDim.x * threads;
@@ -78,7 +87,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
   const bool count_ok = raw_count >= 0 && raw_count <= p.num_blocks;
   const int count = count_ok ? raw_count : 0;
   bool bad = !count_ok;
-  if (tid == 0) served_t = 0, served_b = 0, tok_s[0] = 0, blk_s[0] = 0;
+  if (tid == 0) B.served_t = 0, B.served_b = 0, tok_s[0] = 0, blk_s[0] = 0;
 
   bool cut = false;                // a request of this thread was not served
   long long run_t = 0, run_b = 0;  // totals of the chunks before this one
@@ -98,10 +107,10 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
     }
     long long it = warp_scan(nt, lane), ib = warp_scan(nb, lane);
     if (s0) __syncthreads();  // the last chunk's warp totals have been read
-    if (lane == 31) warp_t[warp] = it, warp_b[warp] = ib;
+    if (lane == 31) B.warp_t[warp] = it, B.warp_b[warp] = ib;
     __syncthreads();
-    const long long wt = warp_scan(lane < warps ? warp_t[lane] : 0, lane);
-    const long long wb = warp_scan(lane < warps ? warp_b[lane] : 0, lane);
+    const long long wt = warp_scan(lane < warps ? B.warp_t[lane] : 0, lane);
+    const long long wb = warp_scan(lane < warps ? B.warp_b[lane] : 0, lane);
     const int before = warp > 0 ? warp - 1 : 0;
     const long long pt = __shfl_sync(0xffffffffu, wt, before);
     const long long pb = __shfl_sync(0xffffffffu, wb, before);
@@ -114,8 +123,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
       tok_s[s + 1] = (int)it;
       blk_s[s + 1] = (int)ib;
       if ((ball >> lane) == 1u) {  // the warp's last served request
-        atomicMax(&served_t, (int)it);
-        atomicMax(&served_b, (int)ib);
+        atomicMax(&B.served_t, (int)it);
+        atomicMax(&B.served_b, (int)ib);
       }
     } else if (mine) {
       tok_s[s + 1] = -1;  // past the served prefix: the totals, below
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
     }
   }
   const int any_cut = __syncthreads_or(cut);
-  const int total_t = served_t, total_b = served_b;
+  const int total_t = B.served_t, total_b = B.served_b;
   if (any_cut) {
     bad |= cut;
     for (int s = tid; s < p.num_seqs; s += threads)
@@ -175,7 +184,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) build_step_kernel(const StepP
 
 cudaError_t launch_build_step(const StepPlanArgs& p, cudaStream_t stream) {
   const size_t smem = ((size_t)3 * p.num_seqs + 2) * sizeof(int);
-  if (smem > 48 * 1024) {
+  if (smem > kPlanSmemPlain) {
     // (always the most any call takes, so that calls on other threads agree)
     cudaError_t e = cudaFuncSetAttribute(build_step_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -244,3 +244,17 @@ def test_outputs_made_by_the_call_are_apart(given):
             torch.empty(1 << 16, dtype=torch.int32, device="cuda").fill_(77)
             for got, w in zip(rest + [last.cpu().numpy()], want[1:5]):
                 assert np.array_equal(got, w)
+
+
+@pytest.mark.parametrize("S", [4051, 4052, 4095, 4096, 16384])
+@pytest.mark.parametrize("pad", [0, 20000])
+def test_as_many_requests_as_the_call_takes(S, pad):
+    """Past a block's 48 KB of shared memory, its fixed part counted: 12 bytes a
+    request beside it reach them at 4052 requests."""
+    ctx, new, tables, free, count, off = _case(S, S, 60, 1, 16, zero=0.9)
+    T = int(new.sum()) + pad
+    want = R.build_step(ctx, new, tables, free, count, 16, T, 1, off)
+    got = _run(ctx, new, tables, free, count, off, 16, T, 1)
+    _errors(want[-1])
+    assert not want[-1]
+    _compare(got, want)
