@@ -40,10 +40,14 @@ constexpr int kRotWarps = kRotThreads / 32;
 // passes): 2.7 / 2.4 / 2.4, 3.5 / 4.4 / 6.2 and 11.3 / 14.6 / 21.9 us.
 constexpr int kRotLong = 8, kRotFew = 512;
 
-// frac(f / 2 pi) * 2^64 of a finite f with |f| < 2^31: the 53-bit mantissa times
-// 2^66 / (2 pi), shifted by the exponent; below 2^-64 of a turn exact.
+// frac(f / 2 pi) * 2^64 of a finite f with |f| < 2^31, to within one: the 53-bit
+// mantissa times 128 bits of 1 / (2 pi), of which those that whole turns take are
+// shifted out (M. Payne and R. Hanek, "Radian reduction for trigonometric
+// functions", 1983).  64 bits of 1 / (2 pi) would leave an error of |f| 2^-66 turns,
+// times the position.
 __device__ __forceinline__ unsigned long long turn_fraction(double f, bool& bad) {
-  constexpr unsigned long long kInvTwoPi66 = 0xA2F9836E4E441529ull;  // floor(2^66 / (2 pi))
+  // floor(2^130 / (2 pi)), from Machin's formula for pi in integers
+  constexpr unsigned long long kInvHi = 0xA2F9836E4E441529ull, kInvLo = 0xFC2757D1F534DDC0ull;
   const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
   const int e = (int)((bits >> 52) & 0x7ff) - 1023;
   if (e >= 31) {  // also infinities and NaN
@@ -51,7 +55,11 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f, bool& bad)
     return 0;
   }
   const unsigned long long m = (bits & 0xfffffffffffffull) | (e > -1023 ? 1ull << 52 : 0);
-  const unsigned long long hi = __umul64hi(m, kInvTwoPi66), lo = m * kInvTwoPi66;
+  // the product's upper 128 of 192 bits (the shift drops 64 and more)
+  unsigned long long hi = __umul64hi(m, kInvHi), lo = m * kInvHi;
+  const unsigned long long below = __umul64hi(m, kInvLo);
+  lo += below;
+  hi += lo < below ? 1 : 0;
   const int shift = 54 - (e > -1023 ? e : -1022);  // >= 24
   unsigned long long t;
   if (shift < 64)

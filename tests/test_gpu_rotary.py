@@ -1,6 +1,8 @@
 """Rotary positions with the slot scatter on the GPU against 64-bit rotation:
 both caches, several axes, pairings, partial rotation, far and negative
 positions, strided inputs, skipped slots, in-place use."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -289,3 +291,62 @@ def test_zeros_and_non_finite_values_as_the_plain_scatter(d):
     ops.reshape_and_cache_fp8(x, x, c, e, slots)
     ops.check_device_errors()
     assert torch.equal(a, c) and torch.equal(b, e)
+
+
+def _two_pi():
+    """2 pi as a fraction, to 300 bits (Machin's formula)."""
+    def arctan_of_inverse(n, one):
+        term = total = one // n
+        k, sign = 3, -1
+        while term:
+            term //= n * n
+            total += sign * (term // k)
+            k, sign = k + 2, -sign
+        return total
+    one = 1 << 320
+    return Fraction(8 * (4 * arctan_of_inverse(5, one) - arctan_of_inverse(239, one)), one)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_any_frequency_at_any_position(fp8):
+    """Frequencies of both signs up to the largest, at positions up to both ends of
+    int32: (1, 0) turned is (cos, sin) of an angle that whole fractions reduce."""
+    freqs = [1.0, 0.37, 3.7, -3.7, 4.1, 10000.1, -7777.7, 1e6 + 0.1, -1e8 - 0.3, 3e8 + 0.7,
+             2.0 ** 30 + 0.3, -(2.0 ** 30) - 0.9, 2.0 ** 31 - 0.7, -(2.0 ** 31) + 0.4,
+             2.0 ** -40, -1e-300]
+    positions = [0, 1, -1, 77, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -2 ** 30 - 7, 123456789,
+                 1999999973]
+    d, T = 64, len(positions)
+    f = np.array(freqs * 2)
+    tau = _two_pi()
+    theta = np.empty((T, d // 2))
+    for t, p in enumerate(positions):
+        for i, x in enumerate(f):
+            turns = p * Fraction(float(x)) / tau
+            turns -= round(turns)
+            theta[t, i] = float(turns * tau)
+    q = torch.zeros(T, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., :d // 2] = 1.0
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
+    if fp8:
+        kc, vc = ops.empty_fp8_cache(1, 16, 1, d)
+        call = ops.rotary_reshape_and_cache_fp8
+    else:
+        kc, vc = (torch.zeros(1, 16, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        call = ops.rotary_reshape_and_cache
+    out = call(q, q, q, pos, torch.from_numpy(f).cuda(), kc, vc, slots)
+    ops.check_device_errors()
+    ref = np.concatenate([np.cos(theta), np.sin(theta)], -1)[:, None]
+    size = np.ones_like(ref)
+    _check_bf16(_f64(out), ref, size, "q")
+    if fp8:
+        codes, scales = ops.fp8_cache_views(kc, 1, d)
+        got = _f64(codes.view(torch.float8_e4m3fn)).reshape(16, 1, d)[:T] \
+            * _f64(scales).reshape(16, 1)[:T, :, None]
+        # half a step of a code (a subnormal one: 2^-10 of the scale, which is at
+        # most 1 / 448), and as above for the turn
+        tol = np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 / 448) * (1 + 2.0 ** -10) + 2.0 ** -17
+        assert (np.abs(got - ref) <= tol).all()
+    else:
+        _check_bf16(_f64(kc).reshape(16, 1, d)[:T], ref, size, "k")
