@@ -307,7 +307,11 @@ int pa_swap_in(pa_bf16 *k_cache, pa_bf16 *v_cache, int32_t num_blocks, int32_t b
  * f16(code * f16(scale)) in shared memory (codes exact in f16, one rounding
  * of the scale and one of the product), and runs
  * its tcgen05 products on f16 operands: q * scale * log2(e) and p rounded
- * to f16.  head_dim is 64 or 128; the same shapes as the bf16 cache.
+ * to f16.  The row maxima this is good for: in the prefill kernel 1.1e-4 to
+ * 65504 (values below 6.1e-5, f16's normal range, are right to 2^-23 whatever
+ * their row; past 65504 they are infinite); in the decode kernel any for keys,
+ * up to 5e4 for values (p * value scale * 2^9 is right to 2^-25 below f16's
+ * normal range).  head_dim is 64 or 128; the same shapes as the bf16 cache.
  *
  * pa_fp8_page_bytes: the page size above (0 for a non-positive argument).
  *

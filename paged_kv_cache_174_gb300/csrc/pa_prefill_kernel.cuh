@@ -67,6 +67,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -297,15 +298,30 @@ __device__ __forceinline__ uint32_t f16x2_from_bf16x2_mul(uint32_t w, float m) {
   return f16x2_from_floats(f.x * m, f.y * m);
 }
 
-// Four E4M3 codes times a row scale given as an f16 pair (both halves the
-// scale), as two f16 pairs: each value is f16(code * f16(scale)) (the codes
-// convert exactly; one packed multiply per pair, round to nearest).
-__device__ __forceinline__ void f16x4_from_e4m3x4_scaled(uint32_t w, uint32_t sc2, uint32_t& lo,
-                                                         uint32_t& hi) {
-  uint32_t a, b;
-  f16x2x2_from_e4m3x4(w, a, b);
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(sc2));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(sc2));
+// A row's 16 E4M3 codes times its scale, as eight f16 pairs: each value is
+// f16(code * f16(scale)) (the codes convert exactly; one rounding of the scale and
+// one of the product).  A scale below f16's normal range (a row maximum below
+// 0.027) would lose bits in its rounding, and below 2^-25 all of them: for a page
+// that holds one (small) the codes are taken times 2^-8 and the scales times 2^8,
+// both exact, which keeps the scale's bits down to a row maximum of 1.1e-4 and
+// leaves the other rows' values as they are.  Values below f16's normal range,
+// 6.1e-5, are right to 2^-25.
+constexpr float kSmallScale = 6.103515625e-5f;  // 2^-14
+__device__ __forceinline__ void f16x16_from_e4m3x16_scaled(const uint4& w, float scale, bool small,
+                                                           uint32_t (&h)[8]) {
+  f16x2x2_from_e4m3x4(w.x, h[0], h[1]);
+  f16x2x2_from_e4m3x4(w.y, h[2], h[3]);
+  f16x2x2_from_e4m3x4(w.z, h[4], h[5]);
+  f16x2x2_from_e4m3x4(w.w, h[6], h[7]);
+  if (small) {
+    scale *= 256.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(0x1c001c00u));  // 2^-8
+  }
+  const uint32_t sc2 = f16x2_from_floats(scale, scale);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(sc2));
 }
 
 // Output rows through shared memory (sliding window).  A thread holds 32 values
@@ -756,16 +772,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto convert = [&](uint32_t st, int i, const uint4 (&w)[JPP], float scale) {
             unsigned char* page_at =
                 ring + st * KV_BYTES + lane_at + i * (k_warp ? kBlock * 128 : V_PAGE);
+            const bool small = __any_sync(0xffffffffu, scale < kSmallScale);
 #pragma unroll
             for (int j = 0; j < JPP; ++j) {
               const int r = j * RPJ + lane / CPR;
               uint32_t h[8];  // the chunk's 16 values, f16
-              const float row_scale = __shfl_sync(0xffffffffu, scale, r);
-              const uint32_t sc2 = f16x2_from_floats(row_scale, row_scale);
-              f16x4_from_e4m3x4_scaled(w[j].x, sc2, h[0], h[1]);
-              f16x4_from_e4m3x4_scaled(w[j].y, sc2, h[2], h[3]);
-              f16x4_from_e4m3x4_scaled(w[j].z, sc2, h[4], h[5]);
-              f16x4_from_e4m3x4_scaled(w[j].w, sc2, h[6], h[7]);
+              f16x16_from_e4m3x16_scaled(w[j], __shfl_sync(0xffffffffu, scale, r), small, h);
               const uint32_t at = sw128_chunk(r, c8);
               *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
               *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
@@ -883,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < PG; ++i) {
               const int64_t page = (int64_t)phys[i] * page_bytes;
-              sc[i] = 0.f;
+              sc[i] = 1.f;  // (no page: nothing small)
               if (phys[i] >= 0) sc[i] = __ldg(reinterpret_cast<const float*>(lane_scales + page));
 #pragma unroll
               for (int j = 0; j < JPP; ++j) {
@@ -903,24 +915,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
             unsigned char* lane_at =
                 ring + st * KV_BYTES + (c16 >> 2) * (k_warp ? HALF : kBlock * 128);
+            // (the two forms of a tile's rows apart: 512 rows of 128 values, 4096 keys,
+            // 63.2 us; one form that branches in each chunk 81.5.  With heads of 64
+            // 48.9 and 50.4, 47.4 without the small scales' form.  In the loop of one
+            // page's code above it is the other way round: 1024 rows 96.3, two forms
+            // 118, without 95.0)
+            auto rows = [&](auto small) {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const int pi = j / JPP;
-              if (phys[pi] < 0) continue;  // no page there: nothing is read from it
-              const int r = (j % JPP) * RPJ + lane / CPR;
-              uint32_t h[8];  // the chunk's 16 values, f16
-              const float row_scale = __shfl_sync(0xffffffffu, sc[pi], r);
-              const uint32_t sc2 = f16x2_from_floats(row_scale, row_scale);
-              f16x4_from_e4m3x4_scaled(w8[j].x, sc2, h[0], h[1]);
-              f16x4_from_e4m3x4_scaled(w8[j].y, sc2, h[2], h[3]);
-              f16x4_from_e4m3x4_scaled(w8[j].z, sc2, h[4], h[5]);
-              f16x4_from_e4m3x4_scaled(w8[j].w, sc2, h[6], h[7]);
-              const uint32_t at = sw128_chunk(r, c8);
-              unsigned char* page_at = lane_at + (pg_lo + pi) * (k_warp ? kBlock * 128 : V_PAGE);
-              *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
-                  make_uint4(h[4], h[5], h[6], h[7]);
-            }
+              for (int j = 0; j < NJ; ++j) {
+                const int pi = j / JPP;
+                if (phys[pi] < 0) continue;  // no page there: nothing is read from it
+                const int r = (j % JPP) * RPJ + lane / CPR;
+                uint32_t h[8];  // the chunk's 16 values, f16
+                const float row_scale = __shfl_sync(0xffffffffu, sc[pi], r);
+                f16x16_from_e4m3x16_scaled(w8[j], row_scale, small.value, h);
+                const uint32_t at = sw128_chunk(r, c8);
+                unsigned char* page_at = lane_at + (pg_lo + pi) * (k_warp ? kBlock * 128 : V_PAGE);
+                *reinterpret_cast<uint4*>(page_at + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(page_at + (at ^ 16u)) =
+                    make_uint4(h[4], h[5], h[6], h[7]);
+              }
+            };
+            float least = sc[0];
+#pragma unroll
+            for (int i = 1; i < PG; ++i) least = fminf(least, sc[i]);
+            if (__any_sync(0xffffffffu, least < kSmallScale))
+              rows(std::true_type());
+            else
+              rows(std::false_type());
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&full[st]));

@@ -362,3 +362,42 @@ def test_either_way_into_the_library(fp8):
         assert torch.equal(b.run(**kw).view(torch.int16), want.view(torch.int16))
     assert b.run(workspace=ws, out=want) is want
     ops.check_device_errors()
+
+
+@pytest.mark.parametrize("form", ["single tiles", "pairs of tiles", "no window"])
+@pytest.mark.parametrize("top", [2.4e-4, 1e-3, 1e-2, 4e4, "mixed"])
+def test_row_maxima_of_the_8_bit_cache(top, form):
+    """Decode rows and chunk rows of one call over cached rows whose maxima lie far
+    from 1, or at 1.2e-4 to 1 within one page."""
+    window, sinks = (9000, 0) if form == "no window" else (6, 1)
+    if form == "pairs of tiles":
+        lens, q_lens, heads = [513, 90, 2, 1100, 60], [513, 1, 2, 400, 40], (32, 8, 128)
+    else:
+        lens, q_lens, heads = [90, 60, 200], [1, 40, 70], (8, 2, 64)
+    d = heads[2]
+    rng = np.random.default_rng(31)
+    b = Batch(30, lens, q_lens, *heads, window, sinks, fp8=True)
+    for cache, rows in ((b.kc, b.K), (b.vc, b.V)):
+        scales = ops.fp8_cache_views(cache, heads[1], d)[1]
+        old = scales.cpu().numpy()
+        if top == "mixed":
+            new = np.exp2(rng.uniform(math.log2(1.2e-4), 0, old.shape))
+        else:  # keys past 1 would make scores that nothing but their largest is seen of
+            new = (min(top, 1.0) if cache is b.kc else top) * rng.uniform(0.5, 1, old.shape)
+        new = np.where(np.isnan(old), old, new / 448).astype(np.float32)
+        scales.copy_(torch.from_numpy(new).cuda())
+        rows *= (new.astype(np.float64) / old).reshape(rows.shape[0], heads[1])[..., None]
+    b.scale = 1.0 / (math.sqrt(d) * (min(top, 1.0) if top != "mixed" else 1.0))
+    got = b.run().cpu().double().numpy()
+    ops.check_device_errors()
+    out, A, S = b.reference()
+    assert np.isfinite(got).all()
+    # beside the relative errors: a key or value below f16's normal range is right
+    # to 2^-25, which a score takes once for each |q_i|; and a decode row's weight
+    # times value scale times 2^9 is, which each key's code, at most 448, takes
+    one = np.repeat(np.array(q_lens) == 1, q_lens)[:, None, None]
+    keys = max(lens) if form == "no window" else window + sinks
+    e = 2.0 ** -25 * b.scale * np.abs(b.q64).sum(-1, keepdims=True)
+    tol = R.window_tolerance(out, A, S, True) + e * (A + np.abs(out)) + 1.01 * 2.0 ** -25 \
+        + one * keys * 2.0 ** -25 * 448 / 512
+    assert (np.abs(got - out) <= tol).all(), float((np.abs(got - out) / tol).max())
