@@ -637,6 +637,15 @@ def _launching(device, stream):
     return _other_device_or_stream(device, stream)
 
 
+def _int32(value, name: str) -> int:
+    """A number that the library takes as int32 (ctypes would pass its lower 32
+    bits on without a word)."""
+    n = int(value)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} {n} does not fit into int32")
+    return n
+
+
 def _shaped(t, name, shape):
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -674,7 +683,8 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
             return r
     L = _lib or _load()
     i32 = torch.int32
-    T, A = int(num_tokens), int(num_axes)
+    T, A = _int32(num_tokens, "num_tokens"), _int32(num_axes, "num_axes")
+    bs = _int32(block_size, "block_size")
     if T < 0 or A < 0:
         raise ValueError(f"num_tokens {T} and num_axes {A} must not be negative")
     device = _check_tensors((
@@ -707,7 +717,7 @@ def build_step(context_lens: torch.Tensor, new_lens: torch.Tensor, block_tables:
         code = L.pa_build_step(
             context_lens.data_ptr(), new_lens.data_ptr(),
             None if position_offsets is None else position_offsets.data_ptr(), S, T, A,
-            block_tables.data_ptr(), width, int(block_size), free_blocks.data_ptr(),
+            block_tables.data_ptr(), width, bs, free_blocks.data_ptr(),
             free_count.data_ptr(), free_count_out.data_ptr(), free_blocks.shape[0],
             seq_lens.data_ptr(), query_start_loc.data_ptr(), slot_mapping.data_ptr(),
             positions.data_ptr(), handle)
@@ -853,6 +863,10 @@ def _window_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_st
         if r is not None:
             return r
     L = _lib or _load()
+    window, num_sinks = _int32(window, "window"), _int32(num_sinks, "num_sinks")
+    min_q_len, max_q_len, max_seq_len = (
+        _int32(x, name) for x, name in ((min_q_len, "min_q_len"), (max_q_len, "max_q_len"),
+                                        (max_seq_len, "max_seq_len")))
     kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
     device = _check_tensors((
         ("q", q, torch.bfloat16, 3), ("k_cache", k_cache, kind, dims),
@@ -886,9 +900,9 @@ def _window_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_st
         fn = L.pa_paged_attention_window_fp8 if fp8 else L.pa_paged_attention_window
         code = fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
                   block_tables.data_ptr(), width, seq_lens.data_ptr(),
-                  query_start_loc.data_ptr(), S, T, int(min_q_len), int(max_q_len),
-                  int(max_seq_len), int(window), int(num_sinks), float(scale), out.data_ptr(),
-                  workspace.data_ptr(), workspace.numel(), handle)
+                  query_start_loc.data_ptr(), S, T, min_q_len, max_q_len, max_seq_len, window,
+                  num_sinks, float(scale), out.data_ptr(), workspace.data_ptr(),
+                  workspace.numel(), handle)
     if code:
         _check(code)
     return out

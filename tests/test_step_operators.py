@@ -179,3 +179,21 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(lib):
     with pytest.raises(ValueError, match="CUDA"):
         ops.paged_attention_window(x, cache, cache, i32.view(2, 2), i32[:2], i32[:3], 0.125,
                                    window=4, max_q_len=2, max_seq_len=4)
+
+
+@pytest.mark.parametrize("past", [2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1, 2 ** 63 + 1])
+def test_numbers_past_int32_are_refused(lib, past):
+    """ctypes passes the lower 32 bits of a number: a window of 2 ** 32 + 5 would be
+    a window of 5."""
+    i32 = torch.zeros(4, dtype=torch.int32)
+    for name in ("block_size", "num_tokens", "num_axes"):
+        with pytest.raises(ValueError, match=f"{name}.*int32"):
+            ops.build_step(i32, i32, torch.zeros(4, 4, dtype=torch.int32), i32, i32[:1],
+                           **{"block_size": 16, "num_tokens": 4, "num_axes": 1, name: past})
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16)
+    for call in (ops.paged_attention_window, ops.paged_attention_window_fp8):
+        for name in ("window", "num_sinks", "min_q_len", "max_q_len", "max_seq_len"):
+            with pytest.raises(ValueError, match=f"{name}.*int32"):
+                call(x, cache, cache, i32.view(2, 2), i32[:2], i32[:3], 0.125,
+                     **{"window": 4, "max_q_len": 2, "max_seq_len": 4, name: past})
