@@ -17,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -33,6 +34,7 @@ SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_decode_fp8.cu", "pa_d
 BINDING_SOURCE = "pa_binding.cpp"
 BINDING_NAME = "pa_binding.so"
 BINDING = os.path.join(OUT_DIR, BINDING_NAME)
+STAMP_NAME = "pa_binding.made_for"  # the torch and the Python of the last extension
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -63,12 +65,26 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _torch_dir() -> str:
-    """torch's folder, found without importing it."""
+def _torch_dir() -> Optional[str]:
+    """torch's folder, found without importing it; None where there is no torch."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found")
+        return None
     return list(spec.submodule_search_locations)[0]
+
+
+def _made_for(torch_dir: str) -> str:
+    """What the extension's headers and ABI come from."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "\n".join([sys.version, torch_dir, f.read()])
+
+
+def _read(path: str) -> Optional[str]:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _run(cmd, verbose: bool):
@@ -81,7 +97,8 @@ def _run(cmd, verbose: bool):
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link; returns the path of the shared library."""
+    """Compile and link; returns the path of the shared library.  Where there is no
+    torch, the library alone (the Python package cannot be used there)."""
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
     headers = _headers()
@@ -97,13 +114,18 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     binding_src = os.path.join(CSRC, BINDING_SOURCE)
     binding_obj = os.path.join(OUT_DIR, BINDING_SOURCE.replace(".cpp", ".o"))
     torch_dir = _torch_dir()
-    if force or _stale(binding_obj, [binding_src, os.path.join(INCLUDE, "pagedattn.h")]):
+    stamp = os.path.join(OUT_DIR, STAMP_NAME)
+    made_for = _made_for(torch_dir) if torch_dir else None
+    if not torch_dir:
+        sys.stderr.write(f"torch not found: {LIB_NAME} is built without {BINDING_NAME}\n")
+    elif force or _stale(binding_obj, [binding_src, os.path.join(INCLUDE, "pagedattn.h")]) or \
+            _read(stamp) != made_for:
         inc = os.path.join(torch_dir, "include")
-        jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-I", INCLUDE, "-I", inc, "-I",
-                     os.path.join(inc, "torch", "csrc", "api", "include"), "-I",
+        jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", inc,
+                     "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
                      os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))),
                                   "include"),
-                     "-I", sysconfig.get_paths()["include"], "-c", binding_src, "-o",
+                     "-isystem", sysconfig.get_paths()["include"], "-c", binding_src, "-o",
                      binding_obj])
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
@@ -113,13 +135,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         _run([cc] + ARCH + ["-shared", "-Xlinker", "-soname=" + LIB_NAME, "-o", tmp] + objs,
              verbose)
         os.replace(tmp, LIB)
-    if force or jobs or _stale(BINDING, [binding_obj, LIB]):
+    if torch_dir and (force or jobs or _stale(BINDING, [binding_obj, LIB])):
         tmp = BINDING + ".tmp"
         torch_lib = os.path.join(torch_dir, "lib")
         _run(["g++", "-shared", "-o", tmp, binding_obj, LIB, "-L", torch_lib, "-ltorch_python",
               "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN",
               "-Wl,-rpath," + torch_lib], verbose)
         os.replace(tmp, BINDING)
+        with open(stamp, "w") as f:
+            f.write(made_for)
     return LIB
 
 
