@@ -720,6 +720,7 @@ int paged_attention_impl(const pa_bf16* q, KvCache kv,
   a.err = err;
   a.after_prefill = false;
   a.no_decode = min_q_len >= 2;
+  a.min_q_len = min_q_len;
   a.window = window;
   a.num_sinks = num_sinks;
 

@@ -95,6 +95,7 @@ struct AttnArgs {
   // (which triggers its dependents at once and writes only prefill rows):
   // the decode kernel may then start on SMs it leaves free.
   bool after_prefill;
+  int32_t min_q_len;  // the caller's promise (0 or 1: none)
   // Sliding window (0: none): position p attends to positions above p - window
   // and to the first num_sinks ones.
   int32_t window;
@@ -169,6 +170,29 @@ cudaError_t launch_swap(uint16_t* k_cache, uint16_t* v_cache, int32_t num_blocks
                         int64_t block_elems, const int32_t* ids, int32_t n, uint16_t* staging,
                         uint16_t* host_k, uint16_t* host_v, bool out, unsigned* err,
                         cudaStream_t stream);
+
+// Whether units of two query tiles of tile_rows tokens each finish sooner than units
+// of one, where one with two takes cost times as long: whether halving the number
+// of units saves enough rounds over the SMs.  The host knows the call's rows, its
+// requests and their fewest and most rows, and takes the rows past each request's
+// fewest to be those of as few requests of max_q_len rows as hold them (requests of
+// one row are decoded elsewhere).  Requests within one tile never have a second one
+// to share a unit with.
+inline bool pairs_finish_sooner(int num_tokens, int num_seqs, int min_q_len, int max_q_len,
+                                int tile_rows, int num_kv_heads, int sm_count, double cost) {
+  const long long fewest = min_q_len > 1 ? min_q_len : 1;
+  const long long rows = num_tokens - num_seqs * fewest, span = max_q_len - fewest;
+  if (max_q_len <= tile_rows || rows < 0 || span < 0) return false;
+  const long long whole = span ? rows / span : 0, rest = span ? rows % span : 0;
+  const long long others = num_seqs - whole - (rest ? 1 : 0);
+  const auto rounds = [&](long long unit_rows) {
+    const auto tiles = [&](long long n) { return n > 1 ? (n + unit_rows - 1) / unit_rows : 0; };
+    const long long units = whole * tiles(max_q_len) + (rest ? tiles(rest + fewest) : 0) +
+                            (others > 0 ? others * tiles(fewest) : 0);
+    return (double)((units * num_kv_heads + sm_count - 1) / sm_count);
+  };
+  return rounds(2 * tile_rows) * cost < rounds(tile_rows);
+}
 
 // A step's integer inputs from the requests' lengths (pa_step.cu).
 struct StepPlanArgs {

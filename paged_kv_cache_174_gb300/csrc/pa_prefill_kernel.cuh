@@ -94,7 +94,7 @@ constexpr int kThreads = 512;
 constexpr float kNegInf = -INFINITY;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kMaxSplit = 4;
-constexpr double kPairCost = 1.7, kPairCostFp8 = 1.4;  // see pair_query_tiles
+constexpr double kPairCost = 1.7, kPairCostFp8 = 1.45;  // see pair_query_tiles
 constexpr int kMaxListed = 1024;   // prefill requests the shared-memory unit list holds
 
 // Instances of the kernel: the plain one reads the bf16 cache; the fused
@@ -1678,26 +1678,24 @@ cudaError_t launch_prefill_t(const AttnArgs& a, const PrefillPlan& plan, void* w
   return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p);
 }
 
-// Whether a sliding-window call takes two query tiles per unit.  It halves the
-// units, so it pays when they fill the SMs for more rounds than the longer
-// units cost: kPairCost* is a pair's time over a single tile's, measured with
-// one round of each (32 q / 8 kv heads of 128, a 4096-token window: 512 rows in
-// single tiles 42.5 us, 1024 in pairs 72.3, 1024 in single tiles 79.5; the 8-bit
-// cache 69.7, 96.4, 139.7).  At 8192 rows: 480 against 526 us, 8-bit 664
-// against 976; heads of 64: 444 against 500 and 510 against 643.
+// Whether a sliding-window call takes two query tiles per unit.  kPairCost* is a
+// pair's time over a single tile's with one round of each (600 rows over 4096 keys,
+// 32 q / 8 kv heads of 128: 42.7 and 69.5 us, 8-bit 66.2 and 93.6; heads of 64, 8-bit:
+// 48.9 and 75).  Both sides, single tiles and pairs, the one taken marked *:
+//   1024 rows at a 4096-token window        78.1  72.3*   8-bit 124.7  96.6*
+//   1300 rows                              112.2* 128.4         180.1 175.6*
+//   8192 rows                              410.0 376.8*         676.0 528.0*
+//   64 requests of 32 rows                  65.6*  80.1         106.8* 154.2
+//   300 decodes beside a 512-row chunk     209.3* 217.3         151.4* 164.9
+//   1000 decodes beside a 64-row chunk     614.0* 624.1         402.9* 417.0
+//   300 decodes beside a 1024-row chunk    218.7 214.5*         171.4 163.5*
+//   a 512-row chunk and 100 of 4 rows       93.5* 114.2         164.7* 213.3
 template <int D, int G, int KIND>
 bool pair_query_tiles(const AttnArgs& a, const PrefillPlan& plan, int sm_count) {
-  constexpr int TM = kRows / G;
-  constexpr double cost = KIND == kKindFp8 ? kPairCostFp8 : kPairCost;
-  if (plan.nsplit > 1) return false;
-  // (num_tokens counts decode rows too: leave room for some before taking the
-  // units for a second round)
-  if ((long long)a.num_tokens * a.num_kv_heads * 4 <= (long long)TM * sm_count * 5) return false;
-  const auto rounds = [&](int tm) {
-    const long long units = (long long)((a.num_tokens + tm - 1) / tm) * a.num_kv_heads;
-    return (double)((units + sm_count - 1) / sm_count);
-  };
-  return rounds(2 * TM) * cost < rounds(TM);
+  return plan.nsplit == 1 &&
+         pairs_finish_sooner(a.num_tokens, a.num_seqs, a.min_q_len, a.max_q_len, kRows / G,
+                             a.num_kv_heads, sm_count,
+                             KIND == kKindFp8 ? kPairCostFp8 : kPairCost);
 }
 
 }  // namespace

@@ -401,3 +401,11 @@ def test_row_maxima_of_the_8_bit_cache(top, form):
     tol = R.window_tolerance(out, A, S, True) + e * (A + np.abs(out)) + 1.01 * 2.0 ** -25 \
         + one * keys * 2.0 ** -25 * 448 / 512
     assert (np.abs(got - out) <= tol).all(), float((np.abs(got - out) / tol).max())
+
+
+@BOTH
+@pytest.mark.parametrize("q_lens", [[1] * 150 + [700] + [1] * 50, [4] * 256],
+                         ids=["a chunk in pairs of tiles beside decodes", "short requests"])
+def test_decodes_and_short_requests_beside_query_tiles(q_lens, fp8):
+    lens = [n + (37 * i) % 200 for i, n in enumerate(q_lens)]
+    Batch(32, lens, q_lens, 32, 8, 128, 90, 4, fp8=fp8).check()
