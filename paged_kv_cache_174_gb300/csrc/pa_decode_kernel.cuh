@@ -671,10 +671,9 @@ __global__ void __launch_bounds__(decode_threads<NKV, F8, MW>(), 1)
   __syncthreads();
   const int s_begin = S.plan[0];
   const int j_begin = S.plan[1];
-  if (s_begin < 0) {  // cannot happen when n_pages > 0
-    if (blockIdx.x == 0 && p.overlap) complete_after_prior();
-    return;
-  }
+  // (cannot happen when n_pages > 0, so without the wait of the other ways out: it
+  // cost a register, 118, and 0.2 to 0.4 of the decode batch's 91.5 us)
+  if (s_begin < 0) return;
   volatile int* abort_flag = &S.abort_flag;
 
   const bool is_qk = warp < NKV;
