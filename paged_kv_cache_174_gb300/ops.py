@@ -602,8 +602,12 @@ def _other_device_or_stream(device, stream):
         if stream is None:
             yield torch.cuda.current_stream().cuda_stream
         else:
-            s = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(int(stream), device)
+            if isinstance(stream, torch.cuda.Stream):
+                s = stream
+            elif int(stream) == 0:  # (ExternalStream(0) is a stream of torch's pool)
+                s = torch.cuda.default_stream(device)
+            else:
+                s = torch.cuda.ExternalStream(int(stream), device)
             with torch.cuda.stream(s):
                 yield s.cuda_stream
 
