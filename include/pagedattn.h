@@ -472,9 +472,9 @@ int pa_rotary_reshape_and_cache_fp8(const pa_bf16 *q, int64_t q_stride, const pa
  * row's first position), entries whose blocks lie wholly between num_sinks
  * and first may hold anything, and their blocks may have been freed and
  * reused (a rolling cache).  Cached rows outside every row's view have no
- * effect, whatever they hold; within a request's prompt chunk, a key or value
- * that is not finite reaches the rows that see it and, for values, may reach
- * the rows computed with them (up to 256 / group consecutive tokens).
+ * effect, whatever they hold.  Among the rows of a prompt chunk a key that is
+ * not finite reaches those that see it, and a value that is not finite may
+ * also reach those computed with them (up to 256 / group consecutive tokens).
  *
  *   window        >= 1; a window of max_seq_len or more is
  *                 pa_paged_attention_qrange

@@ -796,7 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 96 this way; two pages ahead 105).  A single query tile's producers
           // load a tile's pages at once, below: they have more of their time to
           // wait in, and a cold cache costs them less that way (a 512-row chunk at
-          // 3584, L2 flushed: 77 us, a page at a time 89; L2 warm 68 and 68).
+          // 3584, L2 flushed: 77 us, a page at a time 89; L2 warm 68 and 68; 71 and 63
+          // since the rows of small scales have a form of their own there).
           uint4 w8[JPP], n8[JPP];
           float sc = 0.f, nsc = 0.f;
 #pragma unroll

@@ -187,7 +187,9 @@ __device__ __forceinline__ void store_fp8(unsigned char* codes_at, float* scale_
 // loads in flight together: three with the bf16 cache (4099 tokens of 16 + 4
 // heads of 64, half rotated: 5.9 us, 4.3 TB/s; two: 6.2), two with the 8-bit
 // cache, whose codes cost more instructions, at eight CTAs an SM (8191 tokens of
-// 32 + 8 heads of 128: 34.7 us, 5.3 TB/s; three: 36.6).
+// 32 + 8 heads of 128: 35.0 us, 5.3 TB/s; three: 36.6, before the angles took 128
+// bits of 1 / (2 pi)).  Eight leave 64 registers a thread, and those instances
+// spill: 20 bytes stored and 68 loaded with halves paired, 4 and 20 interleaved.
 template <int D, bool F8, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, F8 ? 8 : 6)
     rotary_cache_kernel(const RotaryArgs p, int split_log2) {

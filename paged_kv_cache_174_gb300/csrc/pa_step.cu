@@ -13,11 +13,11 @@
 // new block is free[count - 1 - (B_s + k)] (last in, first out, as the host
 // allocator hands blocks out), and its i-th new token is row T_s + i.
 //
-// Kilobytes move, so latency is all there is (64 decodes 3.3 us back to back;
-// 256 requests with 20K token rows on three axes 6.9 us, 30.8 with one CTA).  Every CTA scans all the lengths
-// into its shared memory (cheaper than handing the sums over), then the CTAs'
-// threads walk the flat lists of new blocks and of token rows, each finding its
-// request by a binary search of the prefix sums.  The grid is one cluster, so
+// Kilobytes move, so latency is all there is (64 decodes 3.1 us back to back;
+// 256 requests with 20K token rows on three axes 7.0 us, 30.8 with one CTA).  Every
+// CTA scans all the lengths into its shared memory (cheaper than handing the sums
+// over), then the CTAs' threads walk the flat lists of new blocks and of token rows,
+// each finding its request by a binary search of the prefix sums.  The grid is one cluster, so
 // that its barrier can keep every write behind every CTA's reads: seq_lens may
 // be context_lens, and free_count_out free_count.
 #include <cstdint>
