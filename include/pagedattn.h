@@ -505,6 +505,185 @@ int pa_paged_attention_window_fp8(const pa_bf16 *q, const uint8_t *k_cache,
                                   size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Long contexts: read less of the cache, or hold less of it.
+ *
+ * pa_summarize_blocks, pa_select_blocks and pa_paged_attention_blocks let each
+ * query attend to a chosen part of its context: bounds of each block's keys
+ * are kept up to date beside the cache, every query picks blocks by a score
+ * from the bounds, and the attention reads those blocks alone.
+ * pa_paged_attention_weights is attention that also adds up how much weight
+ * each cached token gets, and pa_evict_tokens drops the tokens of least weight
+ * and returns the blocks that this empties.  The pages have no counterpart for
+ * either ("PagedAttention 核心机理" reads every block of a request).
+ *
+ * All take block_size 16 or 32, head_dim 64 or 128, num_kv_heads 1, 2, 4 or 8
+ * and (where there are queries) group sizes 1, 2, 4 and 8; anything else is
+ * PA_ERR_UNSUPPORTED.  They run on the GPU alone and may be captured.
+ *
+ * pa_summarize_blocks: for the blocks that the step's new tokens are in
+ * (request s: positions seq_lens[s] - q_len .. seq_lens[s] - 1, q_len from
+ * query_start_loc), and each kv head, the largest and the smallest value of
+ * every channel over the block's keys below seq_lens[s]:
+ *   bounds        int8 [num_blocks, num_kv_heads, 2, head_dim], the maxima's
+ *                 codes, then the minima's; 16-byte aligned
+ *   bound_scales  float [num_blocks, num_kv_heads]: p, the least power of two
+ *                 with |x| <= 127 p for all of them (1 where all are 0; not
+ *                 below 2^-126)
+ *   codes         ceil(max / p) and floor(min / p): bounds after rounding too
+ * A NaN in a key counts as 0 and an infinity as the largest finite float.
+ * Call it after the step's keys are in the cache.  query_start_loc NULL: every
+ * block of every request (after an eviction, a swap in or a block copy);
+ * num_tokens is then not used.  Of blocks that several requests share, those
+ * that are full come out alike whichever request writes them.
+ */
+int pa_summarize_blocks(const pa_bf16 *k_cache, int32_t num_blocks, int32_t block_size,
+                        int32_t num_kv_heads, int32_t head_dim, const int32_t *block_tables,
+                        int32_t max_blocks, const int32_t *seq_lens,
+                        const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                        int8_t *bounds, float *bound_scales, cudaStream_t stream);
+int pa_summarize_blocks_fp8(const uint8_t *k_cache, int32_t num_blocks, int32_t block_size,
+                            int32_t num_kv_heads, int32_t head_dim, const int32_t *block_tables,
+                            int32_t max_blocks, const int32_t *seq_lens,
+                            const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                            int8_t *bounds, float *bound_scales, cudaStream_t stream);
+
+/*
+ * pa_select_blocks: for each new token (position p) and kv head, num_selected
+ * of the blocks 0 .. p / block_size: the first num_sinks, the last num_recent
+ * (at least 1, so the token's own block is among them), and of the others
+ * those of the highest score, ties to the lowest index.
+ *   selected      int32 [num_tokens, num_kv_heads, num_selected]: logical
+ *                 block indices in increasing order, then -1 where there are
+ *                 fewer; rows of no request are left as they were
+ *   score         of a block for a kv head: the largest over the q heads of
+ *                 its group of  p_q p sum_c x_c (x_c > 0 ? max_c : min_c),  with
+ *                 q's codes x = rint(q / p_q) (nearest, ties to even), p_q by
+ *                 the rule of bound_scales, and the block's codes and scale:
+ *                 an upper bound of q k over the block's keys, but for the
+ *                 rounding of q.  The sums are of integers and exact, so the
+ *                 result depends on nothing but the inputs.
+ *   max_seq_len   at most 393216 blocks
+ * The product is with q as it is given (scale the scores and they keep their
+ * order).
+ */
+int pa_select_blocks(const pa_bf16 *q, const int8_t *bounds, const float *bound_scales,
+                     int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, const int32_t *block_tables,
+                     int32_t max_blocks, const int32_t *seq_lens, const int32_t *query_start_loc,
+                     int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
+                     int32_t num_selected, int32_t num_sinks, int32_t num_recent,
+                     int32_t *selected, cudaStream_t stream);
+
+/*
+ * pa_paged_attention_blocks: attention of each new token (position p, q_len
+ * of any length) over the blocks listed for it and its kv head, and in them
+ * over the positions up to p.
+ *   selected      as pa_select_blocks writes it; in any order, negative
+ *                 entries are passed over, an entry listed twice counts twice,
+ *                 an entry past the token's own block is flagged and passed
+ *                 over.  A token with nothing listed gets zeros.
+ * No workspace.  Rows of out that belong to no request are left as they were.
+ * Weights are rounded to 2^-17 (two bf16), sums are in fp32.  Every token
+ * reads its own blocks: meant for decode rows and a few drafted tokens.
+ */
+int pa_paged_attention_blocks(const pa_bf16 *q, const pa_bf16 *k_cache, const pa_bf16 *v_cache,
+                              int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim,
+                              const int32_t *block_tables, int32_t max_blocks,
+                              const int32_t *seq_lens, const int32_t *query_start_loc,
+                              int32_t num_seqs, int32_t num_tokens, float scale,
+                              const int32_t *selected, int32_t num_selected, pa_bf16 *out,
+                              cudaStream_t stream);
+int pa_paged_attention_blocks_fp8(const pa_bf16 *q, const uint8_t *k_cache,
+                                  const uint8_t *v_cache, int32_t num_blocks, int32_t block_size,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  const int32_t *block_tables, int32_t max_blocks,
+                                  const int32_t *seq_lens, const int32_t *query_start_loc,
+                                  int32_t num_seqs, int32_t num_tokens, float scale,
+                                  const int32_t *selected, int32_t num_selected, pa_bf16 *out,
+                                  cudaStream_t stream);
+
+/*
+ * pa_paged_attention_weights: pa_paged_attention, and
+ *   weights       float [num_seqs, num_kv_heads, weights_len], row s of the
+ *                 request in row s of block_tables, entry j its cached token
+ *                 j: for j < seq_lens[s] the sum, over the request's new rows
+ *                 that see token j and over the q heads of the kv head, of the
+ *                 softmax weight of j is added; the entries of the new tokens
+ *                 (the last q_len) start from 0 in this call.  Entries from
+ *                 seq_lens[s] on, and rows of requests without new tokens, are
+ *                 left as they were.  weights_len >= max_seq_len.
+ * The weights are fp32 sums in one order (no atomics); the scores behind them
+ * are sums of exact products in fp32.  Prompt chunks' outputs are
+ * pa_paged_attention's; decode rows' weights are rounded to 2^-17.
+ * Workspace: pa_weights_workspace_size() bytes, 256-byte aligned; calls with
+ * max_q_len <= 1 use none (NULL will do).
+ */
+size_t pa_weights_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_q_len,
+                                 int32_t max_seq_len);
+int pa_paged_attention_weights(const pa_bf16 *q, const pa_bf16 *k_cache, const pa_bf16 *v_cache,
+                               int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim,
+                               const int32_t *block_tables, int32_t max_blocks,
+                               const int32_t *seq_lens, const int32_t *query_start_loc,
+                               int32_t num_seqs, int32_t num_tokens, int32_t min_q_len,
+                               int32_t max_q_len, int32_t max_seq_len, float scale,
+                               float *weights, int32_t weights_len, pa_bf16 *out,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+int pa_paged_attention_weights_fp8(const pa_bf16 *q, const uint8_t *k_cache,
+                                   const uint8_t *v_cache, int32_t num_blocks,
+                                   int32_t block_size, int32_t num_q_heads,
+                                   int32_t num_kv_heads, int32_t head_dim,
+                                   const int32_t *block_tables, int32_t max_blocks,
+                                   const int32_t *seq_lens, const int32_t *query_start_loc,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t min_q_len,
+                                   int32_t max_q_len, int32_t max_seq_len, float scale,
+                                   float *weights, int32_t weights_len, pa_bf16 *out,
+                                   void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/*
+ * pa_evict_tokens: each request s with seq_lens[s] > budgets[s] keeps
+ * budgets[s] tokens, for each kv head its own: the first num_sinks, the last
+ * num_recent, and of those between the ones of the largest weights (ties: the
+ * lowest index; NaN counts as the largest).  The kept tokens' K, V and weights
+ * move together in order: kept token i becomes token i.  Rows and weights from
+ * the new length on are left as they were, and so are the block tables: the
+ * entries past the new length's blocks hold nothing any more (pa_build_step
+ * writes them anew).
+ *   seq_lens      [num_seqs], at most max_seq_len (itself at most 524288);
+ *                 the tokens' rows must belong to the request alone (copy
+ *                 shared blocks first; a budget of seq_lens[s] or more leaves
+ *                 a request alone)
+ *   budgets       [num_seqs], each at least num_sinks + num_recent
+ *   seq_lens_out  [num_seqs] new lengths; may be seq_lens
+ *   free_blocks   [num_blocks], free_count [1]: as pa_build_step takes them;
+ *                 the blocks of the tables' columns from ceil(budget /
+ *                 block_size) on are pushed in the order of requests and
+ *                 columns.  free_count_out [1] may be free_count.
+ *   position_offsets  [num_seqs] or NULL: the tokens that went are added, so
+ *                 that pa_build_step gives later tokens their true positions
+ * A length or budget out of range is flagged and its request left alone; a
+ * table entry that names no block is flagged and the rows behind it stay.
+ */
+int pa_evict_tokens(pa_bf16 *k_cache, pa_bf16 *v_cache, float *weights, int32_t weights_len,
+                    int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                    int32_t head_dim, const int32_t *block_tables, int32_t max_blocks,
+                    const int32_t *seq_lens, const int32_t *budgets, int32_t num_seqs,
+                    int32_t max_seq_len, int32_t num_sinks, int32_t num_recent,
+                    int32_t *free_blocks, const int32_t *free_count, int32_t *seq_lens_out,
+                    int32_t *free_count_out, int32_t *position_offsets, cudaStream_t stream);
+int pa_evict_tokens_fp8(uint8_t *k_cache, uint8_t *v_cache, float *weights, int32_t weights_len,
+                        int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                        int32_t head_dim, const int32_t *block_tables, int32_t max_blocks,
+                        const int32_t *seq_lens, const int32_t *budgets, int32_t num_seqs,
+                        int32_t max_seq_len, int32_t num_sinks, int32_t num_recent,
+                        int32_t *free_blocks, const int32_t *free_count, int32_t *seq_lens_out,
+                        int32_t *free_count_out, int32_t *position_offsets,
+                        cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word that
  * the kernels of this library set on the current device.  Returns PA_OK,
  * PA_ERR_DEVICE_BOUNDS, PA_ERR_TIMEOUT or PA_ERR_CUDA.

@@ -30,7 +30,8 @@ LIB = os.path.join(OUT_DIR, LIB_NAME)
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_decode_fp8.cu", "pa_decode_fused.cu",
            "pa_prefill.cu", "pa_prefill_fp8.cu", "pa_graph.cu", "pa_step.cu", "pa_rotary.cu",
            "pa_decode_window.cu", "pa_decode_window_fp8.cu", "pa_prefill_window.cu",
-           "pa_prefill_window_fp8.cu"]
+           "pa_prefill_window_fp8.cu", "pa_long_api.cu", "pa_blocks.cu", "pa_sparse.cu",
+           "pa_weights.cu", "pa_weights_chunk.cu", "pa_evict.cu"]
 BINDING_SOURCE = "pa_binding.cpp"
 BINDING_NAME = "pa_binding.so"
 BINDING = os.path.join(OUT_DIR, BINDING_NAME)

@@ -90,11 +90,13 @@ int api_fail(int status, const char* fmt, ...) {
 
 int api_warm_device() { return device_state(nullptr, nullptr); }
 
+int api_device_state(unsigned** err, int* sms) { return device_state(err, sms); }
+
 }  // namespace pa
 
 extern "C" {
 
-int pa_version(void) { return 300; }  // 0.3.0: step inputs, rotary positions, sliding window
+int pa_version(void) { return 400; }  // 0.4.0: chosen blocks, accumulated weights, eviction
 
 const char* pa_get_last_error(void) { return t_last_error.c_str(); }
 

@@ -1,5 +1,6 @@
 // pa_binding.cpp -- the short way from Python into libpagedattn for the calls
-// around a step (step inputs, rotary positions, sliding-window attention).
+// around a step (step inputs, rotary positions, sliding-window attention) and those
+// for long contexts (bounds, choice and attention of blocks, weights, eviction).
 //
 // Those calls take a few microseconds on the GPU, and reading a dozen tensors'
 // types, shapes and addresses through Python and ctypes takes longer than that
@@ -342,6 +343,285 @@ PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The q heads, kv heads and head_dim that q and a cache agree on, and the step's arrays.
+struct Step {
+  const at::Tensor *q, *tables, *lens, *starts;
+  int64_t T, nq, d, S, blocks, block;
+  void *kc, *vc;
+  // a: q, k_cache, v_cache, block_tables, seq_lens, query_start_loc; n_kv from elsewhere
+  bool take(PyObject* const* a, bool fp8, int64_t nkv, int device) {
+    q = plain(a[0], kBf16, 3, device);
+    tables = plain(a[3], kInt, 2, device);
+    lens = plain(a[4], kInt, 1, device);
+    starts = plain(a[5], kInt, 1, device);
+    if (!q || !tables || !lens || !starts) return false;
+    T = q->size(0), nq = q->size(1), d = q->size(2), S = tables->size(0);
+    return nkv > 0 && nq % nkv == 0 && lens->size(0) == S && starts->size(0) == S + 1 &&
+           T <= INT32_MAX && S <= INT32_MAX && nq <= INT32_MAX && tables->size(1) <= INT32_MAX &&
+           caches(a[1], a[2], fp8, nkv, d, device, &blocks, &block, &kc, &vc);
+  }
+};
+
+int32_t narrow(int64_t n) { return static_cast<int32_t>(n); }
+
+// The output beside q: the caller's (of q's shape), one to be made, or no plain case.
+bool output(PyObject* o, const at::Tensor& q, int device, const at::Tensor** out) {
+  if (o == Py_None) return true;
+  *out = plain(o, kBf16, 3, device);
+  return *out && (*out)->sizes() == q.sizes();
+}
+
+PyObject* returned(PyObject* given, const at::Tensor& made) {
+  if (given == Py_None) return THPVariable_Wrap(made);
+  Py_INCREF(given);
+  return given;
+}
+
+// summarize(fp8, k_cache, block_tables, seq_lens, query_start_loc, bounds,
+//   bound_scales, num_tokens)
+PyObject* summarize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 8) Py_RETURN_NONE;
+  const bool fp8 = a[0] == Py_True;
+  const int device = current_device_of(a[1]);
+  if (device < 0) Py_RETURN_NONE;
+  const at::Tensor *bt = plain(a[2], kInt, 2, device), *sl = plain(a[3], kInt, 1, device),
+                   *qsl = a[4] == Py_None ? nullptr : plain(a[4], kInt, 1, device),
+                   *bounds = plain(a[5], at::kChar, 4, device),
+                   *scales = plain(a[6], at::kFloat, 2, device);
+  int32_t T;
+  if (!bt || !sl || (a[4] != Py_None && !qsl) || !bounds || !scales || !number(a[7], &T))
+    Py_RETURN_NONE;
+  const int64_t S = bt->size(0), nb = bounds->size(0), nkv = bounds->size(1), d = bounds->size(3);
+  int64_t blocks, block;
+  void *kc, *vc;
+  if (sl->size(0) != S || (qsl && qsl->size(0) != S + 1) || bounds->size(2) != 2 ||
+      scales->size(0) != nb || scales->size(1) != nkv || S > INT32_MAX || nkv > INT32_MAX ||
+      d > INT32_MAX || bt->size(1) > INT32_MAX ||
+      !caches(a[1], a[1], fp8, nkv, d, device, &blocks, &block, &kc, &vc) || blocks != nb)
+    Py_RETURN_NONE;
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(device).stream();
+  auto* b = static_cast<int8_t*>(bounds->data_ptr());
+  auto* sc = static_cast<float*>(scales->data_ptr());
+  int st;
+  {
+    Unlocked unlocked;
+    const int32_t* starts = qsl ? ints(*qsl) : nullptr;
+    st = fp8 ? pa_summarize_blocks_fp8(static_cast<uint8_t*>(kc), narrow(nb), narrow(block),
+                                       narrow(nkv), narrow(d), ints(*bt), narrow(bt->size(1)),
+                                       ints(*sl), starts, narrow(S), T, b, sc, s)
+             : pa_summarize_blocks(static_cast<pa_bf16*>(kc), narrow(nb), narrow(block),
+                                   narrow(nkv), narrow(d), ints(*bt), narrow(bt->size(1)),
+                                   ints(*sl), starts, narrow(S), T, b, sc, s);
+  }
+  return PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// select_blocks(q, bounds, bound_scales, block_tables, seq_lens, query_start_loc,
+//   num_selected, num_sinks, num_recent, block_size, max_seq_len, out)
+PyObject* select_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 12) Py_RETURN_NONE;
+  const int device = current_device_of(a[0]);
+  if (device < 0) Py_RETURN_NONE;
+  const at::Tensor *q = plain(a[0], kBf16, 3, device), *bounds = plain(a[1], at::kChar, 4, device),
+                   *scales = plain(a[2], at::kFloat, 2, device), *bt = plain(a[3], kInt, 2, device),
+                   *sl = plain(a[4], kInt, 1, device), *qsl = plain(a[5], kInt, 1, device);
+  int32_t K, sinks, recent, block, maxl;
+  if (!q || !bounds || !scales || !bt || !sl || !qsl || !number(a[6], &K) ||
+      !number(a[7], &sinks) || !number(a[8], &recent) || !number(a[9], &block) ||
+      !number(a[10], &maxl) || K < 1)
+    Py_RETURN_NONE;
+  const int64_t T = q->size(0), nq = q->size(1), d = q->size(2), S = bt->size(0),
+                nb = bounds->size(0), nkv = bounds->size(1);
+  if (bounds->size(2) != 2 || bounds->size(3) != d || nkv <= 0 || nq % nkv ||
+      scales->size(0) != nb || scales->size(1) != nkv || sl->size(0) != S ||
+      qsl->size(0) != S + 1 || T > INT32_MAX || S > INT32_MAX || nb > INT32_MAX ||
+      nq > INT32_MAX || d > INT32_MAX || bt->size(1) > INT32_MAX)
+    Py_RETURN_NONE;
+  at::Tensor made;
+  const at::Tensor* out = nullptr;
+  const int64_t shape[] = {T, nkv, K};
+  if (a[11] != Py_None) {
+    out = plain(a[11], kInt, 3, device);
+    if (!out || out->sizes() != at::IntArrayRef(shape)) Py_RETURN_NONE;
+  }
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(device).stream();
+  int st;
+  {
+    Unlocked unlocked;
+    if (!out) {
+      made = at::empty(shape, sl->options());
+      out = &made;
+    }
+    st = pa_select_blocks(static_cast<const pa_bf16*>(q->data_ptr()),
+                          static_cast<const int8_t*>(bounds->data_ptr()),
+                          static_cast<const float*>(scales->data_ptr()), narrow(nb), block,
+                          narrow(nq), narrow(nkv), narrow(d), ints(*bt), narrow(bt->size(1)),
+                          ints(*sl), ints(*qsl), narrow(S), narrow(T), maxl, K, sinks, recent,
+                          ints(*out), s);
+  }
+  if (st != PA_OK) return PyLong_FromLong(st);
+  return returned(a[11], made);
+  END_HANDLE_TH_ERRORS
+}
+
+// blocks(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+//   selected, out)
+PyObject* blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 10 || !PyFloat_CheckExact(a[7])) Py_RETURN_NONE;
+  const bool fp8 = a[0] == Py_True;
+  const int device = current_device_of(a[1]);
+  if (device < 0) Py_RETURN_NONE;
+  const at::Tensor* sel = plain(a[8], kInt, 3, device);
+  Step x;
+  if (!sel || !x.take(a + 1, fp8, sel->size(1), device) || sel->size(0) != x.T ||
+      sel->size(2) > INT32_MAX)
+    Py_RETURN_NONE;
+  at::Tensor made;
+  const at::Tensor* out = nullptr;
+  if (!output(a[9], *x.q, device, &out)) Py_RETURN_NONE;
+  const float scale = static_cast<float>(PyFloat_AS_DOUBLE(a[7]));
+  const int32_t nkv = narrow(sel->size(1)), K = narrow(sel->size(2));
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(device).stream();
+  int st;
+  {
+    Unlocked unlocked;
+    if (!out) {
+      made = at::empty(x.q->sizes(), x.q->options());
+      out = &made;
+    }
+    const auto* q = static_cast<const pa_bf16*>(x.q->data_ptr());
+    auto* o = static_cast<pa_bf16*>(out->data_ptr());
+    st = fp8 ? pa_paged_attention_blocks_fp8(
+                   q, static_cast<uint8_t*>(x.kc), static_cast<uint8_t*>(x.vc), narrow(x.blocks),
+                   narrow(x.block), narrow(x.nq), nkv, narrow(x.d), ints(*x.tables),
+                   narrow(x.tables->size(1)), ints(*x.lens), ints(*x.starts), narrow(x.S),
+                   narrow(x.T), scale, ints(*sel), K, o, s)
+             : pa_paged_attention_blocks(
+                   q, static_cast<pa_bf16*>(x.kc), static_cast<pa_bf16*>(x.vc), narrow(x.blocks),
+                   narrow(x.block), narrow(x.nq), nkv, narrow(x.d), ints(*x.tables),
+                   narrow(x.tables->size(1)), ints(*x.lens), ints(*x.starts), narrow(x.S),
+                   narrow(x.T), scale, ints(*sel), K, o, s);
+  }
+  if (st != PA_OK) return PyLong_FromLong(st);
+  return returned(a[9], made);
+  END_HANDLE_TH_ERRORS
+}
+
+// weights(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+//   weights, min_q_len, max_q_len, max_seq_len, out, workspace)
+PyObject* weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 14 || !PyFloat_CheckExact(a[7])) Py_RETURN_NONE;
+  const bool fp8 = a[0] == Py_True;
+  const int device = current_device_of(a[1]);
+  if (device < 0) Py_RETURN_NONE;
+  const at::Tensor* w = plain(a[8], at::kFloat, 3, device);
+  const at::Tensor* ws = a[13] == Py_None ? nullptr : plain(a[13], at::kByte, 1, device);
+  int32_t minq, maxq, maxl;
+  Step x;
+  if (!w || (a[13] != Py_None && !ws) || !number(a[9], &minq) || !number(a[10], &maxq) ||
+      !number(a[11], &maxl) || (!ws && maxq > 1) || !x.take(a + 1, fp8, w->size(1), device) ||
+      w->size(0) != x.S || w->size(2) > INT32_MAX)
+    Py_RETURN_NONE;
+  at::Tensor made;
+  const at::Tensor* out = nullptr;
+  if (!output(a[12], *x.q, device, &out)) Py_RETURN_NONE;
+  const float scale = static_cast<float>(PyFloat_AS_DOUBLE(a[7]));
+  const int32_t nkv = narrow(w->size(1)), length = narrow(w->size(2));
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(device).stream();
+  int st;
+  {
+    Unlocked unlocked;
+    if (!out) {
+      made = at::empty(x.q->sizes(), x.q->options());
+      out = &made;
+    }
+    const auto* q = static_cast<const pa_bf16*>(x.q->data_ptr());
+    auto* o = static_cast<pa_bf16*>(out->data_ptr());
+    auto* f = static_cast<float*>(w->data_ptr());
+    void* space = ws ? ws->data_ptr() : nullptr;
+    const size_t bytes = ws ? static_cast<size_t>(ws->numel()) : 0;
+    st = fp8 ? pa_paged_attention_weights_fp8(
+                   q, static_cast<uint8_t*>(x.kc), static_cast<uint8_t*>(x.vc), narrow(x.blocks),
+                   narrow(x.block), narrow(x.nq), nkv, narrow(x.d), ints(*x.tables),
+                   narrow(x.tables->size(1)), ints(*x.lens), ints(*x.starts), narrow(x.S),
+                   narrow(x.T), minq, maxq, maxl, scale, f, length, o, space, bytes, s)
+             : pa_paged_attention_weights(
+                   q, static_cast<pa_bf16*>(x.kc), static_cast<pa_bf16*>(x.vc), narrow(x.blocks),
+                   narrow(x.block), narrow(x.nq), nkv, narrow(x.d), ints(*x.tables),
+                   narrow(x.tables->size(1)), ints(*x.lens), ints(*x.starts), narrow(x.S),
+                   narrow(x.T), minq, maxq, maxl, scale, f, length, o, space, bytes, s);
+  }
+  if (st != PA_OK) return PyLong_FromLong(st);
+  return returned(a[12], made);
+  END_HANDLE_TH_ERRORS
+}
+
+// evict(fp8, k_cache, v_cache, weights, block_tables, seq_lens, budgets, free_blocks,
+//   free_count, num_sinks, num_recent, max_seq_len, seq_lens_out, free_count_out,
+//   position_offsets)
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 15) Py_RETURN_NONE;
+  const bool fp8 = a[0] == Py_True;
+  const int device = current_device_of(a[1]);
+  const at::Tensor* k = tensor(a[1]);
+  if (device < 0 || k->dim() != (fp8 ? 3 : 4)) Py_RETURN_NONE;
+  const at::Tensor *w = plain(a[3], at::kFloat, 3, device), *bt = plain(a[4], kInt, 2, device),
+                   *sl = plain(a[5], kInt, 1, device), *budgets = plain(a[6], kInt, 1, device),
+                   *free = plain(a[7], kInt, 1, device), *count = plain(a[8], kInt, 1, device);
+  const at::Tensor* lens_out = a[12] == Py_None ? sl : plain(a[12], kInt, 1, device);
+  const at::Tensor* count_out = a[13] == Py_None ? count : plain(a[13], kInt, 1, device);
+  const at::Tensor* offsets = a[14] == Py_None ? nullptr : plain(a[14], kInt, 1, device);
+  int32_t sinks, recent, maxl;
+  if (!w || !bt || !sl || !budgets || !free || !count || !lens_out || !count_out ||
+      (a[14] != Py_None && !offsets) || !number(a[9], &sinks) || !number(a[10], &recent) ||
+      !number(a[11], &maxl))
+    Py_RETURN_NONE;
+  const int64_t S = bt->size(0), nkv = w->size(1), length = w->size(2);
+  const int64_t d = fp8 ? (nkv > 0 ? k->size(2) / (16 * nkv) - 4 : 0) : k->size(3);
+  int64_t blocks, block;
+  void *kc, *vc;
+  if (w->size(0) != S || sl->size(0) != S || budgets->size(0) != S || count->size(0) != 1 ||
+      lens_out->size(0) != S || count_out->size(0) != 1 || (offsets && offsets->size(0) != S) ||
+      S > INT32_MAX || length > INT32_MAX || bt->size(1) > INT32_MAX || nkv > INT32_MAX ||
+      d > INT32_MAX || !caches(a[1], a[2], fp8, nkv, d, device, &blocks, &block, &kc, &vc) ||
+      free->size(0) != blocks)
+    Py_RETURN_NONE;
+  const cudaStream_t s = c10::cuda::getCurrentCUDAStream(device).stream();
+  int st;
+  {
+    Unlocked unlocked;
+    auto* f = static_cast<float*>(w->data_ptr());
+    int32_t* off = offsets ? ints(*offsets) : nullptr;
+    st = fp8 ? pa_evict_tokens_fp8(
+                   static_cast<uint8_t*>(kc), static_cast<uint8_t*>(vc), f, narrow(length),
+                   narrow(blocks), narrow(block), narrow(nkv), narrow(d), ints(*bt),
+                   narrow(bt->size(1)), ints(*sl), ints(*budgets), narrow(S), maxl, sinks, recent,
+                   ints(*free), ints(*count), ints(*lens_out), ints(*count_out), off, s)
+             : pa_evict_tokens(
+                   static_cast<pa_bf16*>(kc), static_cast<pa_bf16*>(vc), f, narrow(length),
+                   narrow(blocks), narrow(block), narrow(nkv), narrow(d), ints(*bt),
+                   narrow(bt->size(1)), ints(*sl), ints(*budgets), narrow(S), maxl, sinks, recent,
+                   ints(*free), ints(*count), ints(*lens_out), ints(*count_out), off, s);
+  }
+  if (st != PA_OK) return PyLong_FromLong(st);
+  PyObject* r = a[12] == Py_None ? a[5] : a[12];
+  Py_INCREF(r);
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL,
+          nullptr};
+}
+
 PyMethodDef kMethods[] = {
     {"build_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(build_step)),
      METH_FASTCALL, nullptr},
@@ -349,6 +629,11 @@ PyMethodDef kMethods[] = {
      nullptr},
     {"window", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(window)), METH_FASTCALL,
      nullptr},
+    method<summarize>("summarize"),
+    method<select_blocks>("select_blocks"),
+    method<blocks>("blocks"),
+    method<weights>("weights"),
+    method<evict>("evict"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "pa_binding", nullptr, -1, kMethods,

@@ -237,6 +237,131 @@ struct RotaryArgs {
 };
 cudaError_t launch_rotary_cache(const RotaryArgs& p, cudaStream_t stream);
 
+// Bounds of the blocks' keys (pa_blocks.cu).
+struct BoundsArgs {
+  const void* k_cache;  // bf16 values, or (fp8) pages of E4M3 codes and row scales
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;  // or null: every block of every request
+  int8_t* bounds;                  // [num_blocks, n_kv, 2, head_dim]
+  float* scales;                   // [num_blocks, n_kv]
+  unsigned* err;
+  long long slots;  // (set by the launcher) places for a (request, block)
+  int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_kv, head_dim, block_log2;
+  bool fp8;
+};
+cudaError_t launch_bounds(BoundsArgs p, cudaStream_t stream);
+
+// The blocks that each query attends to (pa_blocks.cu).
+struct SelectArgs {
+  const uint16_t* q;
+  const int8_t* bounds;
+  const float* scales;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  int32_t* selected;  // [num_tokens, n_kv, num_selected]
+  unsigned* err;
+  int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_kv, group, head_dim, block_log2;
+  int32_t num_selected, num_sinks, num_recent, max_seq_len;
+};
+constexpr int kSelectMaxShare = 48 * 1024;  // blocks of a CTA, four bytes of shared memory each
+constexpr int kSelectMaxCtas = 8;
+cudaError_t launch_select(const SelectArgs& p, int sm_count, cudaStream_t stream);
+
+// Attention over chosen blocks (pa_sparse.cu).
+struct SparseArgs {
+  const uint16_t* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  const int32_t* selected;  // [num_tokens, n_kv, num_selected]
+  uint16_t* out;
+  unsigned* err;
+  float scale_log2;
+  int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_kv, group, head_dim;
+  int32_t block_shift;  // log2(block_size / 16)
+  int32_t num_selected;
+  bool fp8;
+};
+cudaError_t launch_sparse(const SparseArgs& p, int sm_count, cudaStream_t stream);
+
+// Decode attention that adds the weights up (pa_weights.cu).
+struct WeighArgs {
+  const uint16_t* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  float* weights;  // [num_seqs, n_kv, weights_stride]
+  uint16_t* out;
+  unsigned* err;
+  int64_t weights_stride;
+  float scale_log2;
+  int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_kv, group, head_dim;
+  int32_t block_shift;  // log2(block_size / 16)
+  int32_t max_seq_len;
+  int32_t kept_pages;  // (set by the launcher) pages of a CTA whose scores are kept
+  bool chunks;         // requests with more than one row are taken elsewhere
+  bool fp8;
+};
+cudaError_t launch_weigh(const WeighArgs& p, int sm_count, cudaStream_t stream);
+
+// Accumulated weights of chunks (pa_weights_chunk.cu).
+struct ChunkArgs {
+  const uint16_t* q;
+  const void* k_cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  float* weights;
+  float2* sums;  // [pieces, num_tokens, n_q] (max in log2 units, sum) of each row
+  unsigned* err;
+  int64_t weights_stride;
+  float scale_log2;
+  int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_q, n_kv, group, head_dim;
+  int32_t block_shift, max_seq_len;
+  int32_t pieces, skip;  // (set by the launcher)
+  bool fp8;
+};
+// The pieces that the keys of a row are cut into, and the bytes of their sums.
+constexpr int kMaxChunkPieces = 8;
+struct ChunkPlan {
+  int pieces;
+  size_t bytes;
+};
+ChunkPlan chunk_plan(int num_tokens, int num_q_heads, int num_kv_heads, int max_seq_len,
+                     int sm_count);
+cudaError_t launch_chunk_weights(const ChunkArgs& p, int max_q_len, int sm_count,
+                                 cudaStream_t stream);
+
+// Eviction by accumulated weight (pa_evict.cu).
+struct EvictArgs {
+  void* k_cache;
+  void* v_cache;
+  float* weights;  // [num_seqs, n_kv, weights_stride]
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* budgets;
+  int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* seq_lens_out;
+  int32_t* free_count_out;
+  int32_t* position_offsets;  // or null
+  unsigned* err;
+  int64_t weights_stride;
+  int32_t num_blocks, max_blocks, num_seqs, n_kv, head_dim, block_log2;
+  int32_t num_sinks, num_recent, max_seq_len;
+  bool fp8;
+  bool staged;  // (set by the launcher) the weights' keys fit in shared memory
+};
+constexpr int kEvictMaxLen = 1 << 19;          // two bits a token in shared memory
+constexpr size_t kEvictStaged = 64 * 1024;
+cudaError_t launch_evict(EvictArgs p, int sm_count, cudaStream_t stream);
+
 cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, unsigned* err,
                                          cudaStream_t stream);
 
@@ -244,5 +369,7 @@ cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, unsigned* 
 // and the per-device state lookup, for the parts of the ABI outside pa_api.cu.
 int api_fail(int status, const char* fmt, ...);
 int api_warm_device();
+// The current device's error word and SM count.
+int api_device_state(unsigned** err, int* sms);
 
 }  // namespace pa

@@ -120,6 +120,24 @@ def _load() -> ctypes.CDLL:
         getattr(L, name).argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32,
                                      i32, i32, i32, i32, i32, i32, f32, vp, vp, sz, vp]
         getattr(L, name).restype = ctypes.c_int
+    for suffix in ("", "_fp8"):
+        for name, args in (
+                ("pa_summarize_blocks", [vp, i32, i32, i32, i32, vp, i32, vp, vp, i32, i32, vp,
+                                         vp, vp]),
+                ("pa_paged_attention_blocks", [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp,
+                                               vp, i32, i32, f32, vp, i32, vp, vp]),
+                ("pa_paged_attention_weights", [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp,
+                                                vp, i32, i32, i32, i32, i32, f32, vp, i32, vp,
+                                                vp, sz, vp]),
+                ("pa_evict_tokens", [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32,
+                                     i32, i32, i32, vp, vp, vp, vp, vp, vp])):
+            getattr(L, name + suffix).argtypes = args
+            getattr(L, name + suffix).restype = ctypes.c_int
+    L.pa_select_blocks.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, i32, i32,
+                                   i32, i32, i32, i32, vp, vp]
+    L.pa_select_blocks.restype = ctypes.c_int
+    L.pa_weights_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    L.pa_weights_workspace_size.restype = sz
     L.pa_step_graph_create.argtypes = [ctypes.POINTER(StepBuffers), ctypes.POINTER(vp)]
     L.pa_step_graph_create.restype = ctypes.c_int
     L.pa_step_graph_launch.argtypes = [vp, vp]
@@ -939,6 +957,413 @@ def paged_attention_window_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     return _window_attention(True, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
                              scale, window, num_sinks, min_q_len, max_q_len, max_seq_len, out,
                              workspace, stream)
+
+
+# ---------------------------------------------------------------------------
+# Long contexts: attention over blocks chosen for each query (bounds of the
+# blocks' keys, the choice, the attention), and eviction by accumulated
+# attention weight.  As the operators around a step: any device, the extension
+# module for the plain case.
+# ---------------------------------------------------------------------------
+
+def _cache_geometry(fp8, k_cache, v_cache, nkv, d):
+    """(num_blocks, block_size) of a cache, or a pair, of nkv heads of d."""
+    if v_cache is not None and v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be alike")
+    if fp8:
+        if k_cache.shape[2] != fp8_page_bytes(nkv, d):
+            raise ValueError(f"the 8-bit cache's pages must have {fp8_page_bytes(nkv, d)} bytes "
+                             f"for n_kv {nkv}, d {d}")
+        return k_cache.shape[0], k_cache.shape[1] * FP8_PAGE_TOKENS
+    nb, bs, n, dc = k_cache.shape
+    if n != nkv or dc != d:
+        raise ValueError(f"the cache must be [num_blocks, block_size, {nkv}, {d}]")
+    return nb, bs
+
+
+def _step_shapes(block_tables, seq_lens, query_start_loc):
+    S, width = block_tables.shape
+    if seq_lens.shape[0] != S or (query_start_loc is not None
+                                  and query_start_loc.shape[0] != S + 1):
+        raise ValueError("seq_lens [S], query_start_loc [S+1], block_tables [S, maxb] disagree")
+    return S, width
+
+
+def _bounds_shapes(bounds, bound_scales):
+    nb, nkv, two, d = bounds.shape
+    if two != 2:
+        raise ValueError("bounds must be [num_blocks, n_kv, 2, d]")
+    _shaped(bound_scales, "bound_scales", (nb, nkv))
+    return nb, nkv, d
+
+
+def alloc_bounds(num_blocks: int, num_kv_heads: int, head_dim: int, device=None):
+    """(bounds int8 [num_blocks, n_kv, 2, d], bound_scales float32 [num_blocks,
+    n_kv]) for summarize_blocks to write, zero-filled, on the device."""
+    dev = device or "cuda"
+    return (torch.zeros(num_blocks, num_kv_heads, 2, head_dim, dtype=torch.int8, device=dev),
+            torch.zeros(num_blocks, num_kv_heads, dtype=torch.float32, device=dev))
+
+
+def _summarize(fp8, k_cache, block_tables, seq_lens, query_start_loc, bounds, bound_scales,
+               num_tokens, stream):
+    if stream is None:
+        r = (_binding or _load_binding()).summarize(fp8, k_cache, block_tables, seq_lens,
+                                                    query_start_loc, bounds, bound_scales,
+                                                    num_tokens)
+        if r is not None:
+            return _check(r)
+    L = _lib or _load()
+    T = _int32(num_tokens, "num_tokens")
+    kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
+    i32 = torch.int32
+    device = _check_tensors((
+        ("k_cache", k_cache, kind, dims), ("block_tables", block_tables, i32, 2),
+        ("seq_lens", seq_lens, i32, 1), ("query_start_loc", query_start_loc, i32, 1),
+        ("bounds", bounds, torch.int8, 4), ("bound_scales", bound_scales, torch.float32, 2)))
+    nb, nkv, d = _bounds_shapes(bounds, bound_scales)
+    blocks, bs = _cache_geometry(fp8, k_cache, None, nkv, d)
+    if blocks != nb:
+        raise ValueError(f"bounds are of {nb} blocks, the cache has {blocks}")
+    S, width = _step_shapes(block_tables, seq_lens, query_start_loc)
+    with _launching(device, stream) as handle:
+        fn = L.pa_summarize_blocks_fp8 if fp8 else L.pa_summarize_blocks
+        code = fn(k_cache.data_ptr(), nb, bs, nkv, d, block_tables.data_ptr(), width,
+                  seq_lens.data_ptr(),
+                  None if query_start_loc is None else query_start_loc.data_ptr(), S, T,
+                  bounds.data_ptr(), bound_scales.data_ptr(), handle)
+    if code:
+        _check(code)
+
+
+def summarize_blocks(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     query_start_loc: Optional[torch.Tensor], bounds: torch.Tensor,
+                     bound_scales: torch.Tensor, *, num_tokens: int = 0, stream=None) -> None:
+    """Bounds of the keys of the blocks that the step's new tokens are in, as
+    8-bit codes with a power-of-two scale for each block and kv head (see
+    pa_summarize_blocks).
+
+    ``bounds`` int8 [num_blocks, n_kv, 2, d] and ``bound_scales`` float32
+    [num_blocks, n_kv] (alloc_bounds) are updated; ``num_tokens`` is the step's
+    (rows of q).  ``query_start_loc`` None: every block of every request.
+    """
+    return _summarize(False, k_cache, block_tables, seq_lens, query_start_loc, bounds,
+                      bound_scales, num_tokens, stream)
+
+
+def summarize_blocks_fp8(k_cache: torch.Tensor, block_tables: torch.Tensor,
+                         seq_lens: torch.Tensor, query_start_loc: Optional[torch.Tensor],
+                         bounds: torch.Tensor, bound_scales: torch.Tensor, *,
+                         num_tokens: int = 0, stream=None) -> None:
+    """summarize_blocks of the 8-bit cache's keys (code times scale)."""
+    return _summarize(True, k_cache, block_tables, seq_lens, query_start_loc, bounds,
+                      bound_scales, num_tokens, stream)
+
+
+def select_blocks(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch.Tensor,
+                  block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                  query_start_loc: torch.Tensor, *, num_selected: int, num_sinks: int = 1,
+                  num_recent: int = 1, block_size: int, max_seq_len: int,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The blocks that each new token attends to, for each kv head (see
+    pa_select_blocks): the first ``num_sinks``, the last ``num_recent`` (its own
+    among them) and those of the highest score, ``num_selected`` in all.
+    Returns ``out`` int32 [T, n_kv, num_selected], logical block indices in
+    increasing order, then -1 (rows of no request: as they were)."""
+    if stream is None:
+        r = (_binding or _load_binding()).select_blocks(
+            q, bounds, bound_scales, block_tables, seq_lens, query_start_loc, num_selected,
+            num_sinks, num_recent, block_size, max_seq_len, out)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
+    L = _lib or _load()
+    num_selected, num_sinks, num_recent, bs, max_seq_len = (
+        _int32(x, name) for x, name in (
+            (num_selected, "num_selected"), (num_sinks, "num_sinks"),
+            (num_recent, "num_recent"), (block_size, "block_size"),
+            (max_seq_len, "max_seq_len")))
+    i32 = torch.int32
+    device = _check_tensors((
+        ("q", q, torch.bfloat16, 3), ("bounds", bounds, torch.int8, 4),
+        ("bound_scales", bound_scales, torch.float32, 2), ("block_tables", block_tables, i32, 2),
+        ("seq_lens", seq_lens, i32, 1), ("query_start_loc", query_start_loc, i32, 1),
+        ("out", out, i32, 3)))
+    nb, nkv, d = _bounds_shapes(bounds, bound_scales)
+    T, nq, dq = q.shape
+    if dq != d:
+        raise ValueError("q and bounds disagree in head_dim")
+    if nkv <= 0 or nq % nkv != 0:
+        raise ValueError(f"num_q_heads {nq} must be a multiple of num_kv_heads {nkv}")
+    if num_selected < 1:
+        raise ValueError(f"num_selected {num_selected} < 1")
+    S, width = _step_shapes(block_tables, seq_lens, query_start_loc)
+    if out is not None:
+        _shaped(out, "out", (T, nkv, num_selected))
+    with _launching(device, stream) as handle:
+        if out is None:
+            out = torch.empty(T, nkv, num_selected, dtype=i32, device=device)
+        code = L.pa_select_blocks(
+            q.data_ptr(), bounds.data_ptr(), bound_scales.data_ptr(), nb, bs, nq, nkv, d,
+            block_tables.data_ptr(), width, seq_lens.data_ptr(), query_start_loc.data_ptr(), S, T,
+            max_seq_len, num_selected, num_sinks, num_recent, out.data_ptr(), handle)
+    if code:
+        _check(code)
+    return out
+
+
+def _blocks_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+                      selected, out, stream):
+    if stream is None:
+        r = (_binding or _load_binding()).blocks(fp8, q, k_cache, v_cache, block_tables, seq_lens,
+                                                 query_start_loc, scale, selected, out)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
+    L = _lib or _load()
+    kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
+    i32 = torch.int32
+    device = _check_tensors((
+        ("q", q, torch.bfloat16, 3), ("k_cache", k_cache, kind, dims),
+        ("v_cache", v_cache, kind, dims), ("block_tables", block_tables, i32, 2),
+        ("seq_lens", seq_lens, i32, 1), ("query_start_loc", query_start_loc, i32, 1),
+        ("selected", selected, i32, 3), ("out", out, torch.bfloat16, 3)))
+    T, nq, d = q.shape
+    rows, nkv, n = selected.shape
+    if rows != T:
+        raise ValueError("selected must be [T, n_kv, num_selected]")
+    nb, bs = _cache_geometry(fp8, k_cache, v_cache, nkv, d)
+    if nkv <= 0 or nq % nkv != 0:
+        raise ValueError(f"num_q_heads {nq} must be a multiple of num_kv_heads {nkv}")
+    S, width = _step_shapes(block_tables, seq_lens, query_start_loc)
+    if out is not None:
+        _shaped(out, "out", q.shape)
+    with _launching(device, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        fn = L.pa_paged_attention_blocks_fp8 if fp8 else L.pa_paged_attention_blocks
+        code = fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
+                  block_tables.data_ptr(), width, seq_lens.data_ptr(),
+                  query_start_loc.data_ptr(), S, T, float(scale), selected.data_ptr(), n,
+                  out.data_ptr(), handle)
+    if code:
+        _check(code)
+    return out
+
+
+def paged_attention_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           query_start_loc: torch.Tensor, scale: float, selected: torch.Tensor,
+                           *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of each new token over the blocks listed for it and its kv head
+    (see pa_paged_attention_blocks): ``selected`` int32 [T, n_kv, n], as
+    select_blocks returns it; negative entries are passed over.  Returns
+    ``out``."""
+    return _blocks_attention(False, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                             scale, selected, out, stream)
+
+
+def paged_attention_blocks_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                               query_start_loc: torch.Tensor, scale: float,
+                               selected: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
+    """paged_attention_blocks over the 8-bit cache."""
+    return _blocks_attention(True, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                             scale, selected, out, stream)
+
+
+def alloc_weights_workspace(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                            head_dim: int, max_q_len: int, max_seq_len: int,
+                            device=None) -> torch.Tensor:
+    """Workspace of paged_attention_weights, enough for every call within these
+    sizes (pa_weights_workspace_size)."""
+    n = int(_load().pa_weights_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                              head_dim, max_q_len, max_seq_len))
+    if n == 0:
+        raise PagedAttnError(1, "pa_weights_workspace_size rejected the arguments or found no "
+                                "device")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _weights_attention(fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+                       weights, min_q_len, max_q_len, max_seq_len, out, workspace, stream):
+    if stream is None:
+        r = (_binding or _load_binding()).weights(
+            fp8, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, weights,
+            min_q_len, max_q_len, max_seq_len, out, workspace)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
+    L = _lib or _load()
+    min_q_len, max_q_len, max_seq_len = (
+        _int32(x, name) for x, name in ((min_q_len, "min_q_len"), (max_q_len, "max_q_len"),
+                                        (max_seq_len, "max_seq_len")))
+    kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
+    i32 = torch.int32
+    device = _check_tensors((
+        ("q", q, torch.bfloat16, 3), ("k_cache", k_cache, kind, dims),
+        ("v_cache", v_cache, kind, dims), ("block_tables", block_tables, i32, 2),
+        ("seq_lens", seq_lens, i32, 1), ("query_start_loc", query_start_loc, i32, 1),
+        ("weights", weights, torch.float32, 3), ("out", out, torch.bfloat16, 3),
+        ("workspace", workspace, torch.uint8, 1)))
+    T, nq, d = q.shape
+    rows, nkv, length = weights.shape
+    nb, bs = _cache_geometry(fp8, k_cache, v_cache, nkv, d)
+    if nkv <= 0 or nq % nkv != 0:
+        raise ValueError(f"num_q_heads {nq} must be a multiple of num_kv_heads {nkv}")
+    S, width = _step_shapes(block_tables, seq_lens, query_start_loc)
+    if rows != S:
+        raise ValueError("weights must be [S, n_kv, length]")
+    if out is not None:
+        _shaped(out, "out", q.shape)
+    with _launching(device, stream) as handle:
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None and max_q_len > 1:
+            workspace = alloc_weights_workspace(S, T, nq, nkv, d, max_q_len, max_seq_len, device)
+        fn = L.pa_paged_attention_weights_fp8 if fp8 else L.pa_paged_attention_weights
+        code = fn(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, nq, nkv, d,
+                  block_tables.data_ptr(), width, seq_lens.data_ptr(),
+                  query_start_loc.data_ptr(), S, T, min_q_len, max_q_len, max_seq_len,
+                  float(scale), weights.data_ptr(), length, out.data_ptr(),
+                  None if workspace is None else workspace.data_ptr(),
+                  0 if workspace is None else workspace.numel(), handle)
+    if code:
+        _check(code)
+    return out
+
+
+def paged_attention_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                            query_start_loc: torch.Tensor, scale: float, weights: torch.Tensor,
+                            *, max_q_len: int, max_seq_len: int,
+                            out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None,
+                            min_q_len: int = 0) -> torch.Tensor:
+    """paged_attention that also adds up the attention weight of each cached
+    token (see pa_paged_attention_weights).
+
+    ``weights`` float32 [S, n_kv, length], row s of the request in row s of
+    block_tables, entry j its cached token j, is updated: the softmax weights of
+    the call's rows, summed over rows and over the q heads of the kv head, are
+    added; the new tokens' entries start from 0.  ``workspace``
+    (alloc_weights_workspace) is needed where max_q_len > 1.  Returns ``out``.
+    """
+    return _weights_attention(False, q, k_cache, v_cache, block_tables, seq_lens,
+                              query_start_loc, scale, weights, min_q_len, max_q_len, max_seq_len,
+                              out, workspace, stream)
+
+
+def paged_attention_weights_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                query_start_loc: torch.Tensor, scale: float,
+                                weights: torch.Tensor, *, max_q_len: int, max_seq_len: int,
+                                out: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None, stream=None,
+                                min_q_len: int = 0) -> torch.Tensor:
+    """paged_attention_weights over the 8-bit cache."""
+    return _weights_attention(True, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                              scale, weights, min_q_len, max_q_len, max_seq_len, out, workspace,
+                              stream)
+
+
+def _evict(fp8, k_cache, v_cache, weights, block_tables, seq_lens, budgets, free_blocks,
+           free_count, num_sinks, num_recent, max_seq_len, seq_lens_out, free_count_out,
+           position_offsets, stream):
+    if stream is None:
+        r = (_binding or _load_binding()).evict(
+            fp8, k_cache, v_cache, weights, block_tables, seq_lens, budgets, free_blocks,
+            free_count, num_sinks, num_recent, max_seq_len, seq_lens_out, free_count_out,
+            position_offsets)
+        if type(r) is int:
+            _check(r)
+        if r is not None:
+            return r
+    L = _lib or _load()
+    num_sinks, num_recent, max_seq_len = (
+        _int32(x, name) for x, name in ((num_sinks, "num_sinks"), (num_recent, "num_recent"),
+                                        (max_seq_len, "max_seq_len")))
+    kind, dims = (torch.uint8, 3) if fp8 else (torch.bfloat16, 4)
+    i32 = torch.int32
+    device = _check_tensors((
+        ("k_cache", k_cache, kind, dims), ("v_cache", v_cache, kind, dims),
+        ("weights", weights, torch.float32, 3), ("block_tables", block_tables, i32, 2),
+        ("seq_lens", seq_lens, i32, 1), ("budgets", budgets, i32, 1),
+        ("free_blocks", free_blocks, i32, 1), ("free_count", free_count, i32, 1),
+        ("seq_lens_out", seq_lens_out, i32, 1), ("free_count_out", free_count_out, i32, 1),
+        ("position_offsets", position_offsets, i32, 1)))
+    rows, nkv, length = weights.shape
+    S, width = _step_shapes(block_tables, seq_lens, None)
+    if rows != S:
+        raise ValueError("weights must be [S, n_kv, length]")
+    if fp8:  # a page is 16 n_kv (d + 4) bytes
+        d = k_cache.shape[2] // (FP8_PAGE_TOKENS * nkv) - 4 if nkv > 0 else 0
+    else:
+        d = k_cache.shape[3]
+    nb, bs = _cache_geometry(fp8, k_cache, v_cache, nkv, d)
+    _shaped(budgets, "budgets", (S,))
+    _shaped(free_blocks, "free_blocks", (nb,))
+    _shaped(free_count, "free_count", (1,))
+    for name, t, shape in (("seq_lens_out", seq_lens_out, (S,)),
+                           ("free_count_out", free_count_out, (1,)),
+                           ("position_offsets", position_offsets, (S,))):
+        if t is not None:
+            _shaped(t, name, shape)
+    if seq_lens_out is None:
+        seq_lens_out = seq_lens
+    if free_count_out is None:
+        free_count_out = free_count
+    with _launching(device, stream) as handle:
+        fn = L.pa_evict_tokens_fp8 if fp8 else L.pa_evict_tokens
+        code = fn(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), length, nb, bs, nkv,
+                  d, block_tables.data_ptr(), width, seq_lens.data_ptr(), budgets.data_ptr(), S,
+                  max_seq_len, num_sinks, num_recent, free_blocks.data_ptr(),
+                  free_count.data_ptr(), seq_lens_out.data_ptr(), free_count_out.data_ptr(),
+                  None if position_offsets is None else position_offsets.data_ptr(), handle)
+    if code:
+        _check(code)
+    return seq_lens_out
+
+
+def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor,
+                 block_tables: torch.Tensor, seq_lens: torch.Tensor, budgets: torch.Tensor,
+                 free_blocks: torch.Tensor, free_count: torch.Tensor, *, num_sinks: int = 0,
+                 num_recent: int = 0, max_seq_len: int,
+                 seq_lens_out: Optional[torch.Tensor] = None,
+                 free_count_out: Optional[torch.Tensor] = None,
+                 position_offsets: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Cut each request down to its budget of tokens, kv head by kv head those
+    of the largest accumulated weights beside the first ``num_sinks`` and the
+    last ``num_recent``, move them together in order, and return the emptied
+    blocks to ``free_blocks`` (see pa_evict_tokens).
+
+    ``k_cache``, ``v_cache``, ``weights`` [S, n_kv, length] and ``free_blocks``
+    are updated in place; so are ``seq_lens`` and ``free_count`` unless
+    ``seq_lens_out`` / ``free_count_out`` are given.  ``position_offsets`` gets
+    the evicted tokens added (pass it to build_step afterwards).  Returns the
+    new lengths.
+    """
+    return _evict(False, k_cache, v_cache, weights, block_tables, seq_lens, budgets,
+                  free_blocks, free_count, num_sinks, num_recent, max_seq_len, seq_lens_out,
+                  free_count_out, position_offsets, stream)
+
+
+def evict_tokens_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, budgets: torch.Tensor,
+                     free_blocks: torch.Tensor, free_count: torch.Tensor, *, num_sinks: int = 0,
+                     num_recent: int = 0, max_seq_len: int,
+                     seq_lens_out: Optional[torch.Tensor] = None,
+                     free_count_out: Optional[torch.Tensor] = None,
+                     position_offsets: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """evict_tokens over the 8-bit cache: codes and scales move as they are."""
+    return _evict(True, k_cache, v_cache, weights, block_tables, seq_lens, budgets,
+                  free_blocks, free_count, num_sinks, num_recent, max_seq_len, seq_lens_out,
+                  free_count_out, position_offsets, stream)
 
 
 def selftest_wait_timeout(limit_ns: int = 5_000_000, stream=None) -> None:
