@@ -2,23 +2,26 @@
 // pages of the cache, by a warp: what the attention over chosen blocks (pa_sparse.cu)
 // and the weighing decode (pa_weights.cu) share.
 //
-// A page is 16 keys of one kv head.  Both products are m16n8k16 on the tensor cores
-// with the query heads as rows 0..7 of A: S = Q K^T takes K rows as they lie in memory
-// as its B operand (the channels of a k step may be any as long as q's agree, so a lane
-// loads 16 contiguous bytes of a key and has the operands of two or four steps), and
-// S's accumulator layout is the A layout of O += P V.  V's operand pairs two keys of a
-// channel: two rows' words are interleaved in registers.  Nothing goes through shared
-// memory, so the loads of several pages per SM are in flight with no ring to manage;
-// the products are a few percent of the time.
+// A page is 16 keys of one kv head.  Each warp streams pages through a ring of its own
+// in shared memory: one TMA box for a page's K and one for its V (the rows of a head lie
+// n_kv rows apart), completion on the stage's mbarrier, and no synchronisation with
+// other warps, so that what is in flight is the ring's bytes whatever the warp does.
+// Both products are m16n8k16 on the tensor cores, transposed, with the query heads as the
+// eight columns, so that no row of a product is idle and O takes 4 d / 16 registers:
+// S^T = K Q^T has the page's keys as its 16 rows, O^T += V^T P^T 16 channels.  K's operand
+// comes by ldmatrix, V's by ldmatrix.trans, P^T's by transposing S^T's accumulators
+// (movmatrix).
 //
-// P is split into two bf16, p = hi + lo: lo takes the otherwise idle rows 8..15, so O
-// has the weights to 2^-17 and the row sums are of the fp32 values.
-// 8-bit cache: K codes become f16 (exact) against q as f16 (divided by a power of two
-// near its largest element, so that what q's rounding loses is below 2^-24 of that);
-// V codes become bf16 (exact) and their scales multiply p before it is split.
+// P is split into two bf16, p = hi + lo, a product each, so O has the weights to 2^-16
+// and the row sums are of the fp32 values.
+// 8-bit cache: ldmatrix moves pairs of codes.  K codes become f16 (exact) against q as
+// f16 (divided by a power of two near its largest element, so that what q's rounding
+// loses is below 2^-24 of that); V codes become bf16 (exact) and their scales multiply
+// p before it is split.
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -40,299 +43,376 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// A page's rows are read once by an SM: past L1.
-__device__ __forceinline__ uint4 ld_page16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
-__device__ __forceinline__ uint2 ld_page8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// An 8 x 8 block of 16-bit values (row lane / 4, columns 2 (lane % 4) and the next) transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int h, int z,
+                                              int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(z), "r"(w), "r"(bar)
+      : "memory");
 }
 
-// The request of token t (all threads of the block; uniform), or false: a row behind
-// the last sequence, or lengths out of range (flagged by one thread).
+// The request of token t, or false: a row behind the last sequence, or lengths out of
+// range (flagged by one thread).  All threads of the block; found: shared memory that one
+// of them set to -1 (its x) before a barrier.
 struct TokenRequest {
-  int s, pos, len, rows;
+  int s, pos;
 };
 __device__ __forceinline__ bool find_request(const int32_t* qsl, const int32_t* seq_lens,
                                              int num_seqs, int num_tokens, long long most, int t,
-                                             unsigned* err, bool report, TokenRequest& R) {
-  int begun = 0;
-  for (int s0 = 0; s0 < num_seqs; s0 += blockDim.x) {
-    const int n = __syncthreads_count(s0 + (int)threadIdx.x < num_seqs &&
-                                      qsl[s0 + threadIdx.x] <= t);
-    begun += n;
-    if (n < (int)blockDim.x) break;
+                                             unsigned* err, bool report, int4* found,
+                                             TokenRequest& R) {
+  // one round of independent loads: every thread looks at requests of its own
+  for (int i = threadIdx.x; i < num_seqs; i += blockDim.x) {
+    const int a = qsl[i], b = qsl[i + 1], len = seq_lens[i];
+    if (a <= t && t < b) *found = make_int4(i, a, b, len);
   }
-  if (begun == 0) return false;
-  R.s = begun - 1;
-  const int a = qsl[R.s], b = qsl[R.s + 1];
-  R.len = seq_lens[R.s];
-  R.rows = b - a;
-  if (t >= b) return false;
-  if (a < 0 || b > num_tokens || R.len < R.rows || R.len > most) {
+  __syncthreads();
+  const int4 f = *found;
+  if (f.x < 0) return false;
+  const int rows = f.z - f.y;
+  if (f.y < 0 || f.z > num_tokens || f.w < rows || f.w > most) {
     if (report) flag_error(err, DEVERR_BOUNDS);
     return false;
   }
-  R.pos = R.len - (b - t);
+  R.s = f.x;
+  R.pos = f.w - (f.z - t);
   return true;
 }
 
+constexpr int kRowsWarps = 4;  // of a CTA
+
+// A warp's ring in shared memory, of at most ROOM bytes.
+template <int D, bool F8, int ROOM>
+struct RowsRing {
+  static constexpr int ROW = F8 ? D : 128;              // bytes of a row as it lies there
+  static constexpr int PAGE = 16 * (F8 ? D : 2 * D);    // bytes of a K or V page
+  static constexpr int STAGE = 2 * PAGE;
+  static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
+  static_assert(STAGES >= 2, "");
+  static constexpr int BYTES = STAGES * STAGE;          // of a warp
+  uint64_t full[kRowsWarps][STAGES];
+  int live[kRowsWarps][STAGES];                         // keys of the page that count
+  alignas(16) float scales[kRowsWarps][STAGES][32];     // 8-bit cache: 16 of K, 16 of V
+  int abort_flag;
+};
+
 template <int D, int G, bool F8>
 struct WarpRows {
-  static constexpr int STEPS = D / 16;            // k steps of S
-  static constexpr int KC = F8 ? D / 64 : D / 32; // 16-byte chunks of a key for a lane
-  static constexpr int VW = F8 ? D / 32 : D / 16; // words of a V row for a lane
-  static constexpr int TILES = D / 8;             // 8-channel tiles of O
+  static constexpr int ROW = F8 ? D : 128;  // bytes of a row in a ring
+  static constexpr int STEPS = D / 16;      // k steps of S^T, and 16-channel tiles of O^T
   uint32_t q0[STEPS], q2[STEPS];
-  float o[TILES][4];
-  float m, l;      // of head lane / 4: reference max (log2 units), this lane's share of the sum
-  float mul;       // score to log2 units (8-bit cache: to be multiplied by the key's scale)
-  uint4 k[2][KC];  // keys lane / 4 and lane / 4 + 8
-  float ks;        // 8-bit cache: K scale of key lane % 16 (lanes 0-15), V scale (16-31)
+  float o[STEPS][4];  // channels lane / 4 and 8 on, heads 2 (lane % 4) and the next
+  float m[2], l[2];   // of those heads: reference max (log2 units), this lane's share of the sum
+  float mul;          // score to log2 units (8-bit cache: to be multiplied by the key's scale)
 
-  // q: the token's G heads of this kv head
+  // q: the token's G heads of this kv head (its loads come back while the first pages do)
   __device__ __forceinline__ void begin(const uint16_t* q, float scale_log2) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    m = -INFINITY;
-    l = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
     mul = scale_log2;
 #pragma unroll
-    for (int n = 0; n < TILES; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int n = 0; n < STEPS; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     if constexpr (!F8) {
 #pragma unroll
-      for (int j = 0; j < KC; ++j) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (g < G) w = __ldg(reinterpret_cast<const uint4*>(q + g * D + (4 * j + t) * 8));
-        q0[2 * j] = w.x, q2[2 * j] = w.y, q0[2 * j + 1] = w.z, q2[2 * j + 1] = w.w;
+      for (int j = 0; j < STEPS; ++j) {
+        q0[j] = q2[j] = 0u;
+        if (g < G) {
+          const uint32_t* at = reinterpret_cast<const uint32_t*>(q + g * D + j * 16 + 2 * t);
+          q0[j] = __ldg(at), q2[j] = __ldg(at + 4);
+        }
       }
     } else {
-      uint32_t w[KC][8];
+      // (a product's k step of 16 codes has codes 4t, 4t + 1 where k is 2t, 2t + 1, and the
+      // next two where k is 2t + 8, 2t + 9: as a lane gets four codes in a register)
+      uint2 w[STEPS];
       float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < KC; ++j) {
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (g < G) {
-          const uint4* at = reinterpret_cast<const uint4*>(q + g * D + (4 * j + t) * 16);
-          a = __ldg(at), b = __ldg(at + 1);
-        }
-        w[j][0] = a.x, w[j][1] = a.y, w[j][2] = a.z, w[j][3] = a.w;
-        w[j][4] = b.x, w[j][5] = b.y, w[j][6] = b.z, w[j][7] = b.w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = bf16x2_to_float2(w[j][i]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
+      for (int j = 0; j < STEPS; ++j) {
+        w[j] = make_uint2(0u, 0u);
+        if (g < G) w[j] = __ldg(reinterpret_cast<const uint2*>(q + g * D + j * 16 + 4 * t));
+        const float2 f = bf16x2_to_float2(w[j].x), v = bf16x2_to_float2(w[j].y);
+        top = fmaxf(fmax3(top, fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(v.x), fabsf(v.y)));
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the power of two below the largest element (its reciprocal is normal too)
+      // the power of two below the head's largest element (its reciprocal is normal too)
       const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
       const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-      mul *= __uint_as_float((uint32_t)e << 23);
 #pragma unroll
-      for (int j = 0; j < KC; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = bf16x2_to_float2(w[j][2 * i]), h = bf16x2_to_float2(w[j][2 * i + 1]);
-          q0[4 * j + i] = f16x2_from_floats(f.x * inv, f.y * inv);
-          q2[4 * j + i] = f16x2_from_floats(h.x * inv, h.y * inv);
-        }
+      for (int j = 0; j < STEPS; ++j) {
+        const float2 f = bf16x2_to_float2(w[j].x), v = bf16x2_to_float2(w[j].y);
+        q0[j] = f16x2_from_floats(f.x * inv, f.y * inv);
+        q2[j] = f16x2_from_floats(v.x * inv, v.y * inv);
       }
+      // the scores' heads are 2t and 2t + 1, not lane / 4: their factors by lane
+      const float own = __uint_as_float((uint32_t)e << 23);
+      head_mul[0] = __shfl_sync(0xffffffffu, own, 8 * t);
+      head_mul[1] = __shfl_sync(0xffffffffu, own, 8 * t + 4);
     }
+  }
+  float head_mul[2];  // (8-bit cache)
+
+  // This lane's row of the four 8 x 8 blocks of an ldmatrix over a page: the one of matrices
+  // 0-3 is (key half, chunk) = (0, 0) (1, 0) (0, 1) (1, 1); chunk c's is an xor with 16 c away.
+  static __device__ __forceinline__ uint32_t k_lane(uint32_t page) {
+    const int lane = threadIdx.x & 31, r = (lane & 7) + 8 * ((lane >> 3) & 1), c = lane >> 4;
+    return row_at(page, r) ^ (c << 4);
+  }
+  // The same with (0, 0) (0, 1) (1, 0) (1, 1) for V in 16 bits; V's codes go as K's.
+  static __device__ __forceinline__ uint32_t v_lane(uint32_t page) {
+    const int lane = threadIdx.x & 31, r = (lane & 7) + 8 * (lane >> 4), c = (lane >> 3) & 1;
+    return F8 ? k_lane(page) : row_at(page, r) ^ (c << 4);
+  }
+  static __device__ __forceinline__ uint32_t row_at(uint32_t page, int r) {
+    return ROW == 128 ? page + r * 128 + ((r & 7) << 4) : page + r * 64 + (((r >> 1) & 3) << 4);
   }
 
-  // Row r of a page: its first byte for kv head h.
-  static __device__ __forceinline__ const uint8_t* row(const uint8_t* page, int r, int n_kv,
-                                                       int h) {
-    return page + ((int64_t)r * n_kv + h) * (F8 ? D : 2 * D);
-  }
-  static __device__ __forceinline__ int64_t page_bytes(int n_kv) {
-    return F8 ? fp8_page_bytes(n_kv, D) : (int64_t)16 * n_kv * D * 2;
-  }
-
-  __device__ __forceinline__ void load_k(const uint8_t* k_page, const uint8_t* v_page, int n_kv,
-                                         int h) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // x: scores of keys lane / 4 (x[0], x[1]) and 8 on with heads 2t and 2t + 1, in log2 units,
+  // of the page at k (shared memory); scales: the stage's (8-bit cache).
+  __device__ __forceinline__ void scores(uint32_t k, const float* scales, float (&x)[4]) const {
+    const uint32_t at = k_lane(k);
+    float c[2][4];  // (two chains of products)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint8_t* at = row(k_page, g + 8 * n, n_kv, h) + t * 16;
-#pragma unroll
-      for (int j = 0; j < KC; ++j) k[n][j] = ld_page16(at + j * 64);
-    }
-    if constexpr (F8) {
-      const uint8_t* page = lane < 16 ? k_page : v_page;
-      ks = __ldg(reinterpret_cast<const float*>(page + fp8_scales_offset(n_kv, D)) +
-                 (lane & 15) * n_kv + h);
-    }
-  }
-  // The rows 2t, 2t + 1, 2t + 8, 2t + 9 of a V page, this lane's channels.
-  __device__ __forceinline__ void load_v(const uint8_t* v_page, int n_kv, int h,
-                                         uint32_t (&v)[4][VW]) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* at = row(v_page, 2 * t + (i & 1) + (i >> 1) * 8, n_kv, h);
-      if constexpr (F8 && D == 64) {
-        const uint2 w = ld_page8(at + g * 8);
-        v[i][0] = w.x, v[i][1] = w.y;
-      } else {
-#pragma unroll
-        for (int c = 0; c < VW / 4; ++c) {
-          const uint4 w = ld_page16(at + c * 128 + g * 16);
-          v[i][4 * c] = w.x, v[i][4 * c + 1] = w.y, v[i][4 * c + 2] = w.z, v[i][4 * c + 3] = w.w;
-        }
-      }
-    }
-  }
-
-  // x: scores of head lane / 4 with keys 2t, 2t + 1, 2t + 8, 2t + 9 in log2 units; vs:
-  // the V scales of those keys.
-  __device__ __forceinline__ void scores(float (&x)[4], float (&vs)[4]) const {
-    const int t = threadIdx.x & 3;
-    float c[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-#pragma unroll
-      for (int j = 0; j < KC; ++j) {
-        const uint32_t w[4] = {k[n][j].x, k[n][j].y, k[n][j].z, k[n][j].w};
-        if constexpr (F8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            f16x2x2_from_e4m3x4(w[i], b0, b1);
-            mma_f16_16816(c[n], q0[4 * j + i], 0u, q2[4 * j + i], 0u, b0, b1);
-          }
-        } else {
-          mma_bf16_16816(c[n], q0[2 * j], 0u, q2[2 * j], 0u, w[0], w[1]);
-          mma_bf16_16816(c[n], q0[2 * j + 1], 0u, q2[2 * j + 1], 0u, w[2], w[3]);
-        }
-      }
-    }
-    x[0] = c[0][0] * mul, x[1] = c[0][1] * mul, x[2] = c[1][0] * mul, x[3] = c[1][1] * mul;
+    for (int n = 0; n < 2; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
     if constexpr (F8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
-        x[i] *= __shfl_sync(0xffffffffu, ks, r);
-        vs[i] = __shfl_sync(0xffffffffu, ks, 16 + r);
-      }
-    }
-  }
-
-  // Keys at and past `live` of the page are not seen: their scores and what is
-  // added of their V rows, which may hold anything, count nothing.
-  __device__ __forceinline__ void hide(int live, float (&x)[4], float (&vs)[4],
-                                       uint32_t (&v)[4][VW]) const {
-    const int t = threadIdx.x & 3;
+      for (int j = 0; j < STEPS; j += 2) {  // 16 codes a chunk, two chunks
+        uint32_t w[4];
+        ldmatrix4(at ^ (j << 4), w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (2 * t + (i & 1) + (i >> 1) * 8 < live) continue;
-      x[i] = -INFINITY;
-      vs[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < VW; ++j) v[i][j] = 0u;
-    }
-  }
-
-  // The running softmax and O += P V.  O is rescaled only when a row's max has grown
-  // by more than 2^8: the same reference scales numerator and sum.
-  __device__ __forceinline__ void add(const float (&x)[4], const float (&vs)[4],
-                                      const uint32_t (&v)[4][VW]) {
-    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-      const float to = fmaxf(m, mx);
-      const float alpha = to == -INFINITY ? 1.f : fast_exp2(m - to);
-      l *= alpha;
-      m = to;
-#pragma unroll
-      for (int n = 0; n < TILES; ++n) {
-        o[n][0] *= alpha, o[n][1] *= alpha, o[n][2] *= alpha, o[n][3] *= alpha;
-      }
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = fast_exp2(x[i] - ref);
-    l += (p[0] + p[1]) + (p[2] + p[3]);
-    if constexpr (F8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] *= vs[i];
-    }
-    const uint32_t hi0 = pack_bf16x2(p[0], p[1]), hi1 = pack_bf16x2(p[2], p[3]);
-    const float2 f0 = bf16x2_to_float2(hi0), f1 = bf16x2_to_float2(hi1);
-    const uint32_t lo0 = pack_bf16x2(p[0] - f0.x, p[1] - f0.y);
-    const uint32_t lo1 = pack_bf16x2(p[2] - f1.x, p[3] - f1.y);
-    if constexpr (F8) {
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        float f[4][4];  // [row][channel]
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a, b;
-          f16x2x2_from_e4m3x4(v[i][w], a, b);
-          const float2 fa = half2_bits_to_float2(a), fb = half2_bits_to_float2(b);
-          f[i][0] = fa.x, f[i][1] = fa.y, f[i][2] = fb.x, f[i][3] = fb.y;
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a0, a1, a2, a3;
+          f16x2x2_from_e4m3x4(w[2 * i], a0, a2);
+          f16x2x2_from_e4m3x4(w[2 * i + 1], a1, a3);
+          mma_f16_16816(c[i], a0, a1, a2, a3, q0[j + i], q2[j + i]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_bf16_16816(o[4 * w + j], hi0, lo0, hi1, lo1, pack_bf16x2(f[0][j], f[1][j]),
-                         pack_bf16x2(f[2][j], f[3][j]));
       }
     } else {
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        mma_bf16_16816(o[2 * w], hi0, lo0, hi1, lo1, __byte_perm(v[0][w], v[1][w], 0x5410),
-                       __byte_perm(v[2][w], v[3][w], 0x5410));
-        mma_bf16_16816(o[2 * w + 1], hi0, lo0, hi1, lo1, __byte_perm(v[0][w], v[1][w], 0x7632),
-                       __byte_perm(v[2][w], v[3][w], 0x7632));
+      for (int j = 0; j < STEPS; ++j) {  // 8 values a chunk, two chunks
+        uint32_t w[4];
+        ldmatrix4((at ^ ((2 * j & 7) << 4)) + (j >> 2) * 2048, w);
+        mma_bf16_16816(c[j & 1], w[0], w[1], w[2], w[3], q0[j], q2[j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (c[0][i] + c[1][i]) * mul;
+    if constexpr (F8) {
+      const int g = (threadIdx.x & 31) >> 2;
+      const float a = scales[g], b = scales[g + 8];
+      x[0] *= a * head_mul[0], x[1] *= a * head_mul[1];
+      x[2] *= b * head_mul[0], x[3] *= b * head_mul[1];
+    }
+  }
+
+  // Keys at and past `live` of the page are not seen.
+  __device__ __forceinline__ void hide(int live, float (&x)[4]) const {
+    const int g = (threadIdx.x & 31) >> 2;
+    if (g >= live) x[0] = x[1] = -INFINITY;
+    if (g + 8 >= live) x[2] = x[3] = -INFINITY;
+  }
+
+  // The running softmax and O^T += V^T P^T with the V page at v (its rows past the live ones
+  // are zeros).  The reference max follows only when a score is more than 2^8 above it: the
+  // same reference scales numerator and sum.
+  __device__ __forceinline__ void add(const float (&x)[4], uint32_t v, const float* scales) {
+    const int g = (threadIdx.x & 31) >> 2;
+    const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+    if (__any_sync(0xffffffffu, mx0 > m[0] + 8.f || mx1 > m[1] + 8.f)) {
+      float to[2] = {mx0, mx1};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o_ = 4; o_ < 32; o_ <<= 1)
+          to[i] = fmaxf(to[i], __shfl_xor_sync(0xffffffffu, to[i], o_));
+        to[i] = fmaxf(to[i], m[i]);
+        const float alpha = to[i] == -INFINITY ? 1.f : fast_exp2(m[i] - to[i]);
+        l[i] *= alpha;
+        m[i] = to[i];
+#pragma unroll
+        for (int n = 0; n < STEPS; ++n) o[n][i] *= alpha, o[n][i + 2] *= alpha;
+      }
+    }
+    const float r0 = m[0] == -INFINITY ? 0.f : m[0], r1 = m[1] == -INFINITY ? 0.f : m[1];
+    float p[4] = {fast_exp2(x[0] - r0), fast_exp2(x[1] - r1), fast_exp2(x[2] - r0),
+                  fast_exp2(x[3] - r1)};
+    l[0] += p[0] + p[2];
+    l[1] += p[1] + p[3];
+    if constexpr (F8) {
+      const float a = scales[16 + g], b = scales[24 + g];
+      p[0] *= a, p[1] *= a, p[2] *= b, p[3] *= b;
+    }
+    const uint32_t hi0 = pack_bf16x2(p[0], p[1]), hi1 = pack_bf16x2(p[2], p[3]);
+    const float2 f0 = bf16x2_to_float2(hi0), f1 = bf16x2_to_float2(hi1);
+    const uint32_t bh0 = movmatrix_trans(hi0), bh1 = movmatrix_trans(hi1);
+    const uint32_t bl0 = movmatrix_trans(pack_bf16x2(p[0] - f0.x, p[1] - f0.y));
+    const uint32_t bl1 = movmatrix_trans(pack_bf16x2(p[2] - f1.x, p[3] - f1.y));
+    const uint32_t at = v_lane(v);
+    if constexpr (F8) {
+      // a register: keys 2t and 2t + 1 (low and high half), codes 2g and 2g + 1 of a chunk;
+      // the even codes are the tile's rows 0-7, the odd ones rows 8-15
+#pragma unroll
+      for (int c = 0; c < STEPS; c += 2) {
+        uint32_t w[4];
+        ldmatrix4_trans(at ^ (c << 4), w);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a, b, a8, b8;
+          f16x2x2_from_e4m3x4(w[2 * i], a, b);
+          f16x2x2_from_e4m3x4(w[2 * i + 1], a8, b8);
+          const float2 fa = half2_bits_to_float2(a), fb = half2_bits_to_float2(b);
+          const float2 ga = half2_bits_to_float2(a8), gb = half2_bits_to_float2(b8);
+          const uint32_t a0 = pack_bf16x2(fa.x, fb.x), a1 = pack_bf16x2(fa.y, fb.y);
+          const uint32_t a2 = pack_bf16x2(ga.x, gb.x), a3 = pack_bf16x2(ga.y, gb.y);
+          mma_bf16_16816(o[c + i], a0, a1, a2, a3, bh0, bh1);
+          mma_bf16_16816(o[c + i], a0, a1, a2, a3, bl0, bl1);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < STEPS; ++n) {
+        uint32_t w[4];
+        ldmatrix4_trans((at ^ ((2 * n & 7) << 4)) + (n >> 2) * 2048, w);
+        mma_bf16_16816(o[n], w[0], w[1], w[2], w[3], bh0, bh1);
+        mma_bf16_16816(o[n], w[0], w[1], w[2], w[3], bl0, bl1);
       }
     }
   }
 
-  // The channel of column c (0 or 1) of O's tile n.
-  __device__ __forceinline__ int channel(int n, int c) const {
-    const int t = threadIdx.x & 3;
-    return F8 ? (2 * t + c) * (D / 8) + n : (n >> 3) * 64 + (2 * t + c) * 8 + (n & 7);
+  // The channel of the first or second row (0 or 1) of this lane in O^T's tile n.
+  __device__ __forceinline__ int channel(int n, int second) const {
+    const int g = (threadIdx.x & 31) >> 2;
+    return n * 16 + (F8 ? 2 * g + second : g + 8 * second);
   }
 };
 
-// A warp's piece of the result in shared memory, and the CTA's.
-template <int D, int G, int W>
-struct RowsShared {
-  float o[W][G][D];
-  float m[W][G], l[W][G];
-  float cta_m[G], cta_l[G];  // o[0] is the CTA's once cta_m is
-};
+// The stages of a warp's ring, in the order of its pages: stage c % STAGES, use c / STAGES.
+template <int D, bool F8, int ROOM>
+struct RowsStream {
+  using Ring = RowsRing<D, F8, ROOM>;
+  Ring& B;
+  unsigned char* smem;  // this warp's stages
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const CUtensorMap* kmap;
+  const CUtensorMap* vmap;
+  unsigned* err;
+  int n_kv, h, warp, lane;
+  uint32_t issued = 0;
 
-// Joins the warps' pieces, then the cluster's; writes G rows of out.  M, L: the rows'
-// reference max and sum over the whole cluster (for each head g, in shared memory of
-// every CTA afterwards: cta_m, cta_l).  Every thread of the cluster calls it.
-template <int D, int G, bool F8, int W>
-__device__ __forceinline__ void join_rows(RowsShared<D, G, W>& B, WarpRows<D, G, F8>& R,
-                                          uint32_t ctas, uint32_t rank, uint16_t* out) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
-  R.l += __shfl_xor_sync(0xffffffffu, R.l, 1);
-  R.l += __shfl_xor_sync(0xffffffffu, R.l, 2);
-  if (g < G) {
-#pragma unroll
-    for (int n = 0; n < WarpRows<D, G, F8>::TILES; ++n) {
-      B.o[warp][g][R.channel(n, 0)] = R.o[n][0] + R.o[n][2];
-      B.o[warp][g][R.channel(n, 1)] = R.o[n][1] + R.o[n][3];
+  // The copies of a page (of which the first `live` keys count) into the next stage,
+  // whose last page this warp has finished with.
+  __device__ __forceinline__ void issue(int page, int live, bool with_v) {
+    const uint32_t st = issued % Ring::STAGES;
+    const uint32_t bar = smem_addr(&B.full[warp][st]);
+    const uint32_t to = smem_addr(smem + st * Ring::STAGE);
+    if (lane == 0) {
+      B.live[warp][st] = live;
+      mbar_arrive_expect_tx(bar, with_v ? Ring::STAGE : Ring::PAGE);
+      const int z = F8 ? 0 : page * 16, w = F8 ? page : 0;
+      tma_load_page(to, kmap, h, z, w, bar);
+      if (with_v) tma_load_page(to + Ring::PAGE, vmap, h, z, w, bar);
     }
-    if ((lane & 3) == 0) B.m[warp][g] = R.m, B.l[warp][g] = R.l;
+    if constexpr (F8) {
+      const uint8_t* at = (lane < 16 ? kc : vc) + page * fp8_page_bytes(n_kv, D) +
+                          fp8_scales_offset(n_kv, D) + ((lane & 15) * n_kv + h) * 4;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                       smem_addr(&B.scales[warp][st][lane])),
+                   "l"(at)
+                   : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    }
+    ++issued;
   }
+  // Page c (all lanes): its stage's bytes and how many of its keys count.  The stage's
+  // next use is issued by this warp after it is done with this one, so the phase waited
+  // for is the current one or the one just completed.
+  __device__ __forceinline__ uint32_t wait(uint32_t c, int& live) {
+    const uint32_t st = c % Ring::STAGES;
+    mbar_wait(smem_addr(&B.full[warp][st]), (c / Ring::STAGES) & 1, err, &B.abort_flag);
+    live = B.live[warp][st];
+    return smem_addr(smem + st * Ring::STAGE);
+  }
+  __device__ __forceinline__ float* scales(uint32_t c) { return B.scales[warp][c % Ring::STAGES]; }
+  // Rows at and past `live` of the V page of page c hold anything: zeros from here on.
+  __device__ __forceinline__ void clear_v(uint32_t c, int live) {
+    unsigned char* v = smem + (c % Ring::STAGES) * Ring::STAGE + Ring::PAGE;
+    constexpr int HALVES = Ring::PAGE / (16 * Ring::ROW), CHUNKS = Ring::ROW / 16;
+    for (int i = lane; i < (16 - live) * CHUNKS * HALVES; i += 32) {
+      const int hf = i / ((16 - live) * CHUNKS), e = i % ((16 - live) * CHUNKS);
+      *reinterpret_cast<uint4*>(v + hf * 16 * Ring::ROW + (live + e / CHUNKS) * Ring::ROW +
+                                (e % CHUNKS) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (F8 && lane >= 16 + live) scales(c)[lane] = 0.f;
+    // (the stage's next copy comes behind these writes)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+  }
+};
+
+// What a CTA holds for the join of its warps' results (a warp's O lies where its ring
+// was) and of the cluster's: each CTA gets a slice of every CTA's O, and all maxima and
+// sums, written by their owners, so that one barrier of the cluster is all they wait for.
+constexpr int kRowsMaxCtas = 16;
+template <int D, int G>
+struct RowsShared {
+  float m[kRowsWarps][G], l[kRowsWarps][G];
+  float all_m[kRowsMaxCtas][G], all_l[kRowsMaxCtas][G];
+  float slice[G * D];    // [CTA][elements of this CTA]
+  float top[G], sum[G];  // the rows' reference max and sum over the cluster
+  int4 found;
+};
+
+// Joins the warps' pieces, then the cluster's; writes G rows of out; B.top and B.sum are
+// the rows' afterwards.  Every thread of the cluster calls it, each warp with nothing in
+// flight, after a cluster_arrive() of its own (more than one CTA).  smem: the warps' rings,
+// STRIDE bytes each.
+template <int STRIDE, int D, int G, bool F8>
+__device__ __forceinline__ void join_rows(RowsShared<D, G>& B, WarpRows<D, G, F8>& R,
+                                          unsigned char* smem, uint32_t ctas, uint32_t rank,
+                                          uint16_t* out) {
+  constexpr int W = kRowsWarps;
+  static_assert(STRIDE >= G * D * 4, "a warp's O in the place of its ring");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane & 3;
+  const auto o_of = [&](int w) { return reinterpret_cast<float*>(smem + w * STRIDE); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) R.l[i] += __shfl_xor_sync(0xffffffffu, R.l[i], o);
+    const int h = 2 * t + i;
+    if (h < G) {
+      float* o = o_of(warp) + h * D;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        o[R.channel(n, 0)] = R.o[n][i];
+        o[R.channel(n, 1)] = R.o[n][i + 2];
+      }
+      if (lane < 4) B.m[warp][h] = R.m[i], B.l[warp][h] = R.l[i];
+    }
+  }
+  if (ctas > 1) cluster_wait();  // (every CTA of the cluster runs: it may be written to)
   __syncthreads();
+  const int per = G * D / (int)ctas;  // elements of a CTA's slice
   for (int i = tid; i < G * D; i += W * 32) {
     const int h = i / D, c = i % D;
     float top = B.m[0][h];
@@ -344,48 +424,64 @@ __device__ __forceinline__ void join_rows(RowsShared<D, G, W>& B, WarpRows<D, G,
       const float f = B.m[w][h] == -INFINITY ? 0.f : fast_exp2(B.m[w][h] - top);
       // (a piece that saw nothing has sum 0, and a sum that is NaN stays so)
       sum += f * B.l[w][h];
-      acc += f * B.o[w][h][c];
+      acc += f * o_of(w)[i];
     }
-    B.o[0][h][c] = acc;  // (only this thread reads this element of any warp's)
-    if (c == 0) B.cta_m[h] = top, B.cta_l[h] = sum;
-    if (ctas == 1) out[i] = float_to_bf16_rn(sum == 0.f ? 0.f : acc / sum);
+    if (ctas == 1) {
+      if (c == 0) B.top[h] = top, B.sum[h] = sum;
+      out[i] = float_to_bf16_rn(sum == 0.f ? 0.f : acc / sum);
+    } else {
+      st_cluster_f32(cluster_addr(smem_addr(&B.slice[(int)rank * per + i % per]), i / per), acc);
+      // (the threads of a head's first channels tell one CTA each its max and sum)
+      if (c < (int)ctas) {
+        st_cluster_f32(cluster_addr(smem_addr(&B.all_m[rank][h]), c), top);
+        st_cluster_f32(cluster_addr(smem_addr(&B.all_l[rank][h]), c), sum);
+      }
+    }
   }
   if (ctas == 1) {
     __syncthreads();
     return;
   }
   cluster_sync();
-  const int per = G * D / (int)ctas;
-  float top_all[G], sum_all[G];
-#pragma unroll
-  for (int h = 0; h < G; ++h) {
-    top_all[h] = -INFINITY;
-    sum_all[h] = 0.f;
-    for (uint32_t r = 0; r < ctas; ++r)
-      top_all[h] = fmaxf(top_all[h], ld_cluster_f32(cluster_addr(smem_addr(&B.cta_m[h]), r)));
+  for (int e = tid; e < per; e += W * 32) {
+    const int i = (int)rank * per + e, h = i / D;
+    float top = -INFINITY;
+    for (uint32_t r = 0; r < ctas; ++r) top = fmaxf(top, B.all_m[r][h]);
+    float sum = 0.f, acc = 0.f;
     for (uint32_t r = 0; r < ctas; ++r) {
-      const float m = ld_cluster_f32(cluster_addr(smem_addr(&B.cta_m[h]), r));
-      sum_all[h] += (m == -INFINITY ? 0.f : fast_exp2(m - top_all[h])) *
-                    ld_cluster_f32(cluster_addr(smem_addr(&B.cta_l[h]), r));
-    }
-  }
-  for (int i = (int)rank * per + tid; i < (int)(rank + 1) * per; i += W * 32) {
-    const int h = i / D;
-    float top = -INFINITY, sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-      if (j == h) top = top_all[j], sum = sum_all[j];
-    for (uint32_t r = 0; r < ctas; ++r) {
-      const float m = ld_cluster_f32(cluster_addr(smem_addr(&B.cta_m[h]), r));
-      acc += (m == -INFINITY ? 0.f : fast_exp2(m - top)) *
-             ld_cluster_f32(cluster_addr(smem_addr(&B.o[0][0][0] + i), r));
+      const float m = B.all_m[r][h], f = m == -INFINITY ? 0.f : fast_exp2(m - top);
+      sum += f * B.all_l[r][h];
+      acc += f * B.slice[r * per + e];
     }
     out[i] = float_to_bf16_rn(sum == 0.f ? 0.f : acc / sum);
   }
-  cluster_sync();  // no CTA leaves, or changes its numbers, while they are read
-  if (tid == 0) {
-#pragma unroll
-    for (int h = 0; h < G; ++h) B.cta_m[h] = top_all[h], B.cta_l[h] = sum_all[h];
+  if (tid < G) {
+    float top = -INFINITY, sum = 0.f;
+    for (uint32_t r = 0; r < ctas; ++r) top = fmaxf(top, B.all_m[r][tid]);
+    for (uint32_t r = 0; r < ctas; ++r) {
+      const float m = B.all_m[r][tid];
+      sum += (m == -INFINITY ? 0.f : fast_exp2(m - top)) * B.all_l[r][tid];
+    }
+    B.top[tid] = top, B.sum[tid] = sum;
+  }
+  __syncthreads();
+}
+
+// Barriers of the CTA's rings (every thread; before any other use), and the tensor maps on
+// their way ahead of the first copy.
+template <int D, bool F8, int ROOM>
+__device__ __forceinline__ void init_rings(RowsRing<D, F8, ROOM>& B, int4* found,
+                                           const CUtensorMap* kmap, const CUtensorMap* vmap) {
+  using Ring = RowsRing<D, F8, ROOM>;
+  if (threadIdx.x == 0) {
+    found->x = -1;
+    for (int w = 0; w < kRowsWarps; ++w)
+      for (int i = 0; i < Ring::STAGES; ++i) mbar_init(smem_addr(&B.full[w][i]), F8 ? 33 : 1);
+    B.abort_flag = 0;
+    fence_mbar_init();
+  } else if (threadIdx.x == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(vmap)) : "memory");
   }
   __syncthreads();
 }

@@ -11,92 +11,125 @@
 #include <cstdint>
 
 #include "pa_rows.cuh"
+#include "pa_tma_host.h"
 
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
+// CTAs of an SM, and the bytes of a warp's ring that leaves.
+template <int D, bool F8>
+constexpr int kCtas = D == 128 && !F8 ? 3 : 5;
+template <int D, bool F8>
+constexpr int kRing = (D == 128 && !F8 ? 16 : 8) * 1024;
 
 template <int D, int G, bool F8>
-__global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const SparseArgs p) {
-  using Rows = WarpRows<D, G, F8>;
-  __shared__ RowsShared<D, G, kWarps> B;
+__global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
+    sparse_kernel(const SparseArgs p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+  using Ring = RowsRing<D, F8, kRing<D, F8>>;
+  extern __shared__ __align__(1024) unsigned char rings[];
+  __shared__ Ring B;
+  __shared__ RowsShared<D, G> J;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ctas = cluster_size(), rank = cluster_rank();
   const long long unit = blockIdx.x / ctas;
   const int h = (int)(unit % p.n_kv), t = (int)(unit / p.n_kv);
+  init_rings(B, &J.found, &kmap, &vmap);
   after_prior_kernels();
+  const int32_t* list = p.selected + ((int64_t)t * p.n_kv + h) * p.num_selected;
+  const int pages = p.num_selected << p.block_shift;
+  const int stride = (int)ctas * kRowsWarps;
+  // lane i has the warp's i-th page of the list; the first ones are on their way while the
+  // request is found
+  int base = (int)rank * kRowsWarps + warp + lane * stride;
+  int entry = base < pages ? list[base >> p.block_shift] : -1;
   TokenRequest req;
   if (!find_request(p.query_start_loc, p.seq_lens, p.num_seqs, p.num_tokens,
                     ((long long)p.max_blocks << p.block_shift) * 16, t, p.err,
-                    threadIdx.x == 0 && rank == 0 && h == 0, req))
+                    threadIdx.x == 0 && rank == 0 && h == 0, &J.found, req))
     return;
+  if (ctas > 1) cluster_arrive();
   const int32_t* table = p.block_tables + (int64_t)req.s * p.max_blocks;
-  const int32_t* list = p.selected + ((int64_t)t * p.n_kv + h) * p.num_selected;
-  const int pages = p.num_selected << p.block_shift;
   const int half = (1 << p.block_shift) - 1;  // 16-token pages of a block, less one
-  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
-  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
-  const int64_t page_bytes = Rows::page_bytes(p.n_kv);
-
-  Rows R;
-  R.begin(p.q + ((int64_t)t * p.n_kv + h) * G * D, p.scale_log2);
-  const int stride = (int)ctas * kWarps;
-  for (int base = (int)rank * kWarps + warp; base < pages; base += 32 * stride) {
-    // lane i looks up the warp's i-th page from here
-    const int i = base + lane * stride;
-    int page = -1, live = 0;
-    if (i < pages) {
-      const int e = list[i >> p.block_shift];
-      if (e > req.pos >> (4 + p.block_shift)) {
+  RowsStream<D, F8, kRing<D, F8>> S{
+      B,     rings + warp * Ring::BYTES, static_cast<const uint8_t*>(p.k_cache),
+      static_cast<const uint8_t*>(p.v_cache), &kmap, &vmap, p.err, p.n_kv, h, warp, lane};
+  int page = -1, live = 0;
+  unsigned todo = 0;  // lanes that hold pages to come
+  const auto issue_next = [&] {
+    while (!todo) {
+      if (base - lane * stride >= pages) return;
+      page = -1;
+      if (entry > req.pos >> (4 + p.block_shift)) {
         flag_error(p.err, DEVERR_BOUNDS);
-      } else if (e >= 0) {
-        const int b = table[e];
-        live = req.pos + 1 - (((e << p.block_shift) + (i & half)) << 4);
+      } else if (entry >= 0) {
+        const int b = table[entry];
+        live = req.pos + 1 - (((entry << p.block_shift) + (base & half)) << 4);
         if (b < 0 || b >= p.num_blocks)
           flag_error(p.err, DEVERR_BOUNDS);
         else if (live > 0)
-          page = (b << p.block_shift) + (i & half);
+          page = (b << p.block_shift) + (base & half);
       }
+      base += 32 * stride;
+      entry = base < pages ? list[base >> p.block_shift] : -1;
+      todo = __ballot_sync(0xffffffffu, page >= 0);
     }
-    unsigned todo = __ballot_sync(0xffffffffu, page >= 0);
-    if (!todo) continue;
-    int at = __ffs(todo) - 1;
-    int64_t off = __shfl_sync(0xffffffffu, page, at) * page_bytes;
-    R.load_k(kc + off, vc + off, p.n_kv, h);
-    while (todo) {
-      todo &= todo - 1;
-      const int n = __shfl_sync(0xffffffffu, live, at);
-      uint32_t v[4][Rows::VW];
-      R.load_v(vc + off, p.n_kv, h, v);
-      float x[4], vs[4] = {0.f, 0.f, 0.f, 0.f};
-      R.scores(x, vs);
-      if (todo) {
-        at = __ffs(todo) - 1;
-        off = __shfl_sync(0xffffffffu, page, at) * page_bytes;
-        R.load_k(kc + off, vc + off, p.n_kv, h);
-      }
-      if (n < 16) R.hide(n, x, vs, v);
-      R.add(x, vs, v);
+    const int at = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int pg = __shfl_sync(0xffffffffu, page, at);
+    const int lv = __shfl_sync(0xffffffffu, live, at);
+    S.issue(pg, lv, true);
+  };
+#pragma unroll 1
+  for (int i = 0; i < Ring::STAGES; ++i) issue_next();
+  WarpRows<D, G, F8> R;
+  R.begin(p.q + ((int64_t)t * p.n_kv + h) * G * D, p.scale_log2);
+  for (uint32_t c = 0; c < S.issued; ++c) {
+    int n;
+    const uint32_t at = S.wait(c, n);
+    float x[4];
+    R.scores(at, S.scales(c), x);
+    if (n < 16) {
+      R.hide(n, x);
+      S.clear_v(c, n);
     }
+    R.add(x, at + Ring::PAGE, S.scales(c));
+    __syncwarp();  // the stage has been read
+    issue_next();
   }
-  join_rows<D, G, F8, kWarps>(B, R, ctas, rank, p.out + ((int64_t)t * p.n_kv + h) * G * D);
+  join_rows<Ring::BYTES, D, G, F8>(J, R, rings, ctas, rank,
+                                   p.out + ((int64_t)t * p.n_kv + h) * G * D);
 }
 
-template <int D, int G>
+template <int D, int G, bool F8>
 cudaError_t launch_t(const SparseArgs& p, int ctas, cudaStream_t stream) {
+  CUtensorMap km, vm;
+  const int64_t pages = (int64_t)p.num_blocks << p.block_shift;
+  cudaError_t e = encode_page_map(&km, p.k_cache, F8, pages, p.n_kv, D);
+  if (e == cudaSuccess) e = encode_page_map(&vm, p.v_cache, F8, pages, p.n_kv, D);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = kRowsWarps * RowsRing<D, F8, kRing<D, F8>>::BYTES;
+  auto kern = sparse_kernel<D, G, F8>;
+  if (ctas > 8) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)p.num_tokens * p.n_kv * ctas));
-  return p.fp8 ? launch_early(sparse_kernel<D, G, true>, grid, dim3(kWarps * 32), 0, stream, ctas, p)
-               : launch_early(sparse_kernel<D, G, false>, grid, dim3(kWarps * 32), 0, stream, ctas,
-                              p);
+  return launch_early(kern, grid, dim3(kRowsWarps * 32), smem, stream, ctas, p, km, vm);
+}
+template <int D, int G>
+cudaError_t launch_f(const SparseArgs& p, int ctas, cudaStream_t stream) {
+  return p.fp8 ? launch_t<D, G, true>(p, ctas, stream) : launch_t<D, G, false>(p, ctas, stream);
 }
 template <int D>
 cudaError_t launch_d(const SparseArgs& p, int ctas, cudaStream_t stream) {
   switch (p.group) {
-    case 1: return launch_t<D, 1>(p, ctas, stream);
-    case 2: return launch_t<D, 2>(p, ctas, stream);
-    case 4: return launch_t<D, 4>(p, ctas, stream);
-    default: return launch_t<D, 8>(p, ctas, stream);
+    case 1: return launch_f<D, 1>(p, ctas, stream);
+    case 2: return launch_f<D, 2>(p, ctas, stream);
+    case 4: return launch_f<D, 4>(p, ctas, stream);
+    default: return launch_f<D, 8>(p, ctas, stream);
   }
 }
 
@@ -106,7 +139,8 @@ cudaError_t launch_sparse(const SparseArgs& p, int sm_count, cudaStream_t stream
   const long long units = (long long)p.num_tokens * p.n_kv;
   const long long pages = (long long)p.num_selected << p.block_shift;
   int ctas = 1;
-  while (ctas < 8 && units * ctas < 4ll * sm_count && pages > 2ll * ctas * kWarps) ctas *= 2;
+  while (ctas < kRowsMaxCtas && units * ctas < sm_count && pages > 2ll * ctas * kRowsWarps)
+    ctas *= 2;
   return p.head_dim == 128 ? launch_d<128>(p, ctas, stream) : launch_d<64>(p, ctas, stream);
 }
 

@@ -12,25 +12,37 @@
 #include <cstdint>
 
 #include "pa_rows.cuh"
+#include "pa_tma_host.h"
 
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
+// CTAs of an SM (with short contexts; the scores of long ones take the room of some),
+// and the bytes of a warp's ring.
+template <int D, bool F8>
+constexpr int kCtas = D == 128 && !F8 ? 3 : 5;
+template <int D, bool F8>
+constexpr int kRing = (D == 128 && !F8 ? 16 : 8) * 1024;
 
 template <int D, int G, bool F8>
-__global__ void __launch_bounds__(kWarps * 32) weigh_kernel(const WeighArgs p) {
-  using Rows = WarpRows<D, G, F8>;
-  extern __shared__ __align__(16) float scores_s[];  // [key of the CTA's first pages][G]
-  __shared__ RowsShared<D, G, kWarps> B;
+__global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
+    weigh_kernel(const WeighArgs p, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  using Ring = RowsRing<D, F8, kRing<D, F8>>;
+  constexpr int W = kRowsWarps;
+  extern __shared__ __align__(1024) unsigned char rings[];
+  float* scores_s = reinterpret_cast<float*>(rings + W * Ring::BYTES);  // [key of the CTA][G]
+  __shared__ Ring B;
+  __shared__ RowsShared<D, G> J;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
   const uint32_t ctas = cluster_size(), rank = cluster_rank();
   const long long unit = blockIdx.x / ctas;
   const int h = (int)(unit % p.n_kv), s = (int)(unit / p.n_kv);
+  init_rings(B, &J.found, &kmap, &vmap);
   after_prior_kernels();
   const int token = p.query_start_loc[s], rows = p.query_start_loc[s + 1] - token;
-  if (rows == 0) return;
   const int L = p.seq_lens[s];
+  if (rows == 0) return;
   const bool report = threadIdx.x == 0 && rank == 0 && h == 0;
   if (rows < 0 || (rows > 1 && !p.chunks)) {
     if (report) flag_error(p.err, DEVERR_BOUNDS);
@@ -42,60 +54,70 @@ __global__ void __launch_bounds__(kWarps * 32) weigh_kernel(const WeighArgs p) {
     if (report) flag_error(p.err, DEVERR_BOUNDS);
     return;
   }
+  if (ctas > 1) cluster_arrive();
   const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
   const int half = (1 << p.block_shift) - 1;
-  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
-  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
-  const int64_t page_bytes = Rows::page_bytes(p.n_kv);
   const int all = (L + 15) >> 4;
   const int per = (all + (int)ctas - 1) / (int)ctas;
   const int first = min((int)rank * per, all), pages = min(per, all - first);
-  // The pool's page of this CTA's page i, or -1.
-  const auto look_up = [&](int i, bool report_it) {
-    const int lp = first + i;
-    const int b = table[lp >> p.block_shift];
-    if (b >= 0 && b < p.num_blocks) return (b << p.block_shift) + (lp & half);
-    if (report_it) flag_error(p.err, DEVERR_BOUNDS);
-    return -1;
-  };
-  const auto live_of = [&](int i) { return L - ((first + i) << 4); };
-
-  Rows R;
-  R.begin(p.q + ((int64_t)token * p.n_kv + h) * G * D, p.scale_log2);
-  for (int base = warp; base < pages; base += 32 * kWarps) {
-    const int i = base + lane * kWarps;
-    const int page = i < pages ? look_up(i, true) : -1;
-    unsigned todo = __ballot_sync(0xffffffffu, page >= 0);
-    // (pages that are not there weigh nothing)
-    if (page < 0 && i < min(pages, p.kept_pages))
-      for (int e = 0; e < 16 * G; ++e) scores_s[i * 16 * G + e] = -INFINITY;
-    if (!todo) continue;
-    int at = __ffs(todo) - 1;
-    int64_t off = __shfl_sync(0xffffffffu, page, at) * page_bytes;
-    R.load_k(kc + off, vc + off, p.n_kv, h);
-    while (todo) {
-      todo &= todo - 1;
-      const int mine = base + at * kWarps;
-      uint32_t v[4][Rows::VW];
-      R.load_v(vc + off, p.n_kv, h, v);
-      float x[4], vs[4] = {0.f, 0.f, 0.f, 0.f};
-      R.scores(x, vs);
-      if (todo) {
-        at = __ffs(todo) - 1;
-        off = __shfl_sync(0xffffffffu, page, at) * page_bytes;
-        R.load_k(kc + off, vc + off, p.n_kv, h);
+  RowsStream<D, F8, kRing<D, F8>> S{
+      B,     rings + warp * Ring::BYTES, static_cast<const uint8_t*>(p.k_cache),
+      static_cast<const uint8_t*>(p.v_cache), &kmap, &vmap, p.err, p.n_kv, h, warp, lane};
+  // The warp's pages of this CTA: base, base + W, ...  Those that the table has no block
+  // for weigh nothing.
+  int base = warp, page = -1, next = 0;
+  unsigned todo = 0;
+  const auto issue_next = [&](bool with_v) {
+    while (!todo) {
+      if (base >= pages) return;
+      const int i = base + lane * W;
+      next = base;
+      base += 32 * W;
+      page = -1;
+      if (i < pages) {
+        const int b = table[(first + i) >> p.block_shift];
+        if (b >= 0 && b < p.num_blocks) {
+          page = (b << p.block_shift) + ((first + i) & half);
+        } else if (with_v) {
+          flag_error(p.err, DEVERR_BOUNDS);
+          if (i < p.kept_pages)
+            for (int e = 0; e < 16 * G; ++e) scores_s[i * 16 * G + e] = -INFINITY;
+        }
       }
-      const int n = live_of(mine);
-      if (n < 16) R.hide(n, x, vs, v);
-      if (mine < p.kept_pages && g < G) {
-        float* to = scores_s + mine * 16 * G + g;
-        to[(2 * t) * G] = x[0], to[(2 * t + 1) * G] = x[1];
-        to[(2 * t + 8) * G] = x[2], to[(2 * t + 9) * G] = x[3];
-      }
-      R.add(x, vs, v);
+      todo = __ballot_sync(0xffffffffu, page >= 0);
     }
+    const int at = __ffs(todo) - 1;
+    todo &= todo - 1;
+    // (`live` here is the page's place among the CTA's)
+    const int pg = __shfl_sync(0xffffffffu, page, at);
+    S.issue(pg, next + at * W, with_v);
+  };
+#pragma unroll 1
+  for (int i = 0; i < Ring::STAGES; ++i) issue_next(true);
+  WarpRows<D, G, F8> R;
+  R.begin(p.q + ((int64_t)token * p.n_kv + h) * G * D, p.scale_log2);
+  uint32_t c = 0;
+  for (; c < S.issued; ++c) {
+    int mine;
+    const uint32_t at = S.wait(c, mine);
+    float x[4];
+    R.scores(at, S.scales(c), x);
+    const int n = L - ((first + mine) << 4);
+    if (n < 16) {
+      R.hide(n, x);
+      S.clear_v(c, n);
+    }
+    if (mine < p.kept_pages && 2 * t < G) {
+      float* to = scores_s + (mine * 16 + g) * G + 2 * t;
+      to[0] = x[0], to[8 * G] = x[2];
+      if (G > 1) to[1] = x[1], to[8 * G + 1] = x[3];
+    }
+    R.add(x, at + Ring::PAGE, S.scales(c));
+    __syncwarp();  // the stage has been read
+    issue_next(true);
   }
-  join_rows<D, G, F8, kWarps>(B, R, ctas, rank, p.out + ((int64_t)token * p.n_kv + h) * G * D);
+  join_rows<Ring::BYTES, D, G, F8>(J, R, rings, ctas, rank,
+                                   p.out + ((int64_t)token * p.n_kv + h) * G * D);
 
   // the weights of this CTA's keys
   float* w = p.weights + ((int64_t)s * p.n_kv + h) * p.weights_stride + (first << 4);
@@ -104,9 +126,9 @@ __global__ void __launch_bounds__(kWarps * 32) weigh_kernel(const WeighArgs p) {
   {
     float m[G], inv[G];
 #pragma unroll
-    for (int i = 0; i < G; ++i) m[i] = B.cta_m[i], inv[i] = 1.f / B.cta_l[i];
+    for (int i = 0; i < G; ++i) m[i] = J.top[i], inv[i] = 1.f / J.sum[i];
     const int kept = min(keys, p.kept_pages << 4);
-    for (int j = threadIdx.x; j < kept; j += kWarps * 32) {
+    for (int j = threadIdx.x; j < kept; j += W * 32) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -117,58 +139,85 @@ __global__ void __launch_bounds__(kWarps * 32) weigh_kernel(const WeighArgs p) {
     }
   }
   if (pages <= p.kept_pages) return;
-  const float m = g < G ? B.cta_m[g] : 0.f, inv = g < G ? 1.f / B.cta_l[g] : 0.f;
-  for (int i = p.kept_pages + warp; i < pages; i += kWarps) {
-    const int page = look_up(i, false);
-    if (page < 0) continue;
-    const int64_t off = page * page_bytes;
-    R.load_k(kc + off, vc + off, p.n_kv, h);
-    float x[4], vs[4];
-    R.scores(x, vs);
-    float sum[4];
+  float m[2], inv[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      sum[c] = g < G && x[c] != -INFINITY ? fast_exp2(x[c] - m) * inv : 0.f;
+  for (int i = 0; i < 2; ++i) {
+    m[i] = 2 * t + i < G ? J.top[2 * t + i] : 0.f;
+    inv[i] = 2 * t + i < G ? 1.f / J.sum[2 * t + i] : 0.f;
+  }
+  // (the rings' places held the warps' results: copies come behind those)
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  base = p.kept_pages + warp;
+  todo = 0;
+#pragma unroll 1
+  for (int i = 0; i < Ring::STAGES; ++i) issue_next(false);
+  for (; c < S.issued; ++c) {
+    int mine;
+    const uint32_t at = S.wait(c, mine);
+    float x[4];
+    R.scores(at, S.scales(c), x);
+    // (a head of no query has scores 0 and no part in the sums)
+    float sum[2];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], o);
+    for (int i = 0; i < 2; ++i) {
+      sum[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (2 * t + k < G && x[2 * i + k] != -INFINITY)
+          sum[i] += fast_exp2(x[2 * i + k] - m[k]) * inv[k];
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
     }
-    if (g == 0) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int j = i * 16 + 2 * t + (c & 1) + (c >> 1) * 8;
-        if (j < keys) w[j] = (j == fresh ? 0.f : w[j]) + sum[c];
-      }
+    if (t < 2) {
+      const int j = mine * 16 + g + 8 * t;
+      const float add = t ? sum[1] : sum[0];
+      if (j < keys) w[j] = (j == fresh ? 0.f : w[j]) + add;
     }
+    __syncwarp();
+    issue_next(false);
   }
 }
 
-// Shared memory for scores: what three CTAs of an SM can have beside the rest.
-constexpr size_t kScoreBytes = 48 * 1024;
+// Shared memory for scores beside the rings, at most.
+constexpr size_t kScoreBytes = 44 * 1024;
 
-template <int D, int G>
+template <int D, int G, bool F8>
 cudaError_t launch_t(WeighArgs p, int ctas, cudaStream_t stream) {
+  CUtensorMap km, vm;
+  const int64_t all = (int64_t)p.num_blocks << p.block_shift;
+  cudaError_t e = encode_page_map(&km, p.k_cache, F8, all, p.n_kv, D);
+  if (e == cudaSuccess) e = encode_page_map(&vm, p.v_cache, F8, all, p.n_kv, D);
+  if (e != cudaSuccess) return e;
   const int pages = (p.max_seq_len + 15) / 16;
   const int share = (pages + ctas - 1) / ctas;
   const int most = (int)(kScoreBytes / (16 * G * sizeof(float)));
   p.kept_pages = share < most ? share : most;
-  const size_t smem = (size_t)p.kept_pages * 16 * G * sizeof(float);
-  auto kern = p.fp8 ? weigh_kernel<D, G, true> : weigh_kernel<D, G, false>;
-  if (smem > 16 * 1024) {
-    // (always the most any call takes, so that calls on other threads agree)
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)kScoreBytes);
+  constexpr size_t ring = kRowsWarps * RowsRing<D, F8, kRing<D, F8>>::BYTES;
+  const size_t smem = ring + (size_t)p.kept_pages * 16 * G * sizeof(float);
+  auto kern = weigh_kernel<D, G, F8>;
+  if (ctas > 8) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
+  // (always the most any call takes, so that calls on other threads agree)
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(ring + kScoreBytes));
+  if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)p.num_seqs * p.n_kv * ctas));
-  return launch_early(kern, grid, dim3(kWarps * 32), smem, stream, ctas, p);
+  return launch_early(kern, grid, dim3(kRowsWarps * 32), smem, stream, ctas, p, km, vm);
+}
+template <int D, int G>
+cudaError_t launch_f(const WeighArgs& p, int ctas, cudaStream_t stream) {
+  return p.fp8 ? launch_t<D, G, true>(p, ctas, stream) : launch_t<D, G, false>(p, ctas, stream);
 }
 template <int D>
 cudaError_t launch_d(const WeighArgs& p, int ctas, cudaStream_t stream) {
   switch (p.group) {
-    case 1: return launch_t<D, 1>(p, ctas, stream);
-    case 2: return launch_t<D, 2>(p, ctas, stream);
-    case 4: return launch_t<D, 4>(p, ctas, stream);
-    default: return launch_t<D, 8>(p, ctas, stream);
+    case 1: return launch_f<D, 1>(p, ctas, stream);
+    case 2: return launch_f<D, 2>(p, ctas, stream);
+    case 4: return launch_f<D, 4>(p, ctas, stream);
+    default: return launch_f<D, 8>(p, ctas, stream);
   }
 }
 
@@ -178,8 +227,8 @@ cudaError_t launch_weigh(const WeighArgs& p, int sm_count, cudaStream_t stream) 
   const long long units = (long long)p.num_seqs * p.n_kv;
   const long long pages = ((long long)p.max_seq_len + 15) / 16;
   int ctas = 1;
-  while (ctas < 8 && pages > 2ll * ctas * kWarps &&
-         (units * ctas < 4ll * sm_count || pages > 64ll * ctas * kWarps))
+  while (ctas < kRowsMaxCtas && pages > 2ll * ctas * kRowsWarps &&
+         (units * ctas < 2ll * sm_count || pages > 192ll * ctas))
     ctas *= 2;
   return p.head_dim == 128 ? launch_d<128>(p, ctas, stream) : launch_d<64>(p, ctas, stream);
 }

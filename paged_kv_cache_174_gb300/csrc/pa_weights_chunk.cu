@@ -20,12 +20,12 @@
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
-#include <mutex>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_select.cuh"
 #include "pa_tcgen05.cuh"
+#include "pa_tma_host.h"
 
 namespace pa {
 namespace {
@@ -534,37 +534,6 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
   }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
-
-cudaError_t make_map(CUtensorMap* m, const void* ptr, const cuuint64_t (&dims)[3],
-                     const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3]) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims,
-                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int D, int G, bool F8, bool COLS>
 cudaError_t launch_pass(const ChunkArgs& p, const CUtensorMap& qm, const CUtensorMap& km, int grid,
                         int ctas, cudaStream_t stream) {
@@ -588,7 +557,8 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
     const cuuint64_t dims[3] = {D, (cuuint64_t)p.n_q, (cuuint64_t)p.num_tokens};
     const cuuint64_t strides[2] = {D * 2, (cuuint64_t)p.n_q * D * 2};
     const cuuint32_t box[3] = {64, G, kTile / G};
-    const cudaError_t e = make_map(&qm, p.q, dims, strides, box);
+    const cudaError_t e = encode_map<3>(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, dims, strides,
+                                        box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
   km = qm;
@@ -596,7 +566,8 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
     const cuuint64_t dims[3] = {D, nkv, slots};
     const cuuint64_t strides[2] = {D * 2, nkv * D * 2};
     const cuuint32_t box[3] = {64, 1, 16};
-    const cudaError_t e = make_map(&km, p.k_cache, dims, strides, box);
+    const cudaError_t e = encode_map<3>(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k_cache, dims,
+                                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
   const long long slots_of_sms = 2ll * sm_count;
