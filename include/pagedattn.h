@@ -562,7 +562,7 @@ int pa_summarize_blocks_fp8(const uint8_t *k_cache, int32_t num_blocks, int32_t 
  *                 an upper bound of q k over the block's keys, but for the
  *                 rounding of q.  The sums are of integers and exact, so the
  *                 result depends on nothing but the inputs.
- *   max_seq_len   at most 393216 blocks
+ *   max_seq_len   at most 49152 blocks
  * The product is with q as it is given (scale the scores and they keep their
  * order).
  */

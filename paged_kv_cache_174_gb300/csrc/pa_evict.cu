@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs p) {
   __syncthreads();
   Threshold th{0xffffffffu, 0u};
   if (K > 0)
-    th = select_threshold(B.select, last - first, (uint32_t)K, 1u,
+    th = select_threshold(B.select, last - first, (uint32_t)K,
                           [&](int i) { return key(first + i); });
   for (int k = warp; k < nw; k += kThreads / 32) {
     const int j = k * 32 + lane;

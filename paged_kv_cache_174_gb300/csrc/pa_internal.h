@@ -247,10 +247,11 @@ struct BoundsArgs {
   float* scales;                   // [num_blocks, n_kv]
   unsigned* err;
   long long slots;  // (set by the launcher) places for a (request, block)
+  int32_t heads;    // (set by the launcher) kv heads that a warp takes in turn
   int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_kv, head_dim, block_log2;
   bool fp8;
 };
-cudaError_t launch_bounds(BoundsArgs p, cudaStream_t stream);
+cudaError_t launch_bounds(BoundsArgs p, int sm_count, cudaStream_t stream);
 
 // The blocks that each query attends to (pa_blocks.cu).
 struct SelectArgs {
@@ -264,10 +265,12 @@ struct SelectArgs {
   unsigned* err;
   int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_kv, group, head_dim, block_log2;
   int32_t num_selected, num_sinks, num_recent, max_seq_len;
+  int32_t max_keys;  // (set by the launcher) blocks of max_seq_len
 };
-constexpr int kSelectMaxShare = 48 * 1024;  // blocks of a CTA, four bytes of shared memory each
-constexpr int kSelectMaxCtas = 8;
-cudaError_t launch_select(const SelectArgs& p, int sm_count, cudaStream_t stream);
+// Blocks of a request: a key each in shared memory, and an eighth of the table.
+constexpr int kSelectMaxBlocks = 48 * 1024;
+constexpr int kSelectSmem = kSelectMaxBlocks / 8 * 9 * 4;
+cudaError_t launch_select(SelectArgs p, int sm_count, cudaStream_t stream);
 
 // Attention over chosen blocks (pa_sparse.cu).
 struct SparseArgs {

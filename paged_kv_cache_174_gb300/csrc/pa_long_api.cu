@@ -97,10 +97,11 @@ int summarize_impl(const void* k_cache, bool fp8, int32_t num_blocks, int32_t bl
   a.head_dim = head_dim;
   a.block_log2 = log2_of(block_size);
   a.fp8 = fp8;
-  st = pa::api_device_state(&a.err, nullptr);
+  int sms = 0;
+  st = pa::api_device_state(&a.err, &sms);
   if (st) return st;
   pa::NvtxRange range("bounds of the blocks' keys");
-  const cudaError_t e = pa::launch_bounds(a, stream);
+  const cudaError_t e = pa::launch_bounds(a, sms, stream);
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "summarize_blocks launch");
 }
 
@@ -401,9 +402,9 @@ int pa_select_blocks(const pa_bf16* q, const int8_t* bounds, const float* bound_
                     num_selected, num_sinks, num_recent);
   st = check_units((int64_t)num_tokens * num_kv_heads);
   if (st) return st;
-  if ((int64_t)max_seq_len > (int64_t)pa::kSelectMaxShare * pa::kSelectMaxCtas * block_size)
+  if ((int64_t)max_seq_len > (int64_t)pa::kSelectMaxBlocks * block_size)
     return api_fail(PA_ERR_UNSUPPORTED, "max_seq_len %d (at most %d blocks)", max_seq_len,
-                    pa::kSelectMaxShare * pa::kSelectMaxCtas);
+                    pa::kSelectMaxBlocks);
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
   if (!q || !bounds || !bound_scales || !block_tables || !seq_lens || !query_start_loc ||
       !selected)

@@ -1,12 +1,13 @@
-// pa_select.cuh -- the K largest of n 32-bit keys spread over the CTAs of a cluster
-// (used by the choice of blocks and by the eviction of tokens).
+// pa_select.cuh -- the K largest of n 32-bit keys, by a block or by a warp (used by the
+// choice of blocks and by the eviction of tokens), and what a cluster's CTAs do together.
 //
-// Keys are unsigned (ordered_key() maps floats to them in their order).  The K-th
-// largest key is found digit by digit from the top: a histogram of the digit among
-// the keys that still agree with what is known, added up over the cluster through
-// distributed shared memory, and the digit where the count from above passes K.
-// Ties at that key go to the lowest index, so what is chosen depends on the keys
-// alone: counts are integers, whatever the order of the atomics.
+// Keys are unsigned (ordered_key() maps floats to them in their order); a key of all bits
+// set is always chosen.  The K-th largest key is found from the top: by a block digit by
+// digit (a histogram of the digit among the keys that agree with what is known, and the
+// digit where the count from above passes K), by a warp bit by bit over registers.  Both
+// begin below the bits that all keys share and end as soon as a count comes out even.
+// Ties go to the lowest index, so what is chosen depends on the keys alone: counts are
+// integers, whatever the order of the atomics.
 #pragma once
 
 #include <cstdint>
@@ -35,11 +36,6 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) 
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
   return a;
 }
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -51,6 +47,9 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -70,54 +69,79 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+constexpr uint32_t kAlways = 0xffffffffu;  // the key that is chosen whatever K
+
 struct SelectShared {
-  uint32_t hist[2][256];
-  uint32_t total[256];
+  uint32_t hist[256];
   uint32_t warp_a[32], warp_b[32];
-  uint32_t digit, above;
-  uint32_t mine[2];  // this CTA's counts above the threshold and at it
+  uint32_t all, any, always;  // bits of all keys, of any; keys that are always chosen
+  uint32_t digit, above, here;
 };
 
-// The threshold that leaves the K largest keys of the cluster: those above `key`,
-// and the first `equal` of those that are `key` itself.  n: keys of this CTA, read
-// by key(i).  0 < K <= keys of the cluster.  Every thread of the cluster calls it;
-// blockDim.x is at least 256.
+// The threshold that leaves the K largest of n keys, read by key(i): those above `key`, and
+// the first `equal` of those that are `key` itself.  0 < K <= n.  Every thread of the block.
 struct Threshold {
   uint32_t key, equal;
 };
 template <class Key>
-__device__ Threshold select_threshold(SelectShared& B, int n, uint32_t K, uint32_t ctas, Key key) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  uint32_t known = 0, mask = 0;
-  uint32_t left = K;  // how many of the keys that agree with `known` are to be kept
-#pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    uint32_t* hist = B.hist[pass & 1];
-    // (remote reads of this buffer, two passes ago, ended before the barrier of the last pass)
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += blockDim.x) {
-      const uint32_t k = key(i);
-      if ((k & mask) == known) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-    }
-    group_sync(ctas);
-    if (tid < 256) {
-      uint32_t sum = 0;
-      if (ctas > 1) {
-        const uint32_t at = smem_addr(&hist[tid]);
-        for (uint32_t r = 0; r < ctas; ++r) sum += ld_cluster_u32(cluster_addr(at, r));
-      } else {
-        sum = hist[tid];
+__device__ Threshold select_threshold(SelectShared& B, int n, uint32_t K, Key key) {
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
+  for (int i = tid; i < 256; i += threads) B.hist[i] = 0;
+  if (tid == 0) B.all = kAlways, B.any = 0, B.always = 0;
+  __syncthreads();
+  {
+    uint32_t all = kAlways, any = 0;
+    int always = 0;
+    for (int i = tid; i < n; i += 4 * threads) {
+      uint32_t k[4];  // (several loads in flight)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i + j * threads < n ? key(i + j * threads) : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j * threads >= n) continue;
+        if (k[j] == kAlways)
+          ++always;
+        else
+          all &= k[j], any |= k[j];
       }
-      B.total[tid] = sum;
+    }
+    all = __reduce_and_sync(kAlways, all);
+    any = __reduce_or_sync(kAlways, any);
+    always = __reduce_add_sync(kAlways, always);
+    if (lane == 0) {
+      atomicAnd(&B.all, all);
+      atomicOr(&B.any, any);
+      atomicAdd(&B.always, (uint32_t)always);
+    }
+  }
+  __syncthreads();
+  const uint32_t all = B.all, any = B.any;
+  // (at most as many as there are are asked for: the others of them are ties at the top)
+  if (B.always >= K) return Threshold{kAlways, K};
+  uint32_t left = K - B.always;  // how many of the keys that agree with `known` are to be kept
+  int top = all == any ? 0 : 32 - __clz(all ^ any);  // bits still open
+  uint32_t mask = top == 32 ? 0u : kAlways << top, known = all & mask;
+  while (top > 0) {
+    const int shift = top > 8 ? top - 8 : 0;
+    for (int i = tid; i < n; i += 4 * threads) {
+      uint32_t k[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i + j * threads < n ? key(i + j * threads) : kAlways;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // (of the digit's bits, those above `top` are zeros)
+        if (k[j] != kAlways && (k[j] & mask) == known)
+          atomicAdd(&B.hist[(k[j] & ~mask) >> shift], 1u);
     }
     __syncthreads();
     if (tid < 32) {
       // lane 0 holds the highest eight digits
       uint32_t c[8], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += c[j] = B.total[255 - (lane * 8 + j)];
+      for (int j = 0; j < 8; ++j) {
+        const int d = 255 - (lane * 8 + j);
+        sum += c[j] = B.hist[d];
+        B.hist[d] = 0;
+      }
       uint32_t incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -128,20 +152,71 @@ __device__ Threshold select_threshold(SelectShared& B, int n, uint32_t K, uint32
       if (before < left && left <= incl) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (before < left && left <= before + c[j]) {
-            B.digit = 255 - (lane * 8 + j);
-            B.above = before;
-          }
+          if (before < left && left <= before + c[j])
+            B.digit = 255 - (lane * 8 + j), B.above = before, B.here = c[j];
           before += c[j];
         }
       }
     }
     __syncthreads();
     known |= B.digit << shift;
-    mask |= 255u << shift;
+    mask |= kAlways << shift;
     left -= B.above;
+    top = shift;
+    // all that agree so far are kept: no lower digit matters
+    if (left == B.here && known != 0) return Threshold{known - 1, 0u};
   }
   return Threshold{known, left};
+}
+
+// The K largest over a warp's registers: k[j] of lane i is key 32 j + i, those from n on are
+// not there.  Sets bit j of the result for the lane's chosen ones.  0 < K <= n.
+template <int NJ>
+__device__ __forceinline__ uint32_t select_in_warp(const uint32_t (&k)[NJ], int n, int K) {
+  const int lane = threadIdx.x & 31;
+  uint32_t chosen = 0, all = kAlways, any = 0;
+  int fixed = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool there = 32 * j + lane < n;
+    if (there && k[j] == kAlways) chosen |= 1u << j, ++fixed;
+    if (there && k[j] != kAlways) all &= k[j], any |= k[j];
+  }
+  K -= __reduce_add_sync(kAlways, fixed);
+  if (K <= 0) return chosen;
+  all = __reduce_and_sync(kAlways, all);
+  any = __reduce_or_sync(kAlways, any);
+  // the bits that all keys share, then bit by bit: the largest T with at least K keys >= T
+  int bit = all == any ? -1 : 31 - __clz(all ^ any);
+  uint32_t T = bit < 0 ? all : bit == 31 ? 0u : all & (kAlways << (bit + 1));
+  bool exact = false;
+  for (; bit >= 0 && !exact; --bit) {
+    const uint32_t t = T | 1u << bit;
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      count += 32 * j + lane < n && k[j] >= t && k[j] != kAlways;
+    count = __reduce_add_sync(kAlways, count);
+    if (count >= K) T = t;
+    exact = count == K;
+  }
+  // all above T, and of those at T the first
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool there = 32 * j + lane < n && k[j] != kAlways;
+    if (there && (k[j] > T || (exact && k[j] == T))) chosen |= 1u << j, ++above;
+  }
+  if (exact) return chosen;
+  int left = K - __reduce_add_sync(kAlways, above);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool tie = 32 * j + lane < n && k[j] == T && T != kAlways;
+    const uint32_t ball = __ballot_sync(kAlways, tie);
+    if (tie && __popc(ball & ((1u << lane) - 1u)) < left) chosen |= 1u << j;
+    left -= __popc(ball);
+  }
+  return chosen;
 }
 
 // Exclusive prefix sums of a and b over the block's threads (in order of threadIdx.x);

@@ -113,9 +113,9 @@ def test_select_refusals(lib):
                 dict(bounds=VP + 4), dict(out=VP + 2)):
         assert call(**bad) == "PA_ERR_INVALID_ARG", bad
     for bad in (dict(bs=64), dict(d=96), dict(nq=32), dict(nkv=16, nq=16), dict(T=1 << 28),
-                dict(maxl=393217 * 16)):
+                dict(maxl=49153 * 16)):
         assert call(**bad) == "PA_ERR_UNSUPPORTED", bad
-    assert call(maxl=393216 * 16, T=0) == "PA_OK"
+    assert call(maxl=49152 * 16, T=0) == "PA_OK"
 
 
 BLOCKS = ["q", "k", "v", "nb", "bs", "nq", "nkv", "d", "bt", "maxb", "sl", "qsl", "S", "T",
