@@ -534,8 +534,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     return;
   }
   if constexpr (THREADS == kFewThreads) return;  // (no request has more)
-  const Threshold th = select_threshold(B, visible, (uint32_t)p.num_selected,
-                                        [&](int i) { return keys[i]; });
+  __shared__ uint32_t hist[THREADS == kFewThreads ? 1 : kSelectBins];
+  KeyBits seen;
+  for (int i = tid; i < visible; i += THREADS) seen.see(keys[i]);
+  const Threshold th = select_threshold(B, hist, visible, (uint32_t)p.num_selected,
+                                        [&](int i) { return keys[i]; }, seen);
   // each thread a run of blocks, of odd length (no bank conflicts)
   const int run = (visible + THREADS - 1) / THREADS | 1;
   const int lo = min(tid * run, visible), hi = min(lo + run, visible);

@@ -362,7 +362,6 @@ struct EvictArgs {
   bool staged;  // (set by the launcher) the weights' keys fit in shared memory
 };
 constexpr int kEvictMaxLen = 1 << 19;          // two bits a token in shared memory
-constexpr size_t kEvictStaged = 64 * 1024;
 cudaError_t launch_evict(EvictArgs p, int sm_count, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, unsigned* err,

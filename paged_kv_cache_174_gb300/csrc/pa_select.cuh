@@ -72,46 +72,73 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
 constexpr uint32_t kAlways = 0xffffffffu;  // the key that is chosen whatever K
 
 struct SelectShared {
-  uint32_t hist[256];
   uint32_t warp_a[32], warp_b[32];
   uint32_t all, any, always;  // bits of all keys, of any; keys that are always chosen
   uint32_t digit, above, here;
 };
 
+// Exclusive prefix sums of a and b over the block's threads (in order of threadIdx.x);
+// the block's totals in all_a, all_b.
+__device__ __forceinline__ void block_scan2(SelectShared& B, uint32_t a, uint32_t b, uint32_t& pre_a,
+                                            uint32_t& pre_b, uint32_t& all_a, uint32_t& all_b) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  uint32_t ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t va = __shfl_up_sync(0xffffffffu, ia, o);
+    const uint32_t vb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) ia += va, ib += vb;
+  }
+  __syncthreads();  // (an earlier call's sums have been read)
+  if (lane == 31) B.warp_a[warp] = ia, B.warp_b[warp] = ib;
+  __syncthreads();
+  uint32_t before_a = 0, before_b = 0;
+  all_a = all_b = 0;
+  for (int w = 0; w < warps; ++w) {
+    const uint32_t wa = B.warp_a[w], wb = B.warp_b[w];
+    if (w < warp) before_a += wa, before_b += wb;
+    all_a += wa, all_b += wb;
+  }
+  pre_a = before_a + ia - a;
+  pre_b = before_b + ib - b;
+}
+
+// What a thread has seen of the keys: the bits of all of them and of any, but for those that
+// are always chosen, which it counts.
+struct KeyBits {
+  uint32_t all = kAlways, any = 0, always = 0;
+  __device__ __forceinline__ void see(uint32_t k) {
+    if (k == kAlways)
+      ++always;
+    else
+      all &= k, any |= k;
+  }
+};
+
 // The threshold that leaves the K largest of n keys, read by key(i): those above `key`, and
-// the first `equal` of those that are `key` itself.  0 < K <= n.  Every thread of the block.
+// the first `equal` of those that are `key` itself.  0 < K <= n.  Every thread of the block,
+// of kSelectBins / 8 threads at least; seen: of the block's threads together every key once;
+// hist: kSelectBins words of shared memory.
 struct Threshold {
   uint32_t key, equal;
 };
+constexpr int kSelectDigit = 11, kSelectBins = 1 << kSelectDigit;
 template <class Key>
-__device__ Threshold select_threshold(SelectShared& B, int n, uint32_t K, Key key) {
+__device__ Threshold select_threshold(SelectShared& B, uint32_t* hist, int n, uint32_t K, Key key,
+                                      KeyBits seen) {
   const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
-  for (int i = tid; i < 256; i += threads) B.hist[i] = 0;
+  const int per = kSelectBins / threads;  // bins of a thread
+  for (int i = tid; i < kSelectBins; i += threads) hist[i] = 0;
   if (tid == 0) B.all = kAlways, B.any = 0, B.always = 0;
   __syncthreads();
   {
-    uint32_t all = kAlways, any = 0;
-    int always = 0;
-    for (int i = tid; i < n; i += 4 * threads) {
-      uint32_t k[4];  // (several loads in flight)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = i + j * threads < n ? key(i + j * threads) : 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (i + j * threads >= n) continue;
-        if (k[j] == kAlways)
-          ++always;
-        else
-          all &= k[j], any |= k[j];
-      }
-    }
-    all = __reduce_and_sync(kAlways, all);
-    any = __reduce_or_sync(kAlways, any);
-    always = __reduce_add_sync(kAlways, always);
+    const uint32_t all = __reduce_and_sync(kAlways, seen.all);
+    const uint32_t any = __reduce_or_sync(kAlways, seen.any);
+    const uint32_t always = __reduce_add_sync(kAlways, seen.always);
     if (lane == 0) {
       atomicAnd(&B.all, all);
       atomicOr(&B.any, any);
-      atomicAdd(&B.always, (uint32_t)always);
+      if (always) atomicAdd(&B.always, always);
     }
   }
   __syncthreads();
@@ -122,40 +149,37 @@ __device__ Threshold select_threshold(SelectShared& B, int n, uint32_t K, Key ke
   int top = all == any ? 0 : 32 - __clz(all ^ any);  // bits still open
   uint32_t mask = top == 32 ? 0u : kAlways << top, known = all & mask;
   while (top > 0) {
-    const int shift = top > 8 ? top - 8 : 0;
-    for (int i = tid; i < n; i += 4 * threads) {
-      uint32_t k[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = i + j * threads < n ? key(i + j * threads) : kAlways;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)  // (of the digit's bits, those above `top` are zeros)
-        if (k[j] != kAlways && (k[j] & mask) == known)
-          atomicAdd(&B.hist[(k[j] & ~mask) >> shift], 1u);
+    const int shift = top > kSelectDigit ? top - kSelectDigit : 0;
+    // (of the digit's bits, those above `top` are zeros)
+    const auto count = [&](uint32_t k) {
+      if (k != kAlways && (k & mask) == known) atomicAdd(&hist[(k & ~mask) >> shift], 1u);
+    };
+    int i = tid;
+    for (; i + 3 * threads < n; i += 4 * threads) {  // (several loads in flight)
+      const uint32_t k0 = key(i), k1 = key(i + threads), k2 = key(i + 2 * threads),
+                     k3 = key(i + 3 * threads);
+      count(k0), count(k1), count(k2), count(k3);
     }
+    for (; i < n; i += threads) count(key(i));
     __syncthreads();
-    if (tid < 32) {
-      // lane 0 holds the highest eight digits
-      uint32_t c[8], sum = 0;
+    // thread 0 has the highest bins
+    uint32_t c[8], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= per) continue;
+      const int d = kSelectBins - 1 - (tid * per + j);
+      sum += c[j] = hist[d];
+      hist[d] = 0;
+    }
+    uint32_t before, unused, total, unused2;
+    block_scan2(B, sum, 0u, before, unused, total, unused2);
+    if (before < left && left <= before + sum) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int d = 255 - (lane * 8 + j);
-        sum += c[j] = B.hist[d];
-        B.hist[d] = 0;
-      }
-      uint32_t incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      uint32_t before = incl - sum;
-      if (before < left && left <= incl) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (before < left && left <= before + c[j])
-            B.digit = 255 - (lane * 8 + j), B.above = before, B.here = c[j];
-          before += c[j];
-        }
+        if (j >= per) continue;
+        if (before < left && left <= before + c[j])
+          B.digit = kSelectBins - 1 - (tid * per + j), B.above = before, B.here = c[j];
+        before += c[j];
       }
     }
     __syncthreads();
@@ -217,32 +241,6 @@ __device__ __forceinline__ uint32_t select_in_warp(const uint32_t (&k)[NJ], int 
     left -= __popc(ball);
   }
   return chosen;
-}
-
-// Exclusive prefix sums of a and b over the block's threads (in order of threadIdx.x);
-// the block's totals in all_a, all_b.
-__device__ __forceinline__ void block_scan2(SelectShared& B, uint32_t a, uint32_t b, uint32_t& pre_a,
-                                            uint32_t& pre_b, uint32_t& all_a, uint32_t& all_b) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  uint32_t ia = a, ib = b;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t va = __shfl_up_sync(0xffffffffu, ia, o);
-    const uint32_t vb = __shfl_up_sync(0xffffffffu, ib, o);
-    if (lane >= o) ia += va, ib += vb;
-  }
-  __syncthreads();  // (an earlier call's sums have been read)
-  if (lane == 31) B.warp_a[warp] = ia, B.warp_b[warp] = ib;
-  __syncthreads();
-  uint32_t before_a = 0, before_b = 0;
-  all_a = all_b = 0;
-  for (int w = 0; w < warps; ++w) {
-    const uint32_t wa = B.warp_a[w], wb = B.warp_b[w];
-    if (w < warp) before_a += wa, before_b += wb;
-    all_a += wa, all_b += wb;
-  }
-  pre_a = before_a + ia - a;
-  pre_b = before_b + ib - b;
 }
 
 }  // namespace pa
