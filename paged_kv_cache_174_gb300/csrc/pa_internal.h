@@ -321,23 +321,15 @@ struct ChunkArgs {
   const int32_t* seq_lens;
   const int32_t* query_start_loc;
   float* weights;
-  float2* sums;  // [pieces, num_tokens, n_q] (max in log2 units, sum) of each row
+  float* sums;  // [n_kv, num_tokens, group] log2 of each row's sum of exponentials
   unsigned* err;
   int64_t weights_stride;
   float scale_log2;
   int32_t num_blocks, max_blocks, num_seqs, num_tokens, n_q, n_kv, group, head_dim;
   int32_t block_shift, max_seq_len;
-  int32_t pieces, skip;  // (set by the launcher)
+  int32_t skip;  // (set by the launcher) chunk requests of earlier launches
   bool fp8;
 };
-// The pieces that the keys of a row are cut into, and the bytes of their sums.
-constexpr int kMaxChunkPieces = 8;
-struct ChunkPlan {
-  int pieces;
-  size_t bytes;
-};
-ChunkPlan chunk_plan(int num_tokens, int num_q_heads, int num_kv_heads, int max_seq_len,
-                     int sm_count);
 cudaError_t launch_chunk_weights(const ChunkArgs& p, int max_q_len, int sm_count,
                                  cudaStream_t stream);
 

@@ -204,8 +204,7 @@ int weights_impl(const pa_bf16* q, const void* k_cache, const void* v_cache, boo
   const int group = num_q_heads / num_kv_heads;
   const int shift = log2_of(block_size) - 4;
   if (max_q_len >= 2) {
-    const size_t sums = round_up(
-        pa::chunk_plan(num_tokens, num_q_heads, num_kv_heads, max_seq_len, sms).bytes);
+    const size_t sums = round_up((size_t)num_tokens * num_q_heads * sizeof(float));
     if (!workspace || !aligned(workspace, 256))
       return api_fail(PA_ERR_WORKSPACE, "workspace must be a non-null 256-byte aligned pointer");
     if (workspace_bytes < sums)
@@ -249,7 +248,7 @@ int weights_impl(const pa_bf16* q, const void* k_cache, const void* v_cache, boo
     c.seq_lens = seq_lens;
     c.query_start_loc = query_start_loc;
     c.weights = weights;
-    c.sums = static_cast<float2*>(workspace);
+    c.sums = static_cast<float*>(workspace);
     c.err = err;
     c.weights_stride = weights_len;
     c.scale_log2 = scale * kLog2E;
@@ -476,9 +475,7 @@ size_t pa_weights_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t n
   int sms = 0;
   if (pa::api_device_state(nullptr, &sms)) return 0;
   if (max_q_len < 2) return 256;
-  // (a call of fewer tokens may cut its keys into more pieces)
-  const size_t sums =
-      (size_t)num_tokens * num_q_heads * pa::kMaxChunkPieces * sizeof(float2);
+  const size_t sums = (size_t)num_tokens * num_q_heads * sizeof(float);
   return round_up(sums + 256) +
          round_up(pa::prefill_workspace_bound(num_tokens, num_q_heads, num_kv_heads, head_dim,
                                               max_q_len, max_seq_len, sms));

@@ -8,7 +8,7 @@
 // neither of which needs V or P in shared memory:
 //  * rows: a tile of 128 / G tokens x G heads stays, key tiles of 128 stream past; each
 //    thread keeps the running max and sum of half a row (the halves of the key tile).
-//    The keys may be cut into pieces for more units; pieces are (max, sum) pairs.
+//    The CTAs of a cluster take a piece of the keys each, for more units.
 //  * columns: a tile of 128 keys stays, query tiles stream past; S^T puts a key in
 //    each TMEM lane, so the sum over rows is a thread's own.  A cluster's CTAs take
 //    query tiles in turn and add their sums up at the end: no atomics, and one order.
@@ -81,7 +81,6 @@ struct ChunkUnit {
   int q0, ntok;            // rows pass: first token and tokens of the query tile
   int key0;                // columns pass: first key of the tile
   int first, step, count;  // B tiles of this CTA: first, first + step, ...
-  int piece;               // rows pass: piece of the keys
 };
 
 template <int D, int G, bool F8, bool COLS>
@@ -169,8 +168,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
   tc::fence_after_sync();
   const uint32_t tmem = B.tmem_slot;
   volatile int* abort_flag = &B.abort_flag;
-  const int pieces = COLS ? 1 : p.pieces;
-  const long long units = (long long)tiles_all * p.n_kv * pieces;
+  const long long units = (long long)tiles_all * p.n_kv;
   const long long groups = gridDim.x / ctas, group = blockIdx.x / ctas;
 
   uint32_t c0 = 0;      // B tiles of this CTA before this unit
@@ -182,8 +180,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
     if (!COLS) u = units - 1 - u;
     ChunkUnit U;
     {
-      const int per = p.n_kv * pieces;
-      const int tile = (int)(u / per), rem = (int)(u % per);
+      const int tile = (int)(u / p.n_kv);
       int lo = 0, hi = B.listed;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -193,8 +190,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
           hi = mid;
       }
       U.s = B.list_seq[lo];
-      U.h = rem / pieces;
-      U.piece = rem % pieces;
+      U.h = (int)(u % p.n_kv);
       U.a = p.query_start_loc[U.s];
       U.ql = p.query_start_loc[U.s + 1] - U.a;
       U.L = p.seq_lens[U.s];
@@ -212,9 +208,9 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
         U.q0 = U.a + nth * TM;
         U.ntok = min(TM, U.ql - nth * TM);
         const int tiles = (U.c0 + nth * TM + U.ntok + kTile - 1) / kTile;
-        U.first = (int)((long long)U.piece * tiles / pieces);
+        U.first = (int)((long long)rank * tiles / ctas);
         U.step = 1;
-        U.count = (int)((long long)(U.piece + 1) * tiles / pieces) - U.first;
+        U.count = (int)((long long)(rank + 1) * tiles / ctas) - U.first;
       }
     }
     const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
@@ -224,31 +220,29 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
     if (warp == 0) {
       // ------------------------------------------------ query tiles
       if constexpr (COLS) {
+        // the log sums of a query tile's rows, four columns a lane, a tile ahead
+        const auto log_sums = [&](int i) {
+          float4 v = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);  // (no row: weight 0)
+          if (i < U.count) {
+            const int qt = U.first + i * U.step, n = tokens_of(qt) * G;
+            const float* at = p.sums + ((int64_t)U.h * p.num_tokens + U.a + qt * TM) * G + lane * 4;
+            if (lane * 4 < n) v.x = at[0];
+            if (lane * 4 + 1 < n) v.y = at[1];
+            if (lane * 4 + 2 < n) v.z = at[2];
+            if (lane * 4 + 3 < n) v.w = at[3];
+          }
+          return v;
+        };
+        float4 ls = log_sums(0);
         for (int i = 0; i < U.count; ++i) {
           const uint32_t c = c0 + i, st = c % NB;
-          const int qt = U.first + i * U.step, q0 = U.a + qt * TM, ntok = tokens_of(qt);
-          // The log sums of the tile's rows.  Their slot's last tile, kSide earlier, is done
-          // with: this warp has waited for a stage that a product NB + 1 tiles back freed,
-          // which needed the S buffer of the tile two before that to have been read.
+          const int q0 = U.a + (U.first + i * U.step) * TM;
+          // Their slot's last tile, kSide earlier, is done with: this warp has waited for a
+          // stage that a product NB + 1 tiles back freed, which needed the S buffer of the
+          // tile two before that to have been read.
           static_assert(kSide >= 4 + 4, "");
-          float* side = B.side[c % kSide];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int col = lane * 4 + j, tl = col / G;
-            float v = INFINITY;  // (no such row: weight 0)
-            if (tl < ntok) {
-              const int64_t row = (int64_t)(q0 + tl) * p.n_q + U.h * G + col % G;
-              float m = -INFINITY, sum = 0.f;
-              for (int k = 0; k < p.pieces; ++k)
-                m = fmaxf(m, p.sums[(int64_t)k * p.num_tokens * p.n_q + row].x);
-              for (int k = 0; k < p.pieces; ++k) {
-                const float2 ml = p.sums[(int64_t)k * p.num_tokens * p.n_q + row];
-                if (ml.x != -INFINITY || ml.y != 0.f) sum += ml.y * fast_exp2(ml.x - m);
-              }
-              v = m + __log2f(sum);
-            }
-            side[col] = v;
-          }
+          *reinterpret_cast<float4*>(B.side[c % kSide] + lane * 4) = ls;
+          ls = log_sums(i + 1);
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_addr(&B.side_full[c % kSide]));
@@ -290,42 +284,25 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
     } else if (warp >= kFirstKWarp) {
       // ------------------------------------------------ key tiles
       const int idx = warp - kFirstKWarp;
-      // Pages idx * PAGES .. of the K tile at key0 into dst, completion on bar.
-      const auto load_tile = [&](int key0, unsigned char* dst, uint32_t bar, float* scales) {
-        int page[PAGES];
-        uint32_t bytes = 0;
+      constexpr int CPR = D / 16, RPL = 32 / CPR, LOADS = 16 / RPL;  // (8-bit cache)
+      int page[PAGES];
+      uint4 w[F8 ? PAGES : 1][LOADS];
+      float sc[F8 ? PAGES : 1];
+      // This warp's pages of the K tile at key0: the pool's pages (-1: none), and the codes'
+      // loads (8-bit cache).
+      const auto look_up = [&](int key0) {
 #pragma unroll
         for (int i = 0; i < PAGES; ++i) {
           const int lp = key0 / 16 + idx * PAGES + i;
           page[i] = -1;
-          if (lp * 16 < U.L) {
-            const int b = table[lp >> p.block_shift];
-            if (b >= 0 && b < p.num_blocks) {
-              page[i] = (b << p.block_shift) + (lp & ((1 << p.block_shift) - 1));
-              bytes += NH * 2048;
-            } else if (lane == 0) {
-              flag_error(p.err, DEVERR_BOUNDS);
-            }
-          }
+          if (lp * 16 >= U.L) continue;
+          const int b = table[lp >> p.block_shift];
+          if (b >= 0 && b < p.num_blocks)
+            page[i] = (b << p.block_shift) + (lp & ((1 << p.block_shift) - 1));
+          else if (lane == 0)
+            flag_error(p.err, DEVERR_BOUNDS);
         }
-        if constexpr (!F8) {
-          if (lane != 0) return;
-          if (bytes)
-            mbar_arrive_expect_tx(bar, bytes);
-          else
-            mbar_arrive(bar);
-#pragma unroll
-          for (int i = 0; i < PAGES; ++i) {
-            if (page[i] < 0) continue;
-#pragma unroll
-            for (int hf = 0; hf < NH; ++hf)
-              tc::tma_load_3d(smem_addr(dst + hf * HALF + (idx * PAGES + i) * 2048), &kmap,
-                              hf * 64, U.h, page[i] * 16, bar);
-          }
-        } else {
-          constexpr int CPR = D / 16, RPL = 32 / CPR, LOADS = 16 / RPL;
-          uint4 w[PAGES][LOADS];
-          float sc[PAGES];
+        if constexpr (F8) {
 #pragma unroll
           for (int i = 0; i < PAGES; ++i) {
             sc[i] = 0.f;
@@ -339,10 +316,34 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
               w[i][j] = __ldg(reinterpret_cast<const uint4*>(
                   at + ((int64_t)(j * RPL + lane / CPR) * p.n_kv + U.h) * D + (lane % CPR) * 16));
           }
+        }
+      };
+      // They go to dst, completion on bar.
+      const auto bring = [&](unsigned char* dst, uint32_t bar, float* scales) {
+        if constexpr (!F8) {
+          if (lane != 0) return;
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int i = 0; i < PAGES; ++i) bytes += page[i] < 0 ? 0 : NH * 2048;
+          if (bytes)
+            mbar_arrive_expect_tx(bar, bytes);
+          else
+            mbar_arrive(bar);
+#pragma unroll
+          for (int i = 0; i < PAGES; ++i) {
+            if (page[i] < 0) continue;
+#pragma unroll
+            for (int hf = 0; hf < NH; ++hf)
+              tc::tma_load_3d(smem_addr(dst + hf * HALF + (idx * PAGES + i) * 2048), &kmap,
+                              hf * 64, U.h, page[i] * 16, bar);
+          }
+        } else {
+          const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
 #pragma unroll
           for (int i = 0; i < PAGES; ++i) {
             if (scales && lane < 16) scales[(idx * PAGES + i) * 16 + lane] = sc[i];
             if (page[i] < 0) continue;
+            unsigned char* to = dst + (c16 >> 2) * HALF + (idx * PAGES + i) * 2048;
 #pragma unroll
             for (int j = 0; j < LOADS; ++j) {
               const uint32_t src[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
@@ -355,8 +356,6 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
                 out[2 * k] = pack_bf16x2(f.x, f.y);
                 out[2 * k + 1] = pack_bf16x2(g.x, g.y);
               }
-              const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
-              unsigned char* to = dst + (c16 >> 2) * HALF + (idx * PAGES + i) * 2048;
               const uint32_t at = swizzled(j * RPL + lane / CPR, c8);
               *reinterpret_cast<uint4*>(to + at) = make_uint4(out[0], out[1], out[2], out[3]);
               *reinterpret_cast<uint4*>(to + (at ^ 16u)) =
@@ -369,19 +368,24 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
         }
       };
       if constexpr (COLS) {
-        if (U.count > 0) load_tile(U.key0, a_s, smem_addr(&B.a_full), nullptr);
+        if (U.count > 0) {
+          look_up(U.key0);
+          bring(a_s, smem_addr(&B.a_full), nullptr);
+        }
       } else {
+        // (a tile's places are looked up, and its codes on their way, before its stage is free)
+        if (U.count > 0) look_up(U.first * kTile);
         for (int i = 0; i < U.count; ++i) {
           const uint32_t c = c0 + i, st = c % NB;
           if (lane == 0 && c >= NB)
             mbar_wait(smem_addr(&B.b_empty[st]), (c / NB - 1) & 1, p.err, abort_flag);
           __syncwarp();
-          load_tile((U.first + i) * kTile, b_s + st * TILE, smem_addr(&B.b_full[st]),
-                    F8 ? B.side[c % kSide] : nullptr);
+          bring(b_s + st * TILE, smem_addr(&B.b_full[st]), F8 ? B.side[c % kSide] : nullptr);
           if constexpr (F8) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&B.side_full[c % kSide]));
           }
+          if (i + 1 < U.count) look_up((U.first + i + 1) * kTile);
         }
       }
     } else {
@@ -453,8 +457,8 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
                 const float2 b = __ffma2_rn(
                     make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), m2,
                     make_float2(-ls.z, -ls.w));
-                acc[0].x += fast_exp2(a.x), acc[0].y += fast_exp2(a.y);
-                acc[1].x += fast_exp2(b.x), acc[1].y += fast_exp2(b.y);
+                acc[0] = __fadd2_rn(acc[0], make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+                acc[1] = __fadd2_rn(acc[1], make_float2(fast_exp2(b.x), fast_exp2(b.y)));
               }
               sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
             } else {
@@ -466,24 +470,49 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
               }
             }
           } else {
-            float mx = -INFINITY;
+            // With a positive factor the largest raw score gives the largest scaled one and the
+            // factor goes into the exponent's FMA; else (and with the keys' scales) the scores
+            // are scaled first.
+            const bool raw = !F8 && mul > 0.f;
+            if (!raw) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float v = __uint_as_float(x[j]) * mul;
-              if constexpr (F8) v *= side[part * 32 + j];
-              if (!whole) v = part * 32 + j < hi ? v : -INFINITY;
-              x[j] = __float_as_uint(v);
-              mx = fmaxf(mx, v);
+              for (int j = 0; j < 32; ++j) {
+                float v = __uint_as_float(x[j]) * mul;
+                if constexpr (F8) v *= side[part * 32 + j];
+                x[j] = __float_as_uint(v);
+              }
             }
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (part * 32 + j >= hi) x[j] = __float_as_uint(-INFINITY);
+            }
+            float m4[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              m4[0] = fmax3(m4[0], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+              m4[1] = fmax3(m4[1], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+            }
+            const float f = raw ? mul : 1.f;
+            const float mx = fmaxf(m4[0], m4[1]) * f;
             if (mx > top) {
               sum *= fast_exp2(top - mx);  // (0 from -inf)
               top = mx;
             }
             const float ref = top == -INFINITY ? 0.f : top;
-            float add[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 f2 = make_float2(f, f), r2 = make_float2(-ref, -ref);
+            float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int j = 0; j < 32; ++j) add[j & 3] += fast_exp2(__uint_as_float(x[j]) - ref);
-            sum += (add[0] + add[1]) + (add[2] + add[3]);
+            for (int j = 0; j < 32; j += 4) {
+              const float2 a = __ffma2_rn(
+                  make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, r2);
+              const float2 b = __ffma2_rn(
+                  make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), f2, r2);
+              add[0] = __fadd2_rn(add[0], make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+              add[1] = __fadd2_rn(add[1], make_float2(fast_exp2(b.x), fast_exp2(b.y)));
+            }
+            add[0] = __fadd2_rn(add[0], add[1]);
+            sum += add[0].x + add[0].y;
           }
         }
       }
@@ -509,13 +538,22 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
         float* w = p.weights + ((int64_t)U.s * p.n_kv + U.h) * p.weights_stride + j;
         *w = (j < U.c0 ? *w : 0.f) + sum;
       }
-    } else if (tid < kTile && tid < U.ntok * G) {
-      const float m0 = B.part[0][0][tid], m1 = B.part[0][1][tid], m = fmaxf(m0, m1);
-      const float s0 = B.part[1][0][tid], s1 = B.part[1][1][tid];
-      const float sum = (m0 == -INFINITY ? s0 : s0 * fast_exp2(m0 - m)) +
-                        (m1 == -INFINITY ? s1 : s1 * fast_exp2(m1 - m));
-      const int64_t row = (int64_t)(U.q0 + tid / G) * p.n_q + U.h * G + tid % G;
-      p.sums[(int64_t)U.piece * p.num_tokens * p.n_q + row] = make_float2(m, sum);
+    } else if (rank == 0 && tid < U.ntok * G) {
+      // the row's log sum over the halves of the keys' tiles and the cluster's pieces of them
+      float m = -INFINITY, sum = 0.f;
+      for (uint32_t k = 0; k < ctas; ++k)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float pm = ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(&B.part[0][hf][tid]), k))
+                                    : B.part[0][hf][tid];
+          const float ps = ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(&B.part[1][hf][tid]), k))
+                                    : B.part[1][hf][tid];
+          const float to = fmaxf(m, pm);
+          sum = (m == -INFINITY ? sum : sum * fast_exp2(m - to)) +
+                (pm == -INFINITY ? ps : ps * fast_exp2(pm - to));
+          m = to;
+        }
+      p.sums[((int64_t)U.h * p.num_tokens + U.q0) * G + tid] = m + __log2f(sum);
     }
     group_sync(ctas);
   }
@@ -571,23 +609,25 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
     if (e != cudaSuccess) return e;
   }
   const long long slots_of_sms = 2ll * sm_count;
-  const ChunkPlan plan = chunk_plan(p.num_tokens, p.n_q, p.n_kv, p.max_seq_len, sm_count);
   // upper bounds of the units: the kernel has the exact count
-  const long long q_tiles = (long long)p.num_tokens / (kTile / G) + p.num_seqs;
-  const long long row_units = q_tiles * p.n_kv * plan.pieces;
+  const long long row_units = ((long long)p.num_tokens / (kTile / G) + p.num_seqs) * p.n_kv;
   const long long most_chunks = std::min<long long>(p.num_seqs, p.num_tokens / 2);
-  const long long col_units =
-      most_chunks * (((long long)p.max_seq_len + kTile - 1) / kTile) * p.n_kv;
-  // query tiles that a key tile may see: their cluster's CTAs take them in turn
+  const long long key_tiles = ((long long)p.max_seq_len + kTile - 1) / kTile;
+  const long long col_units = most_chunks * key_tiles * p.n_kv;
+  // CTAs of a cluster: pieces of a row's keys where query tiles are few, and query tiles of
+  // a key tile in turn
+  const long long least = ((long long)p.num_tokens / (kTile / G) + 1) * p.n_kv;
+  int pieces = 1;
+  while (pieces < 8 && least * pieces < slots_of_sms && key_tiles >= 8ll * pieces) pieces *= 2;
   const int tiles = (max_q_len + kTile / G - 1) / (kTile / G);
   int ctas = 1;
   while (ctas < 4 && tiles >= 4 * ctas) ctas *= 2;
-  p.pieces = plan.pieces;
   for (p.skip = 0; p.skip < most_chunks; p.skip += kListed) {
-    cudaError_t e = launch_pass<D, G, F8, false>(
-        p, qm, km, (int)std::min(row_units, slots_of_sms), 1, stream);
+    long long groups = std::min(row_units, slots_of_sms / pieces);
+    cudaError_t e =
+        launch_pass<D, G, F8, false>(p, qm, km, (int)(groups * pieces), pieces, stream);
     if (e != cudaSuccess) return e;
-    const long long groups = std::min(col_units, slots_of_sms / ctas);
+    groups = std::min(col_units, slots_of_sms / ctas);
     e = launch_pass<D, G, F8, true>(p, qm, km, (int)(groups * ctas), ctas, stream);
     if (e != cudaSuccess) return e;
   }
@@ -610,19 +650,6 @@ cudaError_t launch_d(const ChunkArgs& p, int max_q_len, int sm_count, cudaStream
 }
 
 }  // namespace
-
-ChunkPlan chunk_plan(int num_tokens, int num_q_heads, int num_kv_heads, int max_seq_len,
-                     int sm_count) {
-  const int per_tile = kTile / (num_q_heads / num_kv_heads);
-  const long long units = ((long long)num_tokens / per_tile + 1) * num_kv_heads;
-  const long long key_tiles = ((long long)max_seq_len + kTile - 1) / kTile;
-  ChunkPlan plan{1, 0};
-  while (plan.pieces < kMaxChunkPieces && units * plan.pieces < 2ll * sm_count &&
-         key_tiles >= 8ll * plan.pieces)
-    plan.pieces *= 2;
-  plan.bytes = (size_t)num_tokens * num_q_heads * plan.pieces * sizeof(float2);
-  return plan;
-}
 
 cudaError_t launch_chunk_weights(const ChunkArgs& p, int max_q_len, int sm_count,
                                  cudaStream_t stream) {
