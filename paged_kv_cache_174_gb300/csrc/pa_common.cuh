@@ -179,13 +179,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned* err,
                                           volatile int* abort,
                                           unsigned long long limit_ns = kWaitLimitNs) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (uint32_t it = 1;; ++it) {
+  unsigned long long t0 = 0;  // (the clock is slow to read: not before the 64th attempt)
+  for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0) {
+    if ((it & 63u) == 63u) {
       if (*abort) return false;
-      if (global_ns() - t0 > limit_ns) {
+      const unsigned long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
         *abort = 1;
         flag_error(err, DEVERR_TIMEOUT);
         return false;
@@ -197,13 +198,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
 // mbar_wait without the suspend hint (see mbar_try_wait_spin).
 __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, unsigned* err,
                                           volatile int* abort) {
-  if (mbar_try_wait_spin(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (uint32_t it = 1;; ++it) {
+  unsigned long long t0 = 0;  // (the clock is slow to read: not before the 64th attempt)
+  for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait_spin(bar, parity)) return true;
-    if ((it & 63u) == 0) {
+    if ((it & 63u) == 63u) {
       if (*abort) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
+      const unsigned long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
         *abort = 1;
         flag_error(err, DEVERR_TIMEOUT);
         return false;

@@ -6,20 +6,21 @@
 //
 // A weight needs its row's sum over all keys, so there are two passes over S = Q K^T,
 // neither of which needs V or P in shared memory:
-//  * rows: a tile of 128 / G tokens x G heads stays, key tiles of 128 stream past; each
-//    thread keeps the running max and sum of half a row (the halves of the key tile).
-//    The CTAs of a cluster take a piece of the keys each, for more units.
-//  * columns: a tile of 128 keys stays, query tiles stream past; S^T puts a key in
-//    each TMEM lane, so the sum over rows is a thread's own.  A cluster's CTAs take
+//  * rows: a tile of 256 / G tokens x G heads stays, key tiles of 64 stream past; each
+//    thread keeps the running max and sum of a row.  The CTAs of a cluster take a piece of
+//    the keys each, for more units.
+//  * columns: a tile of 256 keys stays, query tiles of 64 rows stream past; S^T puts a key
+//    in each TMEM lane, so the sum over rows is a thread's own.  A cluster's CTAs take
 //    query tiles in turn and add their sums up at the end: no atomics, and one order.
-// Both share the code below: the tile that stays is A (128 lanes), those that stream
-// are B (128 columns), bf16 with 128-byte swizzle, two S buffers in TMEM, and two CTAs
-// an SM, so that one's waits, and the drain between units, are the other's work.
+// Both share the code below: the tile that stays is A, two products' 128 lanes of TMEM,
+// copied there once a unit, so that a product reads only the 64 rows of B from shared
+// memory; S has two buffers, each with a group of warps that reads it.
 // 8-bit cache: K codes are converted to bf16 (exact) and the keys' scales multiply
-// the scores.  An exponential for each (row, head, key) in each pass is the bound.
+// the scores.
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -30,26 +31,35 @@
 namespace pa {
 namespace {
 
-constexpr int kTile = 128;          // lanes and columns of a product
-constexpr int kEpilogueWarps = 8;   // warps 2-9: two for each TMEM lane quarter
-constexpr int kFirstKWarp = 10;
-constexpr int kSide = 8;            // slots of the values that go with a B tile's columns
+constexpr int kLanes = 128;         // lanes of a product: rows of A
+constexpr int kCols = 128;          // columns of a product: rows of B
+constexpr int kTile = kLanes;       // rows of the tile that stays
+constexpr int kSumWarps = 16;       // warps 2-17: for each S buffer two a TMEM lane quarter
+constexpr int kFirstKWarp = 18;
+constexpr int kBuffers = 3;         // of S in TMEM
+constexpr int kSide = 12;           // slots of the values that go with a B tile's columns
 constexpr int kListed = 512;        // chunk requests of a launch
 
+// Warps that bring K tiles, eight pages between them.  Of an 8-bit cache each has the codes and
+// scales of its next kRaw tiles' pages on their way to shared memory, and converts them.
 template <bool F8>
 struct Roles {
-  static constexpr int kKWarps = F8 ? 4 : 2;  // load K tiles: eight pages between them
+  static constexpr int kKWarps = F8 ? 4 : 2;
+  static constexpr int kPages = 8 / kKWarps;
+  static constexpr int kStages = F8 ? 3 : 4;  // B tiles on their way or in use
   static constexpr int kThreads = (kFirstKWarp + kKWarps) * 32;
 };
+constexpr int kRaw = 3;
 
 struct alignas(16) ChunkShared {
-  uint64_t a_full, b_full[4], b_empty[4], s_full[2], s_empty[2], side_full[kSide];
+  uint64_t a_full, a_ready, b_full[4], b_empty[4], s_full[kBuffers], s_empty[kBuffers];
+  uint64_t side_full[kSide], raw_full[4][kRaw];
   uint32_t tmem_slot;
   int abort_flag;
   int listed;
   // rows pass: the keys' scales; columns pass: the rows' log sums (read four at a time)
-  alignas(16) float side[kSide][kTile];
-  float part[2][2][kTile];    // rows pass: (max, sum); columns pass: [0][half] sums
+  alignas(16) float side[kSide][kCols];
+  float part[2][4][kTile];    // rows pass: (max, sum) by sum warps' share; columns pass: [0] sums
   int list_seq[kListed];
   int list_base[kListed + 1]; // first tile of each listed request
   SelectShared scan;
@@ -61,18 +71,39 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// S = A B^T, both tiles [half of head_dim][128 rows][64].
+// The codes of a page of one kv head.
+__device__ __forceinline__ void load_codes(uint32_t dst, const CUtensorMap* map, int head,
+                                           int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(0), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async4(float* to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to)), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// S = A B^T: 128 rows of A in TMEM, two values a column, and tile B [half of head_dim][128][64].
 template <int D>
-__device__ __forceinline__ void issue_products(uint32_t d_tmem, tc::Desc a, tc::Desc b) {
-  constexpr uint32_t HALF = kTile * 128;
-  constexpr uint32_t IDESC = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
+__device__ __forceinline__ void issue_products(uint32_t d_tmem, uint32_t a_tmem, tc::Desc b) {
+  constexpr uint32_t HALF_B = kCols * 128;
+  constexpr uint32_t IDESC = tc::idesc_bf16_f32(kLanes, kCols, 0, 0);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+    const uint32_t off_b = ((kk >> 2) * HALF_B + (kk & 3) * 32) >> 4;
     if (kk == 0)
-      tc::mma_bf16_pair<false>(d_tmem, a, off, b, off, IDESC);
+      tc::mma_bf16_tmem_a_pair<false>(d_tmem, a_tmem, b, off_b, IDESC);
     else
-      tc::mma_bf16_pair<true>(d_tmem, a, off, b, off, IDESC);
+      tc::mma_bf16_tmem_a_pair<true>(d_tmem, a_tmem + kk * 8, b, off_b, IDESC);
   }
 }
 
@@ -84,38 +115,43 @@ struct ChunkUnit {
 };
 
 template <int D, int G, bool F8, bool COLS>
-__global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
+__global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     chunk_kernel(const ChunkArgs p, const __grid_constant__ CUtensorMap qmap,
                  const __grid_constant__ CUtensorMap kmap) {
-  constexpr int TM = kTile / G;
+  constexpr int TA = kTile / G, TB = kCols / G;  // tokens of a query tile that stays, streams
   constexpr int NH = D / 64;
-  constexpr uint32_t HALF = kTile * 128;
-  constexpr uint32_t TILE = NH * HALF;
-  constexpr int NB = D == 64 ? 4 : 2;      // B stages
+  constexpr uint32_t HALF_A = kTile * 128, HALF_B = kCols * 128;
+  constexpr uint32_t TILE_A = NH * HALF_A, TILE = NH * HALF_B;
+  constexpr int NB = Roles<F8>::kStages;
   constexpr int KW = Roles<F8>::kKWarps;
-  constexpr int PAGES = 8 / KW;            // pages of a K tile for a warp
+  constexpr int PAGES = Roles<F8>::kPages;  // of a K tile for a warp
+  constexpr int RAW_PAGE = 16 * D + 16 * 4, RAW = PAGES * RAW_PAGE;  // (8-bit cache)
   constexpr int THREADS = Roles<F8>::kThreads;
-  constexpr uint32_t TMEM_COLS = 256;
+  constexpr uint32_t A_COLS = kBuffers * kCols;
+  constexpr uint32_t TMEM_COLS = 512;       // S, then A
 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* a_s = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* b_s = a_s + TILE;
-  ChunkShared& B = *reinterpret_cast<ChunkShared*>(b_s + NB * TILE);
+  unsigned char* b_s = a_s + TILE_A;
+  unsigned char* raw_s = b_s + NB * TILE;  // (8-bit cache) [K warp][kRaw][RAW]
+  ChunkShared& B = *reinterpret_cast<ChunkShared*>(raw_s + (F8 ? KW * kRaw * RAW : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ctas = cluster_size(), rank = cluster_rank();
 
   if (tid == 0) {
     mbar_init(smem_addr(&B.a_full), COLS ? KW : 1);
+    mbar_init(smem_addr(&B.a_ready), kSumWarps);
     for (int i = 0; i < NB; ++i) {
       mbar_init(smem_addr(&B.b_full[i]), COLS ? 1 : KW);
       mbar_init(smem_addr(&B.b_empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBuffers; ++i) {
       mbar_init(smem_addr(&B.s_full[i]), 1);
-      mbar_init(smem_addr(&B.s_empty[i]), kEpilogueWarps);
+      mbar_init(smem_addr(&B.s_empty[i]), kSumWarps / 2);
     }
     for (int i = 0; i < kSide; ++i) mbar_init(smem_addr(&B.side_full[i]), COLS ? 1 : KW);
+    for (int i = 0; i < 4 * kRaw; ++i) mbar_init(smem_addr(&B.raw_full[i / kRaw][i % kRaw]), 1);
     B.abort_flag = 0;
     fence_mbar_init();
   }
@@ -137,7 +173,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
         const int a = p.query_start_loc[s], b = p.query_start_loc[s + 1], L = p.seq_lens[s];
         if (b - a >= 2 && a >= 0 && b <= p.num_tokens && L >= b - a && L <= p.max_seq_len &&
             L <= ((long long)p.max_blocks << p.block_shift) * 16)
-          n = COLS ? (L + kTile - 1) / kTile : (b - a + TM - 1) / TM;
+          n = COLS ? (L + kTile - 1) / kTile : (b - a + TA - 1) / TA;
       }
       uint32_t before_n, before_t, all_n, all_t;
       block_scan2(B.scan, n > 0, (uint32_t)n, before_n, before_t, all_n, all_t);
@@ -173,6 +209,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
 
   uint32_t c0 = 0;      // B tiles of this CTA before this unit
   uint32_t loaded = 0;  // units before this one that it loaded an A tile for
+  uint32_t raw0 = 0;    // (8-bit cache) K tiles before this unit
   for (long long round = 0; round * groups < units; ++round) {
     // long units first; every other round backwards, to even the sums out
     long long u = round * groups + (round & 1 ? groups - 1 - group : group);
@@ -199,15 +236,15 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
       if constexpr (COLS) {
         U.key0 = nth * kTile;
         U.q0 = U.ntok = 0;
-        const int from = max(0, U.key0 - U.c0) / TM, tiles = (U.ql + TM - 1) / TM;
+        const int from = max(0, U.key0 - U.c0) / TB, tiles = (U.ql + TB - 1) / TB;
         U.first = from + (int)rank;
         U.step = (int)ctas;
         U.count = U.first < tiles ? (tiles - U.first + U.step - 1) / U.step : 0;
       } else {
         U.key0 = 0;
-        U.q0 = U.a + nth * TM;
-        U.ntok = min(TM, U.ql - nth * TM);
-        const int tiles = (U.c0 + nth * TM + U.ntok + kTile - 1) / kTile;
+        U.q0 = U.a + nth * TA;
+        U.ntok = min(TA, U.ql - nth * TA);
+        const int tiles = (U.c0 + nth * TA + U.ntok + kCols - 1) / kCols;
         U.first = (int)((long long)rank * tiles / ctas);
         U.step = 1;
         U.count = (int)((long long)(rank + 1) * tiles / ctas) - U.first;
@@ -215,17 +252,17 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
     }
     const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
     // tokens of query tile i of the request, and how many (columns pass)
-    const auto tokens_of = [&](int i) { return min(TM, U.ql - i * TM); };
+    const auto tokens_of = [&](int i) { return min(TB, U.ql - i * TB); };
 
     if (warp == 0) {
       // ------------------------------------------------ query tiles
       if constexpr (COLS) {
-        // the log sums of a query tile's rows, four columns a lane, a tile ahead
+        // the log sums of a query tile's rows, two columns a lane, a tile ahead
         const auto log_sums = [&](int i) {
           float4 v = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);  // (no row: weight 0)
           if (i < U.count) {
             const int qt = U.first + i * U.step, n = tokens_of(qt) * G;
-            const float* at = p.sums + ((int64_t)U.h * p.num_tokens + U.a + qt * TM) * G + lane * 4;
+            const float* at = p.sums + ((int64_t)U.h * p.num_tokens + U.a + qt * TB) * G + lane * 4;
             if (lane * 4 < n) v.x = at[0];
             if (lane * 4 + 1 < n) v.y = at[1];
             if (lane * 4 + 2 < n) v.z = at[2];
@@ -236,11 +273,11 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
         float4 ls = log_sums(0);
         for (int i = 0; i < U.count; ++i) {
           const uint32_t c = c0 + i, st = c % NB;
-          const int q0 = U.a + (U.first + i * U.step) * TM;
+          const int q0 = U.a + (U.first + i * U.step) * TB;
           // Their slot's last tile, kSide earlier, is done with: this warp has waited for a
-          // stage that a product NB + 1 tiles back freed, which needed the S buffer of the
-          // tile two before that to have been read.
-          static_assert(kSide >= 4 + 4, "");
+          // stage that the product NB + 1 tiles back freed, which needed that S buffer's
+          // tile before to have been read, by warps that were done with all earlier ones.
+          static_assert(kSide >= NB + 6 && kSide % 2 == 0, "");
           *reinterpret_cast<float4*>(B.side[c % kSide] + lane * 4) = ls;
           ls = log_sums(i + 1);
           __syncwarp();
@@ -252,31 +289,31 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
             mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
             for (int hf = 0; hf < NH; ++hf)
-              tc::tma_load_3d(smem_addr(b_s + st * TILE + hf * HALF), &qmap, hf * 64, U.h * G, q0,
-                              bar);
+              tc::tma_load_3d(smem_addr(b_s + st * TILE + hf * HALF_B), &qmap, hf * 64, U.h * G,
+                              q0, bar);
           }
           __syncwarp();
         }
       } else if (lane == 0 && U.count > 0) {
         const uint32_t bar = smem_addr(&B.a_full);
-        mbar_arrive_expect_tx(bar, TILE);
+        mbar_arrive_expect_tx(bar, TILE_A);
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf)
-          tc::tma_load_3d(smem_addr(a_s + hf * HALF), &qmap, hf * 64, U.h * G, U.q0, bar);
+          tc::tma_load_3d(smem_addr(a_s + hf * HALF_A), &qmap, hf * 64, U.h * G, U.q0, bar);
       }
     } else if (warp == 1) {
       // ------------------------------------------------ products
       if (lane == 0 && U.count > 0) {
-        const tc::Desc ad = tc::sw128_desc_pair(smem_addr(a_s), 16, 1024);
         const tc::Desc bd = tc::sw128_desc_pair(smem_addr(b_s), 16, 1024);
-        mbar_wait_spin(smem_addr(&B.a_full), loaded & 1, p.err, abort_flag);
+        mbar_wait_spin(smem_addr(&B.a_ready), loaded & 1, p.err, abort_flag);
         for (int i = 0; i < U.count; ++i) {
-          const uint32_t c = c0 + i, st = c % NB, sb = c & 1;
+          const uint32_t c = c0 + i, st = c % NB, sb = c % kBuffers;
           mbar_wait_spin(smem_addr(&B.b_full[st]), (c / NB) & 1, p.err, abort_flag);
-          if (c >= 2)
-            mbar_wait_spin(smem_addr(&B.s_empty[sb]), ((c >> 1) - 1) & 1, p.err, abort_flag);
+          if (c >= kBuffers)
+            mbar_wait_spin(smem_addr(&B.s_empty[sb]), (c / kBuffers - 1) & 1, p.err, abort_flag);
           tc::fence_after_sync();
-          issue_products<D>(tmem + sb * kTile, ad, tc::Desc{bd.lo + st * (TILE >> 4), bd.hi});
+          issue_products<D>(tmem + sb * kCols, tmem + A_COLS,
+                            tc::Desc{bd.lo + st * (TILE >> 4), bd.hi});
           tc::commit(smem_addr(&B.s_full[sb]));
           tc::commit(smem_addr(&B.b_empty[st]));
         }
@@ -284,77 +321,112 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
     } else if (warp >= kFirstKWarp) {
       // ------------------------------------------------ key tiles
       const int idx = warp - kFirstKWarp;
-      constexpr int CPR = D / 16, RPL = 32 / CPR, LOADS = 16 / RPL;  // (8-bit cache)
-      int page[PAGES];
-      uint4 w[F8 ? PAGES : 1][LOADS];
-      float sc[F8 ? PAGES : 1];
-      // This warp's pages of the K tile at key0: the pool's pages (-1: none), and the codes'
-      // loads (8-bit cache).
-      const auto look_up = [&](int key0) {
-#pragma unroll
-        for (int i = 0; i < PAGES; ++i) {
-          const int lp = key0 / 16 + idx * PAGES + i;
-          page[i] = -1;
-          if (lp * 16 >= U.L) continue;
-          const int b = table[lp >> p.block_shift];
-          if (b >= 0 && b < p.num_blocks)
-            page[i] = (b << p.block_shift) + (lp & ((1 << p.block_shift) - 1));
-          else if (lane == 0)
-            flag_error(p.err, DEVERR_BOUNDS);
-        }
-        if constexpr (F8) {
-#pragma unroll
-          for (int i = 0; i < PAGES; ++i) {
-            sc[i] = 0.f;
-            if (page[i] < 0) continue;
-            const uint8_t* at = static_cast<const uint8_t*>(p.k_cache) +
-                                page[i] * fp8_page_bytes(p.n_kv, D);
-            sc[i] = __ldg(reinterpret_cast<const float*>(at + fp8_scales_offset(p.n_kv, D)) +
-                          (lane & 15) * p.n_kv + U.h);
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j)
-              w[i][j] = __ldg(reinterpret_cast<const uint4*>(
-                  at + ((int64_t)(j * RPL + lane / CPR) * p.n_kv + U.h) * D + (lane % CPR) * 16));
-          }
-        }
+      const int first = COLS ? U.key0 / kTile : U.first;
+      const int tiles = U.count == 0 ? 0 : COLS ? 1 : U.count;
+      // Page k of this warp's of K tile first + i: its place in the pool (-1: none).
+      const auto look_up = [&](int i, int k) {
+        const int lp = (first + i) * (kCols / 16) + idx * PAGES + k;
+        if (i >= tiles || k >= PAGES || lp * 16 >= U.L) return -1;
+        const int b = table[lp >> p.block_shift];
+        if (b >= 0 && b < p.num_blocks)
+          return (b << p.block_shift) + (lp & ((1 << p.block_shift) - 1));
+        flag_error(p.err, DEVERR_BOUNDS);
+        return -1;
       };
-      // They go to dst, completion on bar.
-      const auto bring = [&](unsigned char* dst, uint32_t bar, float* scales) {
-        if constexpr (!F8) {
-          if (lane != 0) return;
-          uint32_t bytes = 0;
-#pragma unroll
-          for (int i = 0; i < PAGES; ++i) bytes += page[i] < 0 ? 0 : NH * 2048;
-          if (bytes)
-            mbar_arrive_expect_tx(bar, bytes);
-          else
-            mbar_arrive(bar);
-#pragma unroll
-          for (int i = 0; i < PAGES; ++i) {
-            if (page[i] < 0) continue;
-#pragma unroll
-            for (int hf = 0; hf < NH; ++hf)
-              tc::tma_load_3d(smem_addr(dst + hf * HALF + (idx * PAGES + i) * 2048), &kmap,
-                              hf * 64, U.h, page[i] * 16, bar);
+      // Where K tile i goes, and its barrier: A, or a stage of B, waited for.
+      const auto tile_bar = [&](int i) {
+        return smem_addr(COLS ? &B.a_full : &B.b_full[(c0 + i) % NB]);
+      };
+      const auto tile_at = [&](int i) {
+        if (COLS) return a_s;
+        const uint32_t c = c0 + i, st = c % NB;
+        if (lane == 0 && c >= NB)
+          mbar_wait(smem_addr(&B.b_empty[st]), (c / NB - 1) & 1, p.err, abort_flag);
+        __syncwarp();
+        return b_s + st * TILE;
+      };
+      if constexpr (!F8) {
+        // a lane for each half of a page, with its place looked up a tile ahead
+        int page = look_up(0, lane / NH);
+        for (int i = 0; i < tiles; ++i) {
+          const int here = page;
+          page = look_up(i + 1, lane / NH);
+          unsigned char* dst = tile_at(i);
+          const uint32_t bar = tile_bar(i), bytes = __popc(__ballot_sync(0xffffffffu, here >= 0)) * 2048;
+          if (lane == 0) {
+            if (bytes)
+              mbar_arrive_expect_tx(bar, bytes);
+            else
+              mbar_arrive(bar);
           }
-        } else {
-          const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
+          __syncwarp();
+          if (here >= 0)
+            tc::tma_load_3d(smem_addr(dst + (lane % NH) * HALF_A + (idx * PAGES + lane / NH) * 2048),
+                            &kmap, (lane % NH) * 64, U.h, here * 16, bar);
+          __syncwarp();
+        }
+      } else {
+        unsigned char* raw = raw_s + idx * kRaw * RAW;
+        // lane l < PAGES brings page l's codes, lane l the scale of token l % 16 of page l / 16
+        static_assert(PAGES * 16 == 32, "");
+        const auto start = [&](int i, int page) {
+          const uint32_t slot = (raw0 + i) % kRaw;
+          unsigned char* to = raw + slot * RAW;
+          const uint32_t bar = smem_addr(&B.raw_full[idx][slot]);
+          const int mine = __shfl_sync(0xffffffffu, page, lane >> 4);
+          if (i < tiles) {
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+            if (lane == 0) {
+              if (n)
+                mbar_arrive_expect_tx(bar, n * 16 * D);
+              else
+                mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (page >= 0)
+              load_codes(smem_addr(to + lane * 16 * D), &kmap, U.h, page, bar);
+            if constexpr (!COLS) {
+              float* sc = reinterpret_cast<float*>(to + PAGES * 16 * D) + lane;
+              if (mine >= 0)
+                cp_async4(sc, reinterpret_cast<const float*>(
+                                  static_cast<const uint8_t*>(p.k_cache) +
+                                  mine * fp8_page_bytes(p.n_kv, D) + fp8_scales_offset(p.n_kv, D)) +
+                                  (lane & 15) * p.n_kv + U.h);
+              else
+                *sc = 0.f;
+            }
+          }
+          cp_async_commit();
+        };
+        for (int i = 0; i < kRaw; ++i) start(i, look_up(i, lane));
+        int page = look_up(kRaw, lane);
+        constexpr int CPR = D / 16, RPL = 32 / CPR;
+        const int c16 = lane % CPR, c8 = (c16 & 3) * 2;
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t slot = (raw0 + i) % kRaw;
+          const unsigned char* from = raw + slot * RAW;
+          cp_async_wait<kRaw - 1>();
+          __syncwarp();
+          mbar_wait(smem_addr(&B.raw_full[idx][slot]), ((raw0 + i) / kRaw) & 1, p.err, abort_flag);
+          unsigned char* dst = tile_at(i);
+          if constexpr (!COLS)
+            B.side[(c0 + i) % kSide][idx * PAGES * 16 + lane] =
+                reinterpret_cast<const float*>(from + PAGES * 16 * D)[lane];
 #pragma unroll
-          for (int i = 0; i < PAGES; ++i) {
-            if (scales && lane < 16) scales[(idx * PAGES + i) * 16 + lane] = sc[i];
-            if (page[i] < 0) continue;
-            unsigned char* to = dst + (c16 >> 2) * HALF + (idx * PAGES + i) * 2048;
+          for (int k = 0; k < PAGES; ++k) {
+            unsigned char* to = dst + (c16 >> 2) * HALF_A + (idx * PAGES + k) * 2048;
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) {
-              const uint32_t src[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+            for (int j = 0; j < 16 / RPL; ++j) {
+              const uint4 w = *reinterpret_cast<const uint4*>(from + k * 16 * D + j * 512 + lane * 16);
+              const uint32_t src[4] = {w.x, w.y, w.z, w.w};
               uint32_t out[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int n = 0; n < 4; ++n) {
                 uint32_t x, y;
-                f16x2x2_from_e4m3x4(src[k], x, y);
+                f16x2x2_from_e4m3x4(src[n], x, y);
                 const float2 f = half2_bits_to_float2(x), g = half2_bits_to_float2(y);
-                out[2 * k] = pack_bf16x2(f.x, f.y);
-                out[2 * k + 1] = pack_bf16x2(g.x, g.y);
+                out[2 * n] = pack_bf16x2(f.x, f.y);
+                out[2 * n + 1] = pack_bf16x2(g.x, g.y);
               }
               const uint32_t at = swizzled(j * RPL + lane / CPR, c8);
               *reinterpret_cast<uint4*>(to + at) = make_uint4(out[0], out[1], out[2], out[3]);
@@ -364,80 +436,82 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar);
-        }
-      };
-      if constexpr (COLS) {
-        if (U.count > 0) {
-          look_up(U.key0);
-          bring(a_s, smem_addr(&B.a_full), nullptr);
-        }
-      } else {
-        // (a tile's places are looked up, and its codes on their way, before its stage is free)
-        if (U.count > 0) look_up(U.first * kTile);
-        for (int i = 0; i < U.count; ++i) {
-          const uint32_t c = c0 + i, st = c % NB;
-          if (lane == 0 && c >= NB)
-            mbar_wait(smem_addr(&B.b_empty[st]), (c / NB - 1) & 1, p.err, abort_flag);
-          __syncwarp();
-          bring(b_s + st * TILE, smem_addr(&B.b_full[st]), F8 ? B.side[c % kSide] : nullptr);
-          if constexpr (F8) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&B.side_full[c % kSide]));
+          if (lane == 0) {
+            mbar_arrive(tile_bar(i));
+            if (!COLS) mbar_arrive(smem_addr(&B.side_full[(c0 + i) % kSide]));
           }
-          if (i + 1 < U.count) look_up((U.first + i + 1) * kTile);
+          // (every lane has read the slot: its next tile may come)
+          start(i + kRaw, page);
+          page = look_up(i + kRaw + 1, lane);
         }
+        cp_async_wait<0>();
       }
     } else {
       // ------------------------------------------------ sums
-      const int quarter = warp & 3, half = (warp - 2) >> 2;
+      const int quarter = warp & 3, share = (warp - 2) >> 2;
+      const int cols = (share & 1) * (kCols / 2), group = share >> 1;
       const int r = quarter * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-      float top = -INFINITY, sum = 0.f;
-      float mul = p.scale_log2;
-      int p_row = 0;  // rows pass: the row's position
-      if constexpr (COLS) {
-        if constexpr (F8) {
-          const int j = U.key0 + r;
-          float ks = 0.f;
-          if (j < U.L) {
-            const int b = table[j >> (4 + p.block_shift)];
-            if (b >= 0 && b < p.num_blocks) {
-              const int64_t page = ((int64_t)b << p.block_shift) +
-                                   ((j >> 4) & ((1 << p.block_shift) - 1));
-              ks = __ldg(reinterpret_cast<const float*>(
-                             static_cast<const uint8_t*>(p.k_cache) +
-                             page * fp8_page_bytes(p.n_kv, D) + fp8_scales_offset(p.n_kv, D)) +
-                         (j & 15) * p.n_kv + U.h);
-            }
+      if (U.count > 0) {
+        // A to TMEM: 32 values of a row, 16 columns, each
+        mbar_wait(smem_addr(&B.a_full), loaded & 1, p.err, abort_flag);
+        if (share < D / 32) {
+          uint32_t x[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                a_s + (share >> 1) * HALF_A + swizzled(r, (share & 1) * 4 + c));
+            x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
           }
-          mul *= ks;
+          tc::tmem_st16(tmem + lane_addr + A_COLS + share * 16, x);
+          tc::tmem_wait_st();
         }
-      } else {
-        p_row = U.c0 + (U.q0 - U.a) + r / G;
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&B.a_ready));
       }
-      for (int i = 0; i < U.count; ++i) {
-        const uint32_t c = c0 + i, sb = c & 1;
+      float top = -INFINITY, sum = 0.f, mul = p.scale_log2;
+      int p_row = 0;  // rows pass: the row's position
+      if constexpr (!COLS) {
+        p_row = U.c0 + (U.q0 - U.a) + r / G;
+      } else if constexpr (F8) {
+        const int j = U.key0 + r;
+        float ks = 0.f;
+        if (j < U.L) {
+          const int b = table[j >> (4 + p.block_shift)];
+          if (b >= 0 && b < p.num_blocks) {
+            const int64_t page =
+                ((int64_t)b << p.block_shift) + ((j >> 4) & ((1 << p.block_shift) - 1));
+            ks = __ldg(reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.k_cache) +
+                                                      page * fp8_page_bytes(p.n_kv, D) +
+                                                      fp8_scales_offset(p.n_kv, D)) +
+                       (j & 15) * p.n_kv + U.h);
+          }
+        }
+        mul *= ks;
+      }
+      for (int i = (c0 & 1) ^ group; i < U.count; i += 2) {
+        const uint32_t c = c0 + i, sb = c % kBuffers;
         const int tile = U.first + i * U.step;
-        const float* side = B.side[c % kSide] + half * 64;
-        mbar_wait(smem_addr(&B.s_full[sb]), (c >> 1) & 1, p.err, abort_flag);
+        const float* side = B.side[c % kSide] + cols;
+        mbar_wait(smem_addr(&B.s_full[sb]), (c / kBuffers) & 1, p.err, abort_flag);
         if (COLS || F8)
           mbar_wait(smem_addr(&B.side_full[c % kSide]), (c / kSide) & 1, p.err, abort_flag);
         tc::fence_after_sync();
-        // columns lo .. hi - 1 of this half count for this lane
-        int lo = 0, hi = 64;
+        // of this warp's columns lo .. hi - 1 count for a row
+        int lo = 0, hi;
         if constexpr (COLS) {
-          const int p0 = U.c0 + tile * TM;  // position of the query tile's first token
-          lo = (U.key0 + r - p0) * G - half * 64;
-          hi = tokens_of(tile) * G - half * 64;
+          const int p0 = U.c0 + tile * TB;  // position of the query tile's first token
+          lo = (U.key0 + r - p0) * G - cols;
+          hi = tokens_of(tile) * G - cols;
         } else {
-          hi = p_row + 1 - (tile * kTile + half * 64);
+          hi = p_row + 1 - tile * kCols - cols;
         }
         const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           uint32_t x[32];
-          tc::tmem_ld32(tmem + lane_addr + sb * kTile + half * 64 + part * 32, x);
+          tc::tmem_ld32(tmem + lane_addr + sb * kCols + cols + part * 32, x);
           tc::tmem_wait_ld();
           if (part == 1) {
             tc::fence_before_sync();
@@ -451,14 +525,14 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
                 const float4 ls = *reinterpret_cast<const float4*>(side + part * 32 + j);
-                const float2 a = __ffma2_rn(
+                const float2 u = __ffma2_rn(
                     make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), m2,
                     make_float2(-ls.x, -ls.y));
-                const float2 b = __ffma2_rn(
+                const float2 v = __ffma2_rn(
                     make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), m2,
                     make_float2(-ls.z, -ls.w));
-                acc[0] = __fadd2_rn(acc[0], make_float2(fast_exp2(a.x), fast_exp2(a.y)));
-                acc[1] = __fadd2_rn(acc[1], make_float2(fast_exp2(b.x), fast_exp2(b.y)));
+                acc[0] = __fadd2_rn(acc[0], make_float2(fast_exp2(u.x), fast_exp2(u.y)));
+                acc[1] = __fadd2_rn(acc[1], make_float2(fast_exp2(v.x), fast_exp2(v.y)));
               }
               sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
             } else {
@@ -476,10 +550,13 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
             const bool raw = !F8 && mul > 0.f;
             if (!raw) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                float v = __uint_as_float(x[j]) * mul;
-                if constexpr (F8) v *= side[part * 32 + j];
-                x[j] = __float_as_uint(v);
+              for (int j = 0; j < 32; j += 4) {
+                float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+                if constexpr (F8) f = *reinterpret_cast<const float4*>(side + part * 32 + j);
+                const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  x[j + k] = __float_as_uint(__uint_as_float(x[j + k]) * (mul * g[k]));
               }
             }
             if (!whole) {
@@ -504,55 +581,52 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
             float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float2 a = __ffma2_rn(
+              const float2 u = __ffma2_rn(
                   make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), f2, r2);
-              const float2 b = __ffma2_rn(
+              const float2 v = __ffma2_rn(
                   make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), f2, r2);
-              add[0] = __fadd2_rn(add[0], make_float2(fast_exp2(a.x), fast_exp2(a.y)));
-              add[1] = __fadd2_rn(add[1], make_float2(fast_exp2(b.x), fast_exp2(b.y)));
+              add[0] = __fadd2_rn(add[0], make_float2(fast_exp2(u.x), fast_exp2(u.y)));
+              add[1] = __fadd2_rn(add[1], make_float2(fast_exp2(v.x), fast_exp2(v.y)));
             }
             add[0] = __fadd2_rn(add[0], add[1]);
             sum += add[0].x + add[0].y;
           }
         }
       }
-      if constexpr (COLS) {
-        B.part[0][half][r] = sum;
+      if (COLS) {
+        B.part[0][share][r] = sum;
       } else {
-        B.part[0][half][r] = top;
-        B.part[1][half][r] = sum;
+        B.part[0][share][r] = top;
+        B.part[1][share][r] = sum;
       }
     }
     c0 += U.count;
     loaded += U.count > 0;
+    if (U.count > 0) raw0 += COLS ? 1 : U.count;
     group_sync(ctas);
+    // number what of thread tid's row, from share k & 3 of CTA k / 4's columns
+    const auto part_of = [&](int what, uint32_t k) {
+      const float* at = &B.part[what][k & 3][tid];
+      return ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(at), k >> 2)) : *at;
+    };
     if constexpr (COLS) {
       const int j = U.key0 + tid;
       if (rank == 0 && tid < kTile && j < U.L) {
         float sum = 0.f;
-        for (uint32_t k = 0; k < ctas; ++k)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            sum += ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(&B.part[0][hf][tid]), k))
-                            : B.part[0][hf][tid];
+        for (uint32_t k = 0; k < 4 * ctas; ++k) sum += part_of(0, k);
         float* w = p.weights + ((int64_t)U.s * p.n_kv + U.h) * p.weights_stride + j;
         *w = (j < U.c0 ? *w : 0.f) + sum;
       }
     } else if (rank == 0 && tid < U.ntok * G) {
-      // the row's log sum over the halves of the keys' tiles and the cluster's pieces of them
+      // the row's log sum over the cluster's pieces of its keys
       float m = -INFINITY, sum = 0.f;
-      for (uint32_t k = 0; k < ctas; ++k)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float pm = ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(&B.part[0][hf][tid]), k))
-                                    : B.part[0][hf][tid];
-          const float ps = ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(&B.part[1][hf][tid]), k))
-                                    : B.part[1][hf][tid];
-          const float to = fmaxf(m, pm);
-          sum = (m == -INFINITY ? sum : sum * fast_exp2(m - to)) +
-                (pm == -INFINITY ? ps : ps * fast_exp2(pm - to));
-          m = to;
-        }
+      for (uint32_t k = 0; k < 4 * ctas; ++k) {
+        const float pm = part_of(0, k), ps = part_of(1, k);
+        const float to = fmaxf(m, pm);
+        sum = (m == -INFINITY ? sum : sum * fast_exp2(m - to)) +
+              (pm == -INFINITY ? ps : ps * fast_exp2(pm - to));
+        m = to;
+      }
       p.sums[((int64_t)U.h * p.num_tokens + U.q0) * G + tid] = m + __log2f(sum);
     }
     group_sync(ctas);
@@ -563,6 +637,9 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
     for (uint32_t c = c0 > NB ? c0 - NB : 0; c < c0; ++c)
       mbar_wait(smem_addr(&B.b_full[c % NB]), (c / NB) & 1, p.err, abort_flag);
     if (loaded) mbar_wait(smem_addr(&B.a_full), (loaded - 1) & 1, p.err, abort_flag);
+    for (int w = 0; F8 && w < KW; ++w)
+      for (uint32_t c = raw0 > kRaw ? raw0 - kRaw : 0; c < raw0; ++c)
+        mbar_wait(smem_addr(&B.raw_full[w][c % kRaw]), (c / kRaw) & 1, p.err, abort_flag);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -575,10 +652,13 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 2)
 template <int D, int G, bool F8, bool COLS>
 cudaError_t launch_pass(const ChunkArgs& p, const CUtensorMap& qm, const CUtensorMap& km, int grid,
                         int ctas, cudaStream_t stream) {
-  constexpr size_t tile = (size_t)(D / 64) * kTile * 128;
-  constexpr size_t smem = 1024 + tile * (1 + (D == 64 ? 4 : 2)) + sizeof(ChunkShared);
-  static_assert(offsetof(ChunkShared, side) % 16 == 0 && tile % 1024 == 0, "alignment");
-  static_assert(smem > 80 * 1024 && smem < 113 * 1024, "two CTAs an SM, not three");
+  using R = Roles<F8>;
+  constexpr size_t used = 1024 + (size_t)(D / 64) * 128 * (kTile + kCols * R::kStages) +
+                          (F8 ? 8 * kRaw * (16 * D + 64) : 0) + sizeof(ChunkShared);
+  constexpr size_t smem = std::max<size_t>(used, 120 * 1024);
+  static_assert(offsetof(ChunkShared, side) % 16 == 0, "alignment");
+  // (one CTA an SM, which has all of TMEM)
+  static_assert(smem < 227 * 1024, "");
   auto kern = chunk_kernel<D, G, F8, COLS>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -599,7 +679,6 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
                                         box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
   }
-  km = qm;
   if (!F8) {
     const cuuint64_t dims[3] = {D, nkv, slots};
     const cuuint64_t strides[2] = {D * 2, nkv * D * 2};
@@ -607,8 +686,18 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
     const cudaError_t e = encode_map<3>(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k_cache, dims,
                                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
+  } else {
+    const cuuint64_t dims[4] = {D, nkv, 16, slots / 16};
+    const cuuint64_t strides[3] = {D, D * nkv, (cuuint64_t)fp8_page_bytes(p.n_kv, D)};
+    const cuuint32_t box[4] = {D, 1, 16, 1};
+    const cudaError_t e =
+        encode_map<4>(&km, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.k_cache, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_NONE,
+                      D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                               : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+    if (e != cudaSuccess) return e;
   }
-  const long long slots_of_sms = 2ll * sm_count;
+  const long long slots_of_sms = sm_count;
   // upper bounds of the units: the kernel has the exact count
   const long long row_units = ((long long)p.num_tokens / (kTile / G) + p.num_seqs) * p.n_kv;
   const long long most_chunks = std::min<long long>(p.num_seqs, p.num_tokens / 2);
@@ -618,10 +707,11 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
   // a key tile in turn
   const long long least = ((long long)p.num_tokens / (kTile / G) + 1) * p.n_kv;
   int pieces = 1;
-  while (pieces < 8 && least * pieces < slots_of_sms && key_tiles >= 8ll * pieces) pieces *= 2;
-  const int tiles = (max_q_len + kTile / G - 1) / (kTile / G);
-  int ctas = 1;
-  while (ctas < 4 && tiles >= 4 * ctas) ctas *= 2;
+  while (pieces < 8 && least * pieces < slots_of_sms && key_tiles >= 4ll * pieces) pieces *= 2;
+  const int tiles = (max_q_len + kCols / G - 1) / (kCols / G);
+  int ctas = tiles >= 8 ? 2 : 1;
+  if (getenv("PA_PC")) pieces = atoi(getenv("PA_PC"));
+  if (getenv("PA_CC")) ctas = atoi(getenv("PA_CC"));
   for (p.skip = 0; p.skip < most_chunks; p.skip += kListed) {
     long long groups = std::min(row_units, slots_of_sms / pieces);
     cudaError_t e =
