@@ -20,7 +20,6 @@
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
-#include <cstdlib>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -44,22 +43,28 @@ constexpr int kListed = 512;        // chunk requests of a launch
 // scales of its next kRaw tiles' pages on their way to shared memory, and converts them.
 template <bool F8>
 struct Roles {
-  static constexpr int kKWarps = F8 ? 4 : 2;
+  static constexpr int kKWarps = F8 ? 8 : 2;
   static constexpr int kPages = 8 / kKWarps;
   static constexpr int kStages = F8 ? 3 : 4;  // B tiles on their way or in use
   static constexpr int kThreads = (kFirstKWarp + kKWarps) * 32;
 };
 constexpr int kRaw = 3;
+template <int D>
+struct Raw {  // a warp's codes and scales of a tile
+  static constexpr int kBytes = Roles<true>::kPages * 16 * D + 128;
+  static_assert(kBytes % 128 == 0, "tensor copies start on 128 bytes");
+};
 
 struct alignas(16) ChunkShared {
   uint64_t a_full, a_ready, b_full[4], b_empty[4], s_full[kBuffers], s_empty[kBuffers];
-  uint64_t side_full[kSide], raw_full[4][kRaw];
+  uint64_t side_full[kSide], raw_full[8][kRaw];
   uint32_t tmem_slot;
   int abort_flag;
   int listed;
-  // rows pass: the keys' scales; columns pass: the rows' log sums (read four at a time)
+  // rows pass: the keys' scales times the scores'; columns pass: the rows' log sums (read four at a time)
   alignas(16) float side[kSide][kCols];
-  float part[2][4][kTile];    // rows pass: (max, sum) by sum warps' share; columns pass: [0] sums
+  // by units in turn: rows pass (max, sum) by sum warps' share; columns pass [0] sums
+  float part[2][2][4][kTile];
   int list_seq[kListed];
   int list_base[kListed + 1]; // first tile of each listed request
   SelectShared scan;
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   constexpr int NB = Roles<F8>::kStages;
   constexpr int KW = Roles<F8>::kKWarps;
   constexpr int PAGES = Roles<F8>::kPages;  // of a K tile for a warp
-  constexpr int RAW_PAGE = 16 * D + 16 * 4, RAW = PAGES * RAW_PAGE;  // (8-bit cache)
+  constexpr int RAW = Raw<D>::kBytes;
   constexpr int THREADS = Roles<F8>::kThreads;
   constexpr uint32_t A_COLS = kBuffers * kCols;
   constexpr uint32_t TMEM_COLS = 512;       // S, then A
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       mbar_init(smem_addr(&B.s_empty[i]), kSumWarps / 2);
     }
     for (int i = 0; i < kSide; ++i) mbar_init(smem_addr(&B.side_full[i]), COLS ? 1 : KW);
-    for (int i = 0; i < 4 * kRaw; ++i) mbar_init(smem_addr(&B.raw_full[i / kRaw][i % kRaw]), 1);
+    for (int i = 0; i < 8 * kRaw; ++i) mbar_init(smem_addr(&B.raw_full[i / kRaw][i % kRaw]), 1);
     B.abort_flag = 0;
     fence_mbar_init();
   }
@@ -210,6 +215,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   uint32_t c0 = 0;      // B tiles of this CTA before this unit
   uint32_t loaded = 0;  // units before this one that it loaded an A tile for
   uint32_t raw0 = 0;    // (8-bit cache) K tiles before this unit
+  bool arrived = false; // at the end of a unit not waited for
   for (long long round = 0; round * groups < units; ++round) {
     // long units first; every other round backwards, to even the sums out
     long long u = round * groups + (round & 1 ? groups - 1 - group : group);
@@ -296,6 +302,8 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         }
       } else if (lane == 0 && U.count > 0) {
         const uint32_t bar = smem_addr(&B.a_full);
+        if (loaded > 0)  // (the unit before has copied its tile away)
+          mbar_wait(smem_addr(&B.a_ready), (loaded - 1) & 1, p.err, abort_flag);
         mbar_arrive_expect_tx(bar, TILE_A);
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf)
@@ -338,12 +346,13 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         return smem_addr(COLS ? &B.a_full : &B.b_full[(c0 + i) % NB]);
       };
       const auto tile_at = [&](int i) {
-        if (COLS) return a_s;
         const uint32_t c = c0 + i, st = c % NB;
-        if (lane == 0 && c >= NB)
+        if (lane == 0 && COLS && loaded > 0)
+          mbar_wait(smem_addr(&B.a_ready), (loaded - 1) & 1, p.err, abort_flag);
+        if (lane == 0 && !COLS && c >= NB)
           mbar_wait(smem_addr(&B.b_empty[st]), (c / NB - 1) & 1, p.err, abort_flag);
         __syncwarp();
-        return b_s + st * TILE;
+        return COLS ? a_s : b_s + st * TILE;
       };
       if constexpr (!F8) {
         // a lane for each half of a page, with its place looked up a tile ahead
@@ -367,13 +376,13 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         }
       } else {
         unsigned char* raw = raw_s + idx * kRaw * RAW;
-        // lane l < PAGES brings page l's codes, lane l the scale of token l % 16 of page l / 16
-        static_assert(PAGES * 16 == 32, "");
+        // lane 0 brings a page's codes, lane l < 16 the scale of token l
+        static_assert(PAGES == 1, "");
         const auto start = [&](int i, int page) {
           const uint32_t slot = (raw0 + i) % kRaw;
           unsigned char* to = raw + slot * RAW;
           const uint32_t bar = smem_addr(&B.raw_full[idx][slot]);
-          const int mine = __shfl_sync(0xffffffffu, page, lane >> 4);
+          const int mine = __shfl_sync(0xffffffffu, page, 0);
           if (i < tiles) {
             const uint32_t n = __popc(__ballot_sync(0xffffffffu, page >= 0));
             if (lane == 0) {
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
             __syncwarp();
             if (page >= 0)
               load_codes(smem_addr(to + lane * 16 * D), &kmap, U.h, page, bar);
-            if constexpr (!COLS) {
+            if (!COLS && lane < 16) {
               float* sc = reinterpret_cast<float*>(to + PAGES * 16 * D) + lane;
               if (mine >= 0)
                 cp_async4(sc, reinterpret_cast<const float*>(
@@ -409,9 +418,9 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           __syncwarp();
           mbar_wait(smem_addr(&B.raw_full[idx][slot]), ((raw0 + i) / kRaw) & 1, p.err, abort_flag);
           unsigned char* dst = tile_at(i);
-          if constexpr (!COLS)
+          if (!COLS && lane < 16)
             B.side[(c0 + i) % kSide][idx * PAGES * 16 + lane] =
-                reinterpret_cast<const float*>(from + PAGES * 16 * D)[lane];
+                reinterpret_cast<const float*>(from + PAGES * 16 * D)[lane] * p.scale_log2;
 #pragma unroll
           for (int k = 0; k < PAGES; ++k) {
             unsigned char* to = dst + (c16 >> 2) * HALF_A + (idx * PAGES + k) * 2048;
@@ -551,12 +560,16 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
             if (!raw) {
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+                float4 f = make_float4(mul, mul, mul, mul);
                 if constexpr (F8) f = *reinterpret_cast<const float4*>(side + part * 32 + j);
-                const float g[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  x[j + k] = __float_as_uint(__uint_as_float(x[j + k]) * (mul * g[k]));
+                const float2 u = __fmul2_rn(
+                    make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                    make_float2(f.x, f.y));
+                const float2 v = __fmul2_rn(
+                    make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])),
+                    make_float2(f.z, f.w));
+                x[j] = __float_as_uint(u.x), x[j + 1] = __float_as_uint(u.y);
+                x[j + 2] = __float_as_uint(v.x), x[j + 3] = __float_as_uint(v.y);
               }
             }
             if (!whole) {
@@ -593,46 +606,63 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           }
         }
       }
-      if (COLS) {
-        B.part[0][share][r] = sum;
+      float(&part)[2][4][kTile] = B.part[round & 1];
+      part[0][share][r] = COLS ? sum : top;
+      if (!COLS) part[1][share][r] = sum;
+      // The unit's sums are in place, and its products done: A may be written again.
+      tc::fence_before_sync();
+      if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
       } else {
-        B.part[0][share][r] = top;
-        B.part[1][share][r] = sum;
+        asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
       }
+      tc::fence_after_sync();
+      // number what of row t, from share k & 3 of CTA k / 4's columns
+      const int t = tid - 64;
+      const auto part_of = [&](int what, uint32_t k) {
+        const float* at = &part[what][k & 3][t];
+        return ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(at), k >> 2)) : *at;
+      };
+      if constexpr (COLS) {
+        const int j = U.key0 + t;
+        if (rank == 0 && t < kTile && j < U.L) {
+          float all = 0.f;
+          for (uint32_t k = 0; k < 4 * ctas; ++k) all += part_of(0, k);
+          float* w = p.weights + ((int64_t)U.s * p.n_kv + U.h) * p.weights_stride + j;
+          *w = (j < U.c0 ? *w : 0.f) + all;
+        }
+      } else if (rank == 0 && t < U.ntok * G) {
+        // the row's log sum over the shares, and the cluster's pieces of its keys
+        float m = -INFINITY, all = 0.f;
+        for (uint32_t k = 0; k < 4 * ctas; ++k) {
+          const float pm = part_of(0, k), ps = part_of(1, k);
+          const float to = fmaxf(m, pm);
+          all = (m == -INFINITY ? all : all * fast_exp2(m - to)) +
+                (pm == -INFINITY ? ps : ps * fast_exp2(pm - to));
+          m = to;
+        }
+        p.sums[((int64_t)U.h * p.num_tokens + U.q0) * G + t] = m + __log2f(all);
+      }
+    }
+    // (the warps that bring tiles and issue products do not wait for a unit's end: of a
+    // cluster they arrive, and wait for the end of the unit before)
+    if (ctas > 1 && (warp < 2 || warp >= kFirstKWarp)) {
+      __syncwarp();
+      if (arrived) cluster_wait();
+      cluster_arrive();
+      arrived = true;
     }
     c0 += U.count;
     loaded += U.count > 0;
     if (U.count > 0) raw0 += COLS ? 1 : U.count;
-    group_sync(ctas);
-    // number what of thread tid's row, from share k & 3 of CTA k / 4's columns
-    const auto part_of = [&](int what, uint32_t k) {
-      const float* at = &B.part[what][k & 3][tid];
-      return ctas > 1 ? ld_cluster_f32(cluster_addr(smem_addr(at), k >> 2)) : *at;
-    };
-    if constexpr (COLS) {
-      const int j = U.key0 + tid;
-      if (rank == 0 && tid < kTile && j < U.L) {
-        float sum = 0.f;
-        for (uint32_t k = 0; k < 4 * ctas; ++k) sum += part_of(0, k);
-        float* w = p.weights + ((int64_t)U.s * p.n_kv + U.h) * p.weights_stride + j;
-        *w = (j < U.c0 ? *w : 0.f) + sum;
-      }
-    } else if (rank == 0 && tid < U.ntok * G) {
-      // the row's log sum over the cluster's pieces of its keys
-      float m = -INFINITY, sum = 0.f;
-      for (uint32_t k = 0; k < 4 * ctas; ++k) {
-        const float pm = part_of(0, k), ps = part_of(1, k);
-        const float to = fmaxf(m, pm);
-        sum = (m == -INFINITY ? sum : sum * fast_exp2(m - to)) +
-              (pm == -INFINITY ? ps : ps * fast_exp2(pm - to));
-        m = to;
-      }
-      p.sums[((int64_t)U.h * p.num_tokens + U.q0) * G + tid] = m + __log2f(sum);
-    }
-    group_sync(ctas);
   }
-  // A unit ends with every product done and so every copy landed, unless a wait was
-  // given up: then the last copies into each stage are waited for (again with a limit).
+  if (arrived) cluster_wait();
+  if (ctas > 1) cluster_sync();  // (the first CTA has read the others' last sums)
+  tc::fence_before_sync();
+  __syncthreads();
+  // Every product is done and so every copy landed, unless a wait was given up: then the
+  // last copies into each stage are waited for (again with a limit).
   if (B.abort_flag && tid == 0) {
     for (uint32_t c = c0 > NB ? c0 - NB : 0; c < c0; ++c)
       mbar_wait(smem_addr(&B.b_full[c % NB]), (c / NB) & 1, p.err, abort_flag);
@@ -641,8 +671,6 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       for (uint32_t c = raw0 > kRaw ? raw0 - kRaw : 0; c < raw0; ++c)
         mbar_wait(smem_addr(&B.raw_full[w][c % kRaw]), (c / kRaw) & 1, p.err, abort_flag);
   }
-  tc::fence_before_sync();
-  __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, TMEM_COLS);
@@ -654,7 +682,7 @@ cudaError_t launch_pass(const ChunkArgs& p, const CUtensorMap& qm, const CUtenso
                         int ctas, cudaStream_t stream) {
   using R = Roles<F8>;
   constexpr size_t used = 1024 + (size_t)(D / 64) * 128 * (kTile + kCols * R::kStages) +
-                          (F8 ? 8 * kRaw * (16 * D + 64) : 0) + sizeof(ChunkShared);
+                          (F8 ? R::kKWarps * kRaw * Raw<D>::kBytes : 0) + sizeof(ChunkShared);
   constexpr size_t smem = std::max<size_t>(used, 120 * 1024);
   static_assert(offsetof(ChunkShared, side) % 16 == 0, "alignment");
   // (one CTA an SM, which has all of TMEM)
@@ -710,8 +738,6 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
   while (pieces < 8 && least * pieces < slots_of_sms && key_tiles >= 4ll * pieces) pieces *= 2;
   const int tiles = (max_q_len + kCols / G - 1) / (kCols / G);
   int ctas = tiles >= 8 ? 2 : 1;
-  if (getenv("PA_PC")) pieces = atoi(getenv("PA_PC"));
-  if (getenv("PA_CC")) ctas = atoi(getenv("PA_CC"));
   for (p.skip = 0; p.skip < most_chunks; p.skip += kListed) {
     long long groups = std::min(row_units, slots_of_sms / pieces);
     cudaError_t e =
