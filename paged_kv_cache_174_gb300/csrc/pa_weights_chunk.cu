@@ -6,17 +6,24 @@
 //
 // A weight needs its row's sum over all keys, so there are two passes over S = Q K^T,
 // neither of which needs V or P in shared memory:
-//  * rows: a tile of 256 / G tokens x G heads stays, key tiles of 64 stream past; each
-//    thread keeps the running max and sum of a row.  The CTAs of a cluster take a piece of
-//    the keys each, for more units.
-//  * columns: a tile of 256 keys stays, query tiles of 64 rows stream past; S^T puts a key
-//    in each TMEM lane, so the sum over rows is a thread's own.  A cluster's CTAs take
-//    query tiles in turn and add their sums up at the end: no atomics, and one order.
-// Both share the code below: the tile that stays is A, two products' 128 lanes of TMEM,
-// copied there once a unit, so that a product reads only the 64 rows of B from shared
-// memory; S has two buffers, each with a group of warps that reads it.
-// 8-bit cache: K codes are converted to bf16 (exact) and the keys' scales multiply
-// the scores.
+//  * rows: a tile of 128 / G tokens x G heads stays, key tiles of 128 stream past; each
+//    thread keeps the running max and sum of a row.
+//  * columns: a tile of 128 keys stays, query tiles of 128 rows stream past; S^T puts a key
+//    in each TMEM lane, so the sum over rows is a thread's own.
+// In both the CTAs of a cluster share a unit's tiles where units are few, and add up at its
+// end: no atomics, and one order.
+// The passes share the code below.  The tile that stays is A, copied to TMEM once a unit, so
+// that a product reads only B from shared memory; S has three buffers, for two groups of
+// eight warps that take the sums.  The warps that bring tiles and issue products run ahead
+// of a unit's end.  8-bit cache: K codes are converted to bf16 (exact) and the keys' scales
+// multiply the scores.
+// The exponentials and their sums bound it: 4096 rows and keys, 32 q / 8 kv heads of 128,
+// take 92 us for the rows and 81 for the columns (the products alone 34 each), and of an
+// 8-bit cache, whose conversion shares the exponentials' pipe, 167 and 87.  Measured too, in
+// the same terms: A in shared memory and two CTAs an SM 82 and 134 (8-bit 214 and 157); a
+// tile of 256 by products of 64 columns, which issue at a third of the rate, 114 and 117; the
+// accumulators read as 16 x 256 bits, for fewer reads of a column's value, 87 and 158;
+// codes converted by shifts and one product 198 instead of 167.
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
@@ -30,9 +37,7 @@
 namespace pa {
 namespace {
 
-constexpr int kLanes = 128;         // lanes of a product: rows of A
-constexpr int kCols = 128;          // columns of a product: rows of B
-constexpr int kTile = kLanes;       // rows of the tile that stays
+constexpr int kTile = 128;          // rows of A and of B: a product's lanes and columns
 constexpr int kSumWarps = 16;       // warps 2-17: for each S buffer two a TMEM lane quarter
 constexpr int kFirstKWarp = 18;
 constexpr int kBuffers = 3;         // of S in TMEM
@@ -61,8 +66,8 @@ struct alignas(16) ChunkShared {
   uint32_t tmem_slot;
   int abort_flag;
   int listed;
-  // rows pass: the keys' scales times the scores'; columns pass: the rows' log sums (read four at a time)
-  alignas(16) float side[kSide][kCols];
+  // rows pass: the keys' scales times the scores'; columns pass: the rows' log sums
+  alignas(16) float side[kSide][kTile];
   // by units in turn: rows pass (max, sum) by sum warps' share; columns pass [0] sums
   float part[2][2][4][kTile];
   int list_seq[kListed];
@@ -100,11 +105,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // S = A B^T: 128 rows of A in TMEM, two values a column, and tile B [half of head_dim][128][64].
 template <int D>
 __device__ __forceinline__ void issue_products(uint32_t d_tmem, uint32_t a_tmem, tc::Desc b) {
-  constexpr uint32_t HALF_B = kCols * 128;
-  constexpr uint32_t IDESC = tc::idesc_bf16_f32(kLanes, kCols, 0, 0);
+  constexpr uint32_t HALF = kTile * 128;
+  constexpr uint32_t IDESC = tc::idesc_bf16_f32(kTile, kTile, 0, 0);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off_b = ((kk >> 2) * HALF_B + (kk & 3) * 32) >> 4;
+    const uint32_t off_b = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
     if (kk == 0)
       tc::mma_bf16_tmem_a_pair<false>(d_tmem, a_tmem, b, off_b, IDESC);
     else
@@ -123,22 +128,21 @@ template <int D, int G, bool F8, bool COLS>
 __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     chunk_kernel(const ChunkArgs p, const __grid_constant__ CUtensorMap qmap,
                  const __grid_constant__ CUtensorMap kmap) {
-  constexpr int TA = kTile / G, TB = kCols / G;  // tokens of a query tile that stays, streams
+  constexpr int TM = kTile / G;  // tokens of a query tile
   constexpr int NH = D / 64;
-  constexpr uint32_t HALF_A = kTile * 128, HALF_B = kCols * 128;
-  constexpr uint32_t TILE_A = NH * HALF_A, TILE = NH * HALF_B;
+  constexpr uint32_t HALF = kTile * 128, TILE = NH * HALF;
   constexpr int NB = Roles<F8>::kStages;
   constexpr int KW = Roles<F8>::kKWarps;
   constexpr int PAGES = Roles<F8>::kPages;  // of a K tile for a warp
   constexpr int RAW = Raw<D>::kBytes;
   constexpr int THREADS = Roles<F8>::kThreads;
-  constexpr uint32_t A_COLS = kBuffers * kCols;
+  constexpr uint32_t A_COLS = kBuffers * kTile;
   constexpr uint32_t TMEM_COLS = 512;       // S, then A
 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* a_s = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* b_s = a_s + TILE_A;
+  unsigned char* b_s = a_s + TILE;
   unsigned char* raw_s = b_s + NB * TILE;  // (8-bit cache) [K warp][kRaw][RAW]
   ChunkShared& B = *reinterpret_cast<ChunkShared*>(raw_s + (F8 ? KW * kRaw * RAW : 0));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         const int a = p.query_start_loc[s], b = p.query_start_loc[s + 1], L = p.seq_lens[s];
         if (b - a >= 2 && a >= 0 && b <= p.num_tokens && L >= b - a && L <= p.max_seq_len &&
             L <= ((long long)p.max_blocks << p.block_shift) * 16)
-          n = COLS ? (L + kTile - 1) / kTile : (b - a + TA - 1) / TA;
+          n = COLS ? (L + kTile - 1) / kTile : (b - a + TM - 1) / TM;
       }
       uint32_t before_n, before_t, all_n, all_t;
       block_scan2(B.scan, n > 0, (uint32_t)n, before_n, before_t, all_n, all_t);
@@ -242,15 +246,15 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       if constexpr (COLS) {
         U.key0 = nth * kTile;
         U.q0 = U.ntok = 0;
-        const int from = max(0, U.key0 - U.c0) / TB, tiles = (U.ql + TB - 1) / TB;
+        const int from = max(0, U.key0 - U.c0) / TM, tiles = (U.ql + TM - 1) / TM;
         U.first = from + (int)rank;
         U.step = (int)ctas;
         U.count = U.first < tiles ? (tiles - U.first + U.step - 1) / U.step : 0;
       } else {
         U.key0 = 0;
-        U.q0 = U.a + nth * TA;
-        U.ntok = min(TA, U.ql - nth * TA);
-        const int tiles = (U.c0 + nth * TA + U.ntok + kCols - 1) / kCols;
+        U.q0 = U.a + nth * TM;
+        U.ntok = min(TM, U.ql - nth * TM);
+        const int tiles = (U.c0 + nth * TM + U.ntok + kTile - 1) / kTile;
         U.first = (int)((long long)rank * tiles / ctas);
         U.step = 1;
         U.count = (int)((long long)(rank + 1) * tiles / ctas) - U.first;
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     }
     const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
     // tokens of query tile i of the request, and how many (columns pass)
-    const auto tokens_of = [&](int i) { return min(TB, U.ql - i * TB); };
+    const auto tokens_of = [&](int i) { return min(TM, U.ql - i * TM); };
 
     if (warp == 0) {
       // ------------------------------------------------ query tiles
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           float4 v = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);  // (no row: weight 0)
           if (i < U.count) {
             const int qt = U.first + i * U.step, n = tokens_of(qt) * G;
-            const float* at = p.sums + ((int64_t)U.h * p.num_tokens + U.a + qt * TB) * G + lane * 4;
+            const float* at = p.sums + ((int64_t)U.h * p.num_tokens + U.a + qt * TM) * G + lane * 4;
             if (lane * 4 < n) v.x = at[0];
             if (lane * 4 + 1 < n) v.y = at[1];
             if (lane * 4 + 2 < n) v.z = at[2];
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         float4 ls = log_sums(0);
         for (int i = 0; i < U.count; ++i) {
           const uint32_t c = c0 + i, st = c % NB;
-          const int q0 = U.a + (U.first + i * U.step) * TB;
+          const int q0 = U.a + (U.first + i * U.step) * TM;
           // Their slot's last tile, kSide earlier, is done with: this warp has waited for a
           // stage that the product NB + 1 tiles back freed, which needed that S buffer's
           // tile before to have been read, by warps that were done with all earlier ones.
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
             mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
             for (int hf = 0; hf < NH; ++hf)
-              tc::tma_load_3d(smem_addr(b_s + st * TILE + hf * HALF_B), &qmap, hf * 64, U.h * G,
+              tc::tma_load_3d(smem_addr(b_s + st * TILE + hf * HALF), &qmap, hf * 64, U.h * G,
                               q0, bar);
           }
           __syncwarp();
@@ -304,10 +308,10 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         const uint32_t bar = smem_addr(&B.a_full);
         if (loaded > 0)  // (the unit before has copied its tile away)
           mbar_wait(smem_addr(&B.a_ready), (loaded - 1) & 1, p.err, abort_flag);
-        mbar_arrive_expect_tx(bar, TILE_A);
+        mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf)
-          tc::tma_load_3d(smem_addr(a_s + hf * HALF_A), &qmap, hf * 64, U.h * G, U.q0, bar);
+          tc::tma_load_3d(smem_addr(a_s + hf * HALF), &qmap, hf * 64, U.h * G, U.q0, bar);
       }
     } else if (warp == 1) {
       // ------------------------------------------------ products
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           if (c >= kBuffers)
             mbar_wait_spin(smem_addr(&B.s_empty[sb]), (c / kBuffers - 1) & 1, p.err, abort_flag);
           tc::fence_after_sync();
-          issue_products<D>(tmem + sb * kCols, tmem + A_COLS,
+          issue_products<D>(tmem + sb * kTile, tmem + A_COLS,
                             tc::Desc{bd.lo + st * (TILE >> 4), bd.hi});
           tc::commit(smem_addr(&B.s_full[sb]));
           tc::commit(smem_addr(&B.b_empty[st]));
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       const int tiles = U.count == 0 ? 0 : COLS ? 1 : U.count;
       // Page k of this warp's of K tile first + i: its place in the pool (-1: none).
       const auto look_up = [&](int i, int k) {
-        const int lp = (first + i) * (kCols / 16) + idx * PAGES + k;
+        const int lp = (first + i) * (kTile / 16) + idx * PAGES + k;
         if (i >= tiles || k >= PAGES || lp * 16 >= U.L) return -1;
         const int b = table[lp >> p.block_shift];
         if (b >= 0 && b < p.num_blocks)
@@ -361,7 +365,8 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           const int here = page;
           page = look_up(i + 1, lane / NH);
           unsigned char* dst = tile_at(i);
-          const uint32_t bar = tile_bar(i), bytes = __popc(__ballot_sync(0xffffffffu, here >= 0)) * 2048;
+          const uint32_t bar = tile_bar(i);
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here >= 0)) * 2048;
           if (lane == 0) {
             if (bytes)
               mbar_arrive_expect_tx(bar, bytes);
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           }
           __syncwarp();
           if (here >= 0)
-            tc::tma_load_3d(smem_addr(dst + (lane % NH) * HALF_A + (idx * PAGES + lane / NH) * 2048),
+            tc::tma_load_3d(smem_addr(dst + (lane % NH) * HALF + (idx * PAGES + lane / NH) * 2048),
                             &kmap, (lane % NH) * 64, U.h, here * 16, bar);
           __syncwarp();
         }
@@ -423,10 +428,11 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
                 reinterpret_cast<const float*>(from + PAGES * 16 * D)[lane] * p.scale_log2;
 #pragma unroll
           for (int k = 0; k < PAGES; ++k) {
-            unsigned char* to = dst + (c16 >> 2) * HALF_A + (idx * PAGES + k) * 2048;
+            unsigned char* to = dst + (c16 >> 2) * HALF + (idx * PAGES + k) * 2048;
 #pragma unroll
             for (int j = 0; j < 16 / RPL; ++j) {
-              const uint4 w = *reinterpret_cast<const uint4*>(from + k * 16 * D + j * 512 + lane * 16);
+              const uint4 w =
+                  *reinterpret_cast<const uint4*>(from + k * 16 * D + j * 512 + lane * 16);
               const uint32_t src[4] = {w.x, w.y, w.z, w.w};
               uint32_t out[8];
 #pragma unroll
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     } else {
       // ------------------------------------------------ sums
       const int quarter = warp & 3, share = (warp - 2) >> 2;
-      const int cols = (share & 1) * (kCols / 2), group = share >> 1;
+      const int cols = (share & 1) * (kTile / 2), group = share >> 1;
       const int r = quarter * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
       if (U.count > 0) {
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint4 v = *reinterpret_cast<const uint4*>(
-                a_s + (share >> 1) * HALF_A + swizzled(r, (share & 1) * 4 + c));
+                a_s + (share >> 1) * HALF + swizzled(r, (share & 1) * 4 + c));
             x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
           }
           tc::tmem_st16(tmem + lane_addr + A_COLS + share * 16, x);
@@ -510,17 +516,17 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         // of this warp's columns lo .. hi - 1 count for a row
         int lo = 0, hi;
         if constexpr (COLS) {
-          const int p0 = U.c0 + tile * TB;  // position of the query tile's first token
+          const int p0 = U.c0 + tile * TM;  // position of the query tile's first token
           lo = (U.key0 + r - p0) * G - cols;
           hi = tokens_of(tile) * G - cols;
         } else {
-          hi = p_row + 1 - tile * kCols - cols;
+          hi = p_row + 1 - tile * kTile - cols;
         }
         const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           uint32_t x[32];
-          tc::tmem_ld32(tmem + lane_addr + sb * kCols + cols + part * 32, x);
+          tc::tmem_ld32(tmem + lane_addr + sb * kTile + cols + part * 32, x);
           tc::tmem_wait_ld();
           if (part == 1) {
             tc::fence_before_sync();
@@ -681,7 +687,7 @@ template <int D, int G, bool F8, bool COLS>
 cudaError_t launch_pass(const ChunkArgs& p, const CUtensorMap& qm, const CUtensorMap& km, int grid,
                         int ctas, cudaStream_t stream) {
   using R = Roles<F8>;
-  constexpr size_t used = 1024 + (size_t)(D / 64) * 128 * (kTile + kCols * R::kStages) +
+  constexpr size_t used = 1024 + (size_t)(D / 64) * 128 * (kTile + kTile * R::kStages) +
                           (F8 ? R::kKWarps * kRaw * Raw<D>::kBytes : 0) + sizeof(ChunkShared);
   constexpr size_t smem = std::max<size_t>(used, 120 * 1024);
   static_assert(offsetof(ChunkShared, side) % 16 == 0, "alignment");
@@ -725,25 +731,28 @@ cudaError_t launch_t(ChunkArgs p, int max_q_len, int sm_count, cudaStream_t stre
                                : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
     if (e != cudaSuccess) return e;
   }
-  const long long slots_of_sms = sm_count;
   // upper bounds of the units: the kernel has the exact count
   const long long row_units = ((long long)p.num_tokens / (kTile / G) + p.num_seqs) * p.n_kv;
   const long long most_chunks = std::min<long long>(p.num_seqs, p.num_tokens / 2);
   const long long key_tiles = ((long long)p.max_seq_len + kTile - 1) / kTile;
   const long long col_units = most_chunks * key_tiles * p.n_kv;
-  // CTAs of a cluster: pieces of a row's keys where query tiles are few, and query tiles of
-  // a key tile in turn
+  // CTAs of a cluster, while they leave SMs idle without: pieces of a row's keys, and of a key
+  // tile's query tiles.  A chunk of 64 after 4096 tokens, 8 kv heads (24 units of rows): 47.8
+  // us with 1 piece, 41.2 with 2, 39.2 with 4, 47.8 with 8.  Where the units fill the SMs a
+  // cluster costs: 4096 rows in 2 pieces 347 us, in one 322; with clusters of 4 for the columns
+  // 408, of 2 322, alone 320.
   const long long least = ((long long)p.num_tokens / (kTile / G) + 1) * p.n_kv;
   int pieces = 1;
-  while (pieces < 8 && least * pieces < slots_of_sms && key_tiles >= 4ll * pieces) pieces *= 2;
-  const int tiles = (max_q_len + kCols / G - 1) / (kCols / G);
-  int ctas = tiles >= 8 ? 2 : 1;
+  while (pieces < 4 && least * pieces * 2 <= sm_count && key_tiles >= 4ll * pieces) pieces *= 2;
+  const int tiles = (max_q_len + kTile / G - 1) / (kTile / G);
+  int ctas = 1;
+  while (ctas < 4 && key_tiles * p.n_kv * ctas * 2 <= sm_count && tiles >= 8 * ctas) ctas *= 2;
   for (p.skip = 0; p.skip < most_chunks; p.skip += kListed) {
-    long long groups = std::min(row_units, slots_of_sms / pieces);
+    long long groups = std::min<long long>(row_units, sm_count / pieces);
     cudaError_t e =
         launch_pass<D, G, F8, false>(p, qm, km, (int)(groups * pieces), pieces, stream);
     if (e != cudaSuccess) return e;
-    groups = std::min(col_units, slots_of_sms / ctas);
+    groups = std::min<long long>(col_units, sm_count / ctas);
     e = launch_pass<D, G, F8, true>(p, qm, km, (int)(groups * ctas), ctas, stream);
     if (e != cudaSuccess) return e;
   }
