@@ -434,13 +434,15 @@ cudaError_t launch_evict(EvictArgs p, int sm_count, cudaStream_t stream) {
   const bool many = units * 2 * parts <= sm_count && more <= kEvictSmemMost;
   const size_t ring = many ? more : few;
   const size_t smem = p.staged && with_keys > ring ? with_keys : ring;
-  cudaError_t e;
-  if (p.head_dim == 128)
-    e = p.fp8 ? launch_r<128, true>(p, parts, many, smem, !in_place, stream)
-              : launch_r<128, false>(p, parts, many, smem, !in_place, stream);
-  else
-    e = p.fp8 ? launch_r<64, true>(p, parts, many, smem, !in_place, stream)
-              : launch_r<64, false>(p, parts, many, smem, !in_place, stream);
+  cudaError_t e = cudaSuccess;
+  if (units > 0 || !in_place) {  // (else only the books)
+    if (p.head_dim == 128)
+      e = p.fp8 ? launch_r<128, true>(p, parts, many, smem, !in_place, stream)
+                : launch_r<128, false>(p, parts, many, smem, !in_place, stream);
+    else
+      e = p.fp8 ? launch_r<64, true>(p, parts, many, smem, !in_place, stream)
+                : launch_r<64, false>(p, parts, many, smem, !in_place, stream);
+  }
   if (e != cudaSuccess || !in_place) return e;
   return launch_early(books_kernel, dim3(1), dim3(kThreads), 0, stream, 1, p);
 }
