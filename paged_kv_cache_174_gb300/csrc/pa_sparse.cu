@@ -8,6 +8,8 @@
 // bound.  A cluster of CTAs takes a (token, kv head); its warps take the list's
 // 16-token pages in turn, and the pieces are joined through shared memory of the
 // cluster, so there is no workspace and no second kernel.
+// 512 pairs of 128 blocks of 16 (32 q / 8 kv heads of 128): 90 us, 88% of the copy rate;
+// 8-bit 61 us, 67%, bound by the conversion of the codes.
 #include <cstdint>
 
 #include "pa_rows.cuh"
@@ -138,6 +140,10 @@ cudaError_t launch_d(const SparseArgs& p, int ctas, cudaStream_t stream) {
 cudaError_t launch_sparse(const SparseArgs& p, int sm_count, cudaStream_t stream) {
   const long long units = (long long)p.num_tokens * p.n_kv;
   const long long pages = (long long)p.num_selected << p.block_shift;
+  // CTAs of a cluster, until every SM has one and while each warp has two pages.  One, two,
+  // four and eight for lists of 128 pages: 512 pairs 91.0* 91.1 97 113 us; 256 pairs, 8-bit, 36.2*
+  // 38.7 41.8 47.4; 128 pairs 28.1 30.1* 33 36; 64 pairs 23.4 19.3 18.2* 22.8; 8 pairs 19.3
+  // 13.8 9.5 7.7* (16 like 8).
   int ctas = 1;
   while (ctas < kRowsMaxCtas && units * ctas < sm_count && pages > 2ll * ctas * kRowsWarps)
     ctas *= 2;

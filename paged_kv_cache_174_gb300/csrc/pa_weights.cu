@@ -9,6 +9,9 @@
 // against 4 d of K and V), and those of a cache too long for it are computed again
 // from K.  One pass over K and V, so their bytes are the bound.  A cluster takes a
 // (request, kv head), each CTA a run of its keys.
+// 64 requests of 128 to 4096 tokens, 32 q / 8 kv heads of 128: 101 us, 82% of the copy rate;
+// 8-bit 84 us, 52% (the conversion of the codes, and the last CTAs of a grid of 2.2 for each
+// place); 8 requests of 16384 to 32767 tokens, 8-bit, 122 us, 52%.
 #include <cstdint>
 
 #include "pa_rows.cuh"
@@ -226,6 +229,11 @@ cudaError_t launch_d(const WeighArgs& p, int ctas, cudaStream_t stream) {
 cudaError_t launch_weigh(const WeighArgs& p, int sm_count, cudaStream_t stream) {
   const long long units = (long long)p.num_seqs * p.n_kv;
   const long long pages = ((long long)p.max_seq_len + 15) / 16;
+  // CTAs of a cluster: until there are two an SM, and so many that a CTA's scores of up to 192
+  // pages stay in shared memory.  One, two, four, eight and 16: 512 pairs of 128 to 4096
+  // tokens 118 101* 112 155 213 us, 8-bit 116 84* 82 93 147; 2048 pairs of 200 to 2000 185*
+  // 218 294 349 700; 128 pairs of 4096 to 8191 159 91.5 76.5* 82 122; 64 pairs of 16384 to
+  // 32767, 8-bit, 788 383 202 146 122*.
   int ctas = 1;
   while (ctas < kRowsMaxCtas && pages > 2ll * ctas * kRowsWarps &&
          (units * ctas < 2ll * sm_count || pages > 192ll * ctas))
