@@ -41,6 +41,9 @@ constexpr int kTile = 128;          // rows of A and of B: a product's lanes and
 constexpr int kSumWarps = 16;       // warps 2-17: for each S buffer two a TMEM lane quarter
 constexpr int kFirstKWarp = 18;
 constexpr int kBuffers = 3;         // of S in TMEM
+// Barriers of their products: each is of one group of sum warps, which so meets every phase
+// (of a buffer's barrier it would meet every other one, and take one parity for another).
+constexpr int kFulls = 2 * kBuffers;
 constexpr int kSide = 12;           // slots of the values that go with a B tile's columns
 constexpr int kListed = 512;        // chunk requests of a launch
 
@@ -61,7 +64,7 @@ struct Raw {  // a warp's codes and scales of a tile
 };
 
 struct alignas(16) ChunkShared {
-  uint64_t a_full, a_ready, b_full[4], b_empty[4], s_full[kBuffers], s_empty[kBuffers];
+  uint64_t a_full, a_ready, b_full[4], b_empty[4], s_full[kFulls], s_empty[kBuffers];
   uint64_t side_full[kSide], raw_full[8][kRaw];
   uint32_t tmem_slot;
   int abort_flag;
@@ -155,10 +158,8 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
       mbar_init(smem_addr(&B.b_full[i]), COLS ? 1 : KW);
       mbar_init(smem_addr(&B.b_empty[i]), 1);
     }
-    for (int i = 0; i < kBuffers; ++i) {
-      mbar_init(smem_addr(&B.s_full[i]), 1);
-      mbar_init(smem_addr(&B.s_empty[i]), kSumWarps / 2);
-    }
+    for (int i = 0; i < kFulls; ++i) mbar_init(smem_addr(&B.s_full[i]), 1);
+    for (int i = 0; i < kBuffers; ++i) mbar_init(smem_addr(&B.s_empty[i]), kSumWarps / 2);
     for (int i = 0; i < kSide; ++i) mbar_init(smem_addr(&B.side_full[i]), COLS ? 1 : KW);
     for (int i = 0; i < 8 * kRaw; ++i) mbar_init(smem_addr(&B.raw_full[i / kRaw][i % kRaw]), 1);
     B.abort_flag = 0;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
           tc::fence_after_sync();
           issue_products<D>(tmem + sb * kTile, tmem + A_COLS,
                             tc::Desc{bd.lo + st * (TILE >> 4), bd.hi});
-          tc::commit(smem_addr(&B.s_full[sb]));
+          tc::commit(smem_addr(&B.s_full[c % kFulls]));
           tc::commit(smem_addr(&B.b_empty[st]));
         }
       }
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         const uint32_t c = c0 + i, sb = c % kBuffers;
         const int tile = U.first + i * U.step;
         const float* side = B.side[c % kSide] + cols;
-        mbar_wait(smem_addr(&B.s_full[sb]), (c / kBuffers) & 1, p.err, abort_flag);
+        mbar_wait(smem_addr(&B.s_full[c % kFulls]), (c / kFulls) & 1, p.err, abort_flag);
         if (COLS || F8)
           mbar_wait(smem_addr(&B.side_full[c % kSide]), (c / kSide) & 1, p.err, abort_flag);
         tc::fence_after_sync();
