@@ -53,8 +53,8 @@ int check_heads(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
 
 // Units times the most CTAs that one gets has to fit a grid.
 int check_units(int64_t units) {
-  if (units > INT32_MAX / 8)
-    return api_fail(PA_ERR_UNSUPPORTED, "%lld (row, kv head) pairs (at most 2^28 - 1)",
+  if (units > INT32_MAX / 16)
+    return api_fail(PA_ERR_UNSUPPORTED, "%lld (row, kv head) pairs (at most 2^27 - 1)",
                     (long long)units);
   return PA_OK;
 }

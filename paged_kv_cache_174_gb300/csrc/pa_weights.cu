@@ -231,11 +231,15 @@ cudaError_t launch_weigh(const WeighArgs& p, int sm_count, cudaStream_t stream) 
   const long long pages = ((long long)p.max_seq_len + 15) / 16;
   // CTAs of a cluster: until there are two an SM, and so many that a CTA's scores of up to 192
   // pages stay in shared memory.  One, two, four, eight and 16: 512 pairs of 128 to 4096
-  // tokens 118 101* 112 155 213 us, 8-bit 116 84* 82 93 147; 2048 pairs of 200 to 2000 185*
-  // 218 294 349 700; 128 pairs of 4096 to 8191 159 91.5 76.5* 82 122; 64 pairs of 16384 to
-  // 32767, 8-bit, 788 383 202 146 122*.
+  // tokens 118 101* 112 155 212 us, 8-bit 116 84* 82 93 147; of 8192 to 16384 818 681 542 526*
+  // 680, 8-bit 739 592 465 374* 400; 2048 pairs of 200 to 2000 185* 218 294 349 699, of 4096
+  // to 8191 1268 1042 1003* 1150 1780; 128 pairs of 4096 to 8191 159 91.5 76.5* 82 122; 64
+  // pairs of 16384 to 32767, 8-bit, 788 383 202 146 122*.  Many pairs get no more than eight
+  // or four for scores that do not stay: max_seq_len may be no more than a bound, and what is
+  // computed again is half a page's bytes at most.
+  const int most = units >= 8ll * sm_count ? 4 : units >= 2ll * sm_count ? 8 : kRowsMaxCtas;
   int ctas = 1;
-  while (ctas < kRowsMaxCtas && pages > 2ll * ctas * kRowsWarps &&
+  while (ctas < most && pages > 2ll * ctas * kRowsWarps &&
          (units * ctas < 2ll * sm_count || pages > 192ll * ctas))
     ctas *= 2;
   return p.head_dim == 128 ? launch_d<128>(p, ctas, stream) : launch_d<64>(p, ctas, stream);

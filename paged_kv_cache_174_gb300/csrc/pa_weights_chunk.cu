@@ -17,13 +17,13 @@
 // eight warps that take the sums.  The warps that bring tiles and issue products run ahead
 // of a unit's end.  8-bit cache: K codes are converted to bf16 (exact) and the keys' scales
 // multiply the scores.
-// The exponentials and their sums bound it: 4096 rows and keys, 32 q / 8 kv heads of 128,
-// take 92 us for the rows and 81 for the columns (the products alone 34 each), and of an
-// 8-bit cache, whose conversion shares the exponentials' pipe, 167 and 87.  Measured too, in
-// the same terms: A in shared memory and two CTAs an SM 82 and 134 (8-bit 214 and 157); a
-// tile of 256 by products of 64 columns, which issue at a third of the rate, 114 and 117; the
-// accumulators read as 16 x 256 bits, for fewer reads of a column's value, 87 and 158;
-// codes converted by shifts and one product 198 instead of 167.
+// The waits of the warps that sum, for TMEM and for one another, bound it, and in 8-bit
+// caches the conversion, which shares the exponentials' pipe: 4096 rows and keys, 32 q / 8 kv
+// heads of 128, take 92 us for the rows and 80 for the columns (the products alone 34 each),
+// 8-bit 166 and 84.  Measured in the same terms: A in shared memory and two CTAs an SM 82 and
+// 134 (8-bit 214 and 157); a tile of 256 by products of 64 columns, which took about three
+// times as long a score, 114 and 117; accumulators read as 16 x 256 bits, for fewer reads of
+// a column's value, 87 and 158; codes converted by shifts and one product 198 in place of 167.
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>

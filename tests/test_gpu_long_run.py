@@ -335,3 +335,46 @@ def test_requests_of_nothing():
         ops.check_device_errors()
         for name in STATE:
             assert same(getattr(loop, name), before[name]), name
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_pages_behind_32_bits_of_bytes(fp8):
+    """The same requests at the far end of a cache of more than 2^32 bytes (8-bit codes: 2^31):
+    the same bits."""
+    n_kv, d, blocks = 8, 128, 140_000
+    c = R.Cache([(300, 1), (40, 70), (1000, 1), (0, 33)], n_kv, d, BS, fp8, seed=4)
+    tables, lens, starts = c.step()
+    q, _ = c.queries(4 * n_kv, 4)
+    far = blocks - c.blocks
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def suffixed(name):
+        return getattr(ops, name + "_fp8" if fp8 else name)
+
+    def everything(k, v, first, pool):
+        tables_ = torch.where(tables >= 0, tables + first, tables)
+        codes, scales = ops.alloc_bounds(pool, n_kv, d)
+        suffixed("summarize_blocks")(k, tables_, lens, None, codes, scales)
+        chosen = ops.select_blocks(q, codes, scales, tables_, lens, starts, num_selected=6,
+                                   block_size=BS, max_seq_len=1001)
+        out = suffixed("paged_attention_blocks")(q, k, v, tables_, lens, starts, 0.1, chosen)
+        w = torch.zeros(4, n_kv, 1001, device="cuda")
+        whole = suffixed("paged_attention_weights")(q, k, v, tables_, lens, starts, 0.1, w,
+                                                    max_q_len=70, max_seq_len=1001)
+        free, count = torch.zeros(pool, **i32), torch.zeros(1, **i32)
+        left = suffixed("evict_tokens")(k, v, w, tables_, lens, lens // 2, free, count,
+                                        num_sinks=2, num_recent=3, max_seq_len=1001,
+                                        seq_lens_out=torch.empty_like(lens))
+        n = int(count)
+        return [codes[first:first + c.blocks], scales[first:first + c.blocks], chosen, out, w,
+                whole, left, count, free[:n] - first, k[first:first + c.blocks],
+                v[first:first + c.blocks]]
+
+    big = [torch.empty(blocks, *x.shape[1:], dtype=x.dtype, device="cuda") for x in (c.k, c.v)]
+    for x, y in zip(big, (c.k, c.v)):
+        x[far:] = y
+    near = everything(c.k, c.v, 0, c.blocks)
+    for got, want in zip(everything(*big, far, blocks), near):
+        assert same(got, want)
+    ops.check_device_errors()
+    assert big[0].numel() * big[0].element_size() > (2 ** 31 if fp8 else 2 ** 32)
