@@ -378,3 +378,47 @@ def test_pages_behind_32_bits_of_bytes(fp8):
         assert same(got, want)
     ops.check_device_errors()
     assert big[0].numel() * big[0].element_size() > (2 ** 31 if fp8 else 2 ** 32)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_bounds_far_above_the_lengths(fp8):
+    """Maxima as a captured step has them, far above any length: the same choice and the
+    same tokens kept, and weights to their tolerance."""
+    n_kv, d = 2, 64
+    c = R.Cache([(300, 1), (15, 1), (1000, 1), (40, 70), (0, 33), (7, 0)], n_kv, d, BS, fp8, seed=6)
+    width = 8192
+    wide = np.full((len(c.lens), width), -1, np.int32)
+    wide[:, :c.tables.shape[1]] = c.tables
+    c.tables = wide
+    tables, lens, starts = c.step()
+    q, q64 = c.queries(4 * n_kv, 6)
+    codes, scales = ops.alloc_bounds(c.blocks, n_kv, d)
+    name = (lambda n: n + "_fp8") if fp8 else (lambda n: n)
+    getattr(ops, name("summarize_blocks"))(c.k, tables, lens, None, codes, scales)
+    chosen = [ops.select_blocks(q, codes, scales, tables, lens, starts, num_selected=6,
+                                block_size=BS, max_seq_len=most, out=torch.full(
+                                    (c.tokens, n_kv, 6), -7, dtype=torch.int32, device="cuda"))
+              for most in (1001, width * BS, 49152 * BS)]
+    assert same(chosen[0], chosen[1]) and same(chosen[0], chosen[2])
+    w = torch.zeros(len(c.lens), n_kv, width * BS, device="cuda")
+    out = getattr(ops, name("paged_attention_weights"))(
+        q, c.k, c.v, tables, lens, starts, 0.1, w, max_q_len=2048, max_seq_len=width * BS)
+    ops.check_device_errors()
+    o64, A, E, w64, tol = R.weights_attention(q64, c.K, c.V, c.tables, c.lens, c.starts, 0.1, BS,
+                                              np.zeros((len(c.lens), n_kv, 1001)))
+    got = w.double().cpu().numpy()
+    assert (np.abs(got[..., :1001] - w64) <= tol + 1e-30).all() and not got[..., 1001:].any()
+    S.assert_window_close(out.cpu().double().numpy(), (o64, A, E / (4 * d * R.EPS)), fp8)
+    budgets, i32 = lens // 2, dict(dtype=torch.int32, device="cuda")
+    kept = []
+    for most in (1001, width * BS):
+        k, v, weights = c.k.clone(), c.v.clone(), w.clone()
+        free, count = torch.zeros(c.blocks, **i32), torch.zeros(1, **i32)
+        left = getattr(ops, name("evict_tokens"))(
+            k, v, weights, tables, lens, budgets, free, count, max_seq_len=most,
+            seq_lens_out=torch.empty_like(lens))
+        kept.append((k, v, weights, left, free, count))
+    ops.check_device_errors()
+    assert kept[0][3].tolist() == budgets.tolist()
+    for a, b in zip(*kept):
+        assert same(a, b)
