@@ -8,8 +8,8 @@
 // bound.  A cluster of CTAs takes a (token, kv head); its warps take the list's
 // 16-token pages in turn, and the pieces are joined through shared memory of the
 // cluster, so there is no workspace and no second kernel.
-// 512 pairs of 128 blocks of 16 (32 q / 8 kv heads of 128): 90 us, 88% of the copy rate;
-// 8-bit 61 us, 67%, bound by the conversion of the codes.
+// 512 pairs of 128 blocks of 16 (32 q / 8 kv heads of 128): 84 us, 95% of the copy rate;
+// 8-bit 59 us, 70%, bound by the conversion of the codes.
 #include <cstdint>
 
 #include "pa_rows.cuh"
@@ -18,11 +18,13 @@
 namespace pa {
 namespace {
 
-// CTAs of an SM, and the bytes of a warp's ring that leaves.
+// CTAs of an SM, and the bytes of a warp's ring that leaves: three pages in flight a warp.  512
+// pairs with rings of 16, 24 and 32 KB (3, 2 and 1 CTAs) 91 84* 98 us; 256 pairs, 8-bit, with
+// 8, 12 and 16 KB (5, 4 and 3) 36.4 31.9* 38.8.
 template <int D, bool F8>
-constexpr int kCtas = D == 128 && !F8 ? 3 : 5;
+constexpr int kCtas = D == 128 && !F8 ? 2 : 4;
 template <int D, bool F8>
-constexpr int kRing = (D == 128 && !F8 ? 16 : 8) * 1024;
+constexpr int kRing = (D == 128 && !F8 ? 24 : 12) * 1024;
 
 template <int D, int G, bool F8>
 __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
@@ -141,9 +143,9 @@ cudaError_t launch_sparse(const SparseArgs& p, int sm_count, cudaStream_t stream
   const long long units = (long long)p.num_tokens * p.n_kv;
   const long long pages = (long long)p.num_selected << p.block_shift;
   // CTAs of a cluster, until every SM has one and while each warp has two pages.  One, two,
-  // four and eight for lists of 128 pages: 512 pairs 91.0* 91.1 97 113 us; 256 pairs, 8-bit, 36.2*
-  // 38.7 41.8 47.4; 128 pairs 28.1 30.1* 33 36; 64 pairs 23.4 19.3 18.2* 22.8; 8 pairs 19.3
-  // 13.8 9.5 7.7* (16 like 8).
+  // four, eight and 16 for lists of 128 pages: 512 pairs 82* 93 101 132 260 us; 256 pairs,
+  // 8-bit, 31.8* 32.1 39 54 94; 128 pairs 26.6 27.6* 31 40 71; 64 pairs 21.4 17.8 16.9* 21.6
+  // 38; 8 pairs 19.0 13.4 9.3 7.3 7.3*.
   int ctas = 1;
   while (ctas < kRowsMaxCtas && units * ctas < sm_count && pages > 2ll * ctas * kRowsWarps)
     ctas *= 2;
