@@ -106,6 +106,18 @@ def test_many_query_tiles(fp8):
     check(c, run(c, 32, 0.125), "tiles")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("requests,n_kv,G,d", [
+    ([(0, 1500)], 1, 8, 64),              # clusters of four take a key tile's query tiles
+    ([(1100, 1000)], 2, 2, 128),          # of four, a row's keys, and a key tile's query tiles
+    ([(1100 + s, 2) for s in range(60)], 2, 4, 64),   # ... in several rounds
+    ([(1100 + 9 * s, 2 + s % 3) for s in range(45)] + [(30, 1)], 4, 1, 128),
+])
+def test_clusters(requests, n_kv, G, d, fp8):
+    c = R.Cache(requests, n_kv, d, 16, fp8, seed=8)
+    check(c, run(c, n_kv * G, 1 / d ** 0.5), "clusters")
+
+
 def test_more_chunk_requests_than_a_launch_lists():
     c = R.Cache([(s % 5, 2 + s % 2) for s in range(1100)], 1, 64, 16, False, seed=5)
     check(c, run(c, 1, 0.125), "many requests")
