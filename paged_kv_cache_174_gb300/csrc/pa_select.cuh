@@ -194,7 +194,8 @@ __device__ Threshold select_threshold(SelectShared& B, uint32_t* hist, int n, ui
 }
 
 // The K largest over a warp's registers: k[j] of lane i is key 32 j + i, those from n on are
-// not there.  Sets bit j of the result for the lane's chosen ones.  0 < K <= n.
+// not there.  Sets bit j of the result for the lane's chosen ones: K in all, never more (of
+// more keys that are always chosen the first K).  0 < K <= n.
 template <int NJ>
 __device__ __forceinline__ uint32_t select_in_warp(const uint32_t (&k)[NJ], int n, int K) {
   const int lane = threadIdx.x & 31;
@@ -206,8 +207,24 @@ __device__ __forceinline__ uint32_t select_in_warp(const uint32_t (&k)[NJ], int 
     if (there && k[j] == kAlways) chosen |= 1u << j, ++fixed;
     if (there && k[j] != kAlways) all &= k[j], any |= k[j];
   }
-  K -= __reduce_add_sync(kAlways, fixed);
-  if (K <= 0) return chosen;
+  // of the keys that are T the first `left`
+  const auto take_first = [&](uint32_t T, int left) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const bool tie = 32 * j + lane < n && k[j] == T;
+      const uint32_t ball = __ballot_sync(kAlways, tie);
+      if (tie && __popc(ball & ((1u << lane) - 1u)) < left) chosen |= 1u << j;
+      left -= __popc(ball);
+    }
+  };
+  fixed = __reduce_add_sync(kAlways, fixed);
+  if (fixed > K) {
+    chosen = 0;
+    take_first(kAlways, K);
+    return chosen;
+  }
+  K -= fixed;
+  if (K == 0) return chosen;
   all = __reduce_and_sync(kAlways, all);
   any = __reduce_or_sync(kAlways, any);
   // the bits that all keys share, then bit by bit: the largest T with at least K keys >= T
@@ -232,14 +249,8 @@ __device__ __forceinline__ uint32_t select_in_warp(const uint32_t (&k)[NJ], int 
     if (there && (k[j] > T || (exact && k[j] == T))) chosen |= 1u << j, ++above;
   }
   if (exact) return chosen;
-  int left = K - __reduce_add_sync(kAlways, above);
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const bool tie = 32 * j + lane < n && k[j] == T && T != kAlways;
-    const uint32_t ball = __ballot_sync(kAlways, tie);
-    if (tie && __popc(ball & ((1u << lane) - 1u)) < left) chosen |= 1u << j;
-    left -= __popc(ball);
-  }
+  // (there are keys below kAlways, as K of them are left to choose, so T is one of them)
+  take_first(T, K - __reduce_add_sync(kAlways, above));
   return chosen;
 }
 
