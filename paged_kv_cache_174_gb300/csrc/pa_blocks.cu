@@ -11,9 +11,9 @@
 // bounds the product of q and any key of the block (up to the rounding of q), and a
 // kv head's score is the largest of its group's.  The term of a channel is
 // x+ max + x- min, so the sum is an integer product of [q+, q-] with [max, min] of
-// length 2 d: at most 2^22 in size, exact in fp32 together with the powers of two.
-// So the choice is the same for any order of the sums, and ties are real ties (the
-// lowest index wins).
+// length 2 d: below 2^21 in size, exact for any order of the sums.  Scores compare by
+// that integer and the two exponents (the product of the three leaves fp32's range for
+// large or small q and keys), so ties are real ties (the lowest index wins).
 #include <cstdint>
 
 #include "pa_common.cuh"
@@ -380,6 +380,26 @@ __device__ __forceinline__ void mma_s8_16832(int (&c)[4], uint32_t a0, uint32_t 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A head's sum is held as c 2^(e - 16), e its power of two's exponent: |c| < 2^21 and e
+// between -126 and 122 make it at most 2^127 and, where it is no normal number, a multiple of
+// 2^-142, so exact.
+constexpr float kHeadUnit = 1.f / 65536.f;
+
+// v u as an unsigned number in the order of the scores: v a head's sum, u >= 0 a power of two
+// or 0 (of another number the first 22 bits of the product count).  Zero is 2^31, and the rest
+// lie above and below it by 10 bits of exponent and 21 of fraction, which hold all of c's.
+// (The exponent's field is between 146 and 670, so neither 0 nor kAlways is a score's.)
+__device__ __forceinline__ uint32_t score_key(float v, float u) {
+  const uint32_t b = __float_as_uint(u);
+  const bool low = fabsf(v) < 0x1p-64f;  // (to a normal number, whatever the fraction below)
+  const float m =
+      v * (low ? 0x1p64f : 1.f) * __uint_as_float((b & 0x7fffffu) | 127u << 23);
+  const uint32_t size = ((__float_as_uint(m) & 0x7fffffffu) >> 2) +
+                        ((b >> 23) + (low ? 160u - 64u : 160u) << 21);
+  if (v == 0.f || b >> 23 == 0) return 0x80000000u;
+  return v > 0.f ? 0x80000000u + size : 0x80000000u - size;
+}
+
 template <int NJ>
 __device__ __forceinline__ void choose_in_warp(const uint32_t* keys, int n, int K, int32_t* out) {
   const int lane = threadIdx.x & 31;
@@ -446,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       *reinterpret_cast<uint32_t*>(&codes[i][lane * 4]) = up;
       *reinterpret_cast<uint32_t*>(&codes[i][D + lane * 4]) = down;
     }
-    if (lane == 0) unit_q[i] = power_of_two(e);
+    if (lane == 0) unit_q[i] = power_of_two(e) * kHeadUnit;
   }
   __syncthreads();
   const int4 f = found;
@@ -505,17 +525,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     __syncwarp();  // (one CTA: the keys take the place of the table entries)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float score = -INFINITY;
-      if (2 * l < p.group) score = (float)c[2 * r] * uq0 * ub[r];
-      if (2 * l + 1 < p.group) score = fmaxf(score, (float)c[2 * r + 1] * uq1 * ub[r]);
-      score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 1));
-      score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 2));
+      float most = -INFINITY;
+      if (2 * l < p.group) most = (float)c[2 * r] * uq0;
+      if (2 * l + 1 < p.group) most = fmaxf(most, (float)c[2 * r + 1] * uq1);
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const int mine = i0 + g + 8 * r;
       if (mine < n && l == 0) {
         const int col = first + mine;
         const bool forced = col < p.num_sinks || col >= visible - p.num_recent;
         // (a scale below 0 is that of a table entry that names no block: chosen last)
-        const uint32_t key = forced ? kAlways : ub[r] >= 0.f ? ordered_key(score) : 0u;
+        const uint32_t key = forced ? kAlways : ub[r] >= 0.f ? score_key(most, ub[r]) : 0u;
         if (ctas > 1)
           st_cluster_u32(cluster_addr(smem_addr(keys + col), 0), key);
         else

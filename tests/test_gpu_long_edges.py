@@ -61,3 +61,29 @@ def test_scores_of_no_number_stay_in_their_row(lens, scores):
         assert (guard == -9).all()
         assert (np.diff(got, axis=-1) > 0).all() and (got >= 0).all()
         assert (got[..., -1] < -(-np.array(lens)[:, None] // 16)).all()
+
+
+@pytest.mark.parametrize("n_kv,G,d", [(2, 8, 128), (1, 1, 64), (4, 2, 128)])
+@pytest.mark.parametrize("lens", [[640, 300, 4096], [16000, 640, 90], [40000, 17000, 300]])
+def test_scores_outside_fp32_keep_their_order(lens, n_kv, G, d):
+    """Queries and keys of any finite size: the integer sums and the powers of two decide,
+    whether or not their product is an fp32 number."""
+    b = Bounds(lens, n_kv, d, seed=G)
+    rng = np.random.default_rng(7)
+    cases = [(1e38, 2.0 ** rng.integers(-3, 4, b.scales.shape)),     # past the largest
+             (3e38, 2.0 ** rng.integers(100, 123, b.scales.shape)),
+             (1e-37, 2.0 ** rng.integers(-126, -100, b.scales.shape)),  # below the smallest
+             (1e-39, 2.0 ** rng.integers(-126, 123, b.scales.shape)),
+             (1.0, np.where(rng.random(b.scales.shape) < 0.5, 0.0, 2.0 ** -126)),
+             (2e38, np.where(rng.random(b.scales.shape) < 0.9, 0.0, 64.0))]
+    g = torch.Generator().manual_seed(1)
+    for size, scales in cases:
+        q = (torch.rand(len(lens), n_kv * G, d, generator=g) * 2 - 1) * size
+        q[0, ::2] *= 2.0 ** -20  # (heads of other sizes in a group)
+        q = q.bfloat16().cuda()
+        b.scales = torch.from_numpy(scales).float().cuda()
+        got, guard = b.choose(q, 17, 1, 2)
+        want = R.choose(q.cpu().double().numpy(), b.codes.cpu().double().numpy(), scales,
+                        b.tables, b.lens, b.starts, b.block, 17, 1, 2, np.zeros_like(got))
+        assert np.array_equal(got, want), size
+        assert (guard == -9).all()
