@@ -661,7 +661,8 @@ int pa_paged_attention_weights_fp8(const pa_bf16 *q, const uint8_t *k_cache,
  *   free_blocks   [num_blocks], free_count [1]: as pa_build_step takes them;
  *                 the blocks of the tables' columns from ceil(budget /
  *                 block_size) on are pushed in the order of requests and
- *                 columns.  free_count_out [1] may be free_count.
+ *                 columns, entries that name no block passed over (and
+ *                 flagged).  free_count_out [1] may be free_count.
  *   position_offsets  [num_seqs] or NULL: the tokens that went are added, so
  *                 that pa_build_step gives later tokens their true positions
  * A length or budget out of range is flagged and its request left alone; a

@@ -104,28 +104,35 @@ __device__ void keep_books(const EvictArgs& p, SelectShared& B) {
       }
       return lo;
     };
-    for (uint32_t k0 = tid; k0 < all; k0 += 4 * kThreads) {
+    for (uint32_t k0 = 0; k0 < all; k0 += 4 * kThreads) {
       int id[4];  // (several loads in flight)
+      bool bad = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t k = k0 + i * kThreads;
+        const uint32_t k = k0 + i * kThreads + tid;
         id[i] = -1;
         if (k < all) {
           const int r = owner(k);
           id[i] = p.block_tables[(int64_t)(s0 + r) * p.max_blocks + first_s[r] + (k - before_s[r])];
+          bad |= id[i] < 0 || id[i] >= p.num_blocks;
         }
       }
+      // (an entry that names no block is not pushed, and the others move together)
+      const bool some_bad = __syncthreads_or(bad);
+      if (bad) flag_error(p.err, DEVERR_BOUNDS);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t k = k0 + i * kThreads;
         if (k >= all) continue;
-        const long long at = (long long)raw + total + k;
-        if (id[i] < 0 || id[i] >= p.num_blocks || !ok || at >= p.num_blocks)
-          flag_error(p.err, DEVERR_BOUNDS);
-        if (ok && at < p.num_blocks) p.free_blocks[at] = id[i];
+        const bool push = id[i] >= 0 && id[i] < p.num_blocks;
+        uint32_t nth = tid, unused3, pushed = min(all - k, (uint32_t)kThreads), unused4;
+        if (some_bad) block_scan2(B, push, 0u, nth, unused3, pushed, unused4);
+        const long long at = (long long)raw + total + nth;
+        if (push && (!ok || at >= p.num_blocks)) flag_error(p.err, DEVERR_BOUNDS);
+        if (push && ok && at < p.num_blocks) p.free_blocks[at] = id[i];
+        total += pushed;
       }
     }
-    total += all;
     __syncthreads();
   }
   if (tid == 0) {

@@ -87,3 +87,36 @@ def test_scores_outside_fp32_keep_their_order(lens, n_kv, G, d):
                         b.tables, b.lens, b.starts, b.block, 17, 1, 2, np.zeros_like(got))
         assert np.array_equal(got, want), size
         assert (guard == -9).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_entries_that_name_no_block_are_not_handed_out(in_place):
+    """Evicted from a table with bad entries: flagged, the blocks of the others returned in
+    order, and the next step gets blocks without a flag."""
+    requests, n, budget, pushed = 300, 200, 40, 2
+    c = R.Cache([(n, 0)] * requests, 1, 64, 16, False, seed=1)
+    rng = np.random.default_rng(1)
+    for s, col in zip(rng.integers(0, requests, 40), rng.integers(3, 13, 40)):
+        c.tables[s, col] = rng.choice([-1, c.blocks, 2 ** 31 - 1, -2 ** 31])
+    c.tables[7, 3:13] = -1
+    entries = c.tables[:, 3:13].ravel()
+    good = entries[(entries >= 0) & (entries < c.blocks)]
+    assert len(good) < entries.size - 20 and entries.size > 2048
+    i32 = dict(dtype=torch.int32, device="cuda")
+    tables, lens, _ = c.step()
+    free, count = torch.full((c.blocks,), -5, **i32), torch.tensor([pushed], **i32)
+    free[:pushed] = torch.from_numpy(c.spare[:pushed]).int()
+    out = None if in_place else torch.empty_like(lens)
+    w = torch.rand(requests, 1, n, device="cuda")
+    left = ops.evict_tokens(c.k, c.v, w, tables, lens, torch.full((requests,), budget, **i32), free,
+                            count, num_sinks=budget // 2, num_recent=budget // 2, max_seq_len=n,
+                            seq_lens_out=out)
+    with pytest.raises(ops.PagedAttnError, match="out of range"):
+        ops.check_device_errors()
+    assert left.tolist() == [budget] * requests and count.tolist() == [pushed + len(good)]
+    want = np.full(c.blocks, -5)
+    want[:pushed], want[pushed:pushed + len(good)] = c.spare[:pushed], good
+    assert np.array_equal(free.cpu().numpy(), want)
+    ops.build_step(left, torch.full((requests,), 16, **i32), tables, free, count, block_size=16,
+                   num_tokens=16 * requests)
+    ops.check_device_errors()
