@@ -665,8 +665,9 @@ int pa_paged_attention_weights_fp8(const pa_bf16 *q, const uint8_t *k_cache,
  *                 flagged).  free_count_out [1] may be free_count.
  *   position_offsets  [num_seqs] or NULL: the tokens that went are added, so
  *                 that pa_build_step gives later tokens their true positions
- * A length or budget out of range is flagged and its request left alone; a
- * table entry that names no block is flagged and the rows behind it stay.
+ * A length or budget out of range is flagged and its request left alone.  A
+ * table entry that names no block is flagged: a row that would move from or to
+ * it does not, and the row and weight in its place stay as they are.
  */
 int pa_evict_tokens(pa_bf16 *k_cache, pa_bf16 *v_cache, float *weights, int32_t weights_len,
                     int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs p) {
       const int i = v * kThreads + tid;
       if (i >= rows) continue;
       if (scales && B.to[i] >= 0) x[v] = *scale_at(B.from[i]);
-      if (weights) y[v] = __float_as_uint(w[B.token[i]]);
+      if (weights && B.to[i] >= 0) y[v] = __float_as_uint(w[B.token[i]]);
     }
     const int tiles = (rows + TILE - 1) / TILE;
     // A tile's rows are read before any of them is written, and rows read for later tiles lie
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictArgs p) {
       const int i = v * kThreads + tid;
       if (i >= rows) continue;
       if (scales && B.to[i] >= 0) *scale_at(B.to[i]) = x[v];
-      if (weights) w[base + i] = __uint_as_float(y[v]);
+      if (weights && B.to[i] >= 0) w[base + i] = __uint_as_float(y[v]);
     }
   }
   if (bad) flag_error(p.err, DEVERR_BOUNDS);

@@ -120,3 +120,39 @@ def test_entries_that_name_no_block_are_not_handed_out(in_place):
     ops.build_step(left, torch.full((requests,), 16, **i32), tables, free, count, block_size=16,
                    num_tokens=16 * requests)
     ops.check_device_errors()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_row_that_stays_keeps_its_weight(fp8):
+    """Rows from or to an entry that names no block do not move, and neither do their weights;
+    all others do."""
+    c = R.Cache([(300, 0), (90, 0), (2000, 0)], 2, 64, 16, fp8, seed=2)
+    tables = c.tables.copy()
+    tables[0, 3], tables[0, 9], tables[1, 1], tables[2, 90] = c.blocks, -1, c.blocks + 7, -2
+    w = torch.rand(3, 2, 2003, generator=torch.Generator().manual_seed(2))
+    budgets, sinks, recent = [150, 60, 1800], 3, 20
+    want_rows, want_w = c.parts(), w.numpy().copy()
+    for s, (n, B) in enumerate(zip(c.lens, budgets)):
+        bad = (tables[s] < 0) | (tables[s] >= c.blocks)
+        slot = c.tables[s][np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16
+        for h in range(2):
+            middle = sinks + np.argsort(-w[s, h, sinks:n - recent].numpy(), kind="stable")
+            keep = np.sort(np.concatenate([np.arange(sinks), middle[:B - sinks - recent],
+                                           np.arange(n - recent, n)]))
+            to = np.arange(B)
+            move = ~bad[keep // 16] & ~bad[to // 16]
+            to, keep = to[move], keep[move]
+            for x, y in zip(want_rows, c.parts()):
+                x[slot[to], h] = y[slot[keep], h]
+            want_w[s, h, to] = w[s, h, keep].numpy()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    wd = w.cuda()
+    call = ops.evict_tokens_fp8 if fp8 else ops.evict_tokens
+    call(c.k, c.v, wd, torch.from_numpy(tables).cuda(), c.step()[1], torch.tensor(budgets, **i32),
+         torch.zeros(c.blocks, **i32), torch.zeros(1, **i32), num_sinks=sinks, num_recent=recent,
+         max_seq_len=2000)
+    with pytest.raises(ops.PagedAttnError, match="out of range"):
+        ops.check_device_errors()
+    assert np.array_equal(wd.cpu().numpy(), want_w)
+    for got, want in zip(c.parts(), want_rows):
+        assert np.array_equal(got, want)
