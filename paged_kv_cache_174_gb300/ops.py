@@ -1007,6 +1007,10 @@ def alloc_bounds(num_blocks: int, num_kv_heads: int, head_dim: int, device=None)
 
 def _summarize(fp8, k_cache, block_tables, seq_lens, query_start_loc, bounds, bound_scales,
                num_tokens, stream):
+    if num_tokens is None:
+        if query_start_loc is not None:  # (0 rows would leave every bound as it was)
+            raise ValueError("num_tokens (the rows of q) is needed with query_start_loc")
+        num_tokens = 0
     if stream is None:
         r = (_binding or _load_binding()).summarize(fp8, k_cache, block_tables, seq_lens,
                                                     query_start_loc, bounds, bound_scales,
@@ -1038,14 +1042,16 @@ def _summarize(fp8, k_cache, block_tables, seq_lens, query_start_loc, bounds, bo
 
 def summarize_blocks(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
                      query_start_loc: Optional[torch.Tensor], bounds: torch.Tensor,
-                     bound_scales: torch.Tensor, *, num_tokens: int = 0, stream=None) -> None:
+                     bound_scales: torch.Tensor, *, num_tokens: Optional[int] = None,
+                     stream=None) -> None:
     """Bounds of the keys of the blocks that the step's new tokens are in, as
     8-bit codes with a power-of-two scale for each block and kv head (see
     pa_summarize_blocks).
 
     ``bounds`` int8 [num_blocks, n_kv, 2, d] and ``bound_scales`` float32
     [num_blocks, n_kv] (alloc_bounds) are updated; ``num_tokens`` is the step's
-    (rows of q).  ``query_start_loc`` None: every block of every request.
+    (rows of q), and has to be given with ``query_start_loc``.
+    ``query_start_loc`` None: every block of every request.
     """
     return _summarize(False, k_cache, block_tables, seq_lens, query_start_loc, bounds,
                       bound_scales, num_tokens, stream)
@@ -1054,7 +1060,7 @@ def summarize_blocks(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens
 def summarize_blocks_fp8(k_cache: torch.Tensor, block_tables: torch.Tensor,
                          seq_lens: torch.Tensor, query_start_loc: Optional[torch.Tensor],
                          bounds: torch.Tensor, bound_scales: torch.Tensor, *,
-                         num_tokens: int = 0, stream=None) -> None:
+                         num_tokens: Optional[int] = None, stream=None) -> None:
     """summarize_blocks of the 8-bit cache's keys (code times scale)."""
     return _summarize(True, k_cache, block_tables, seq_lens, query_start_loc, bounds,
                       bound_scales, num_tokens, stream)

@@ -236,3 +236,20 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(lib):
                                                  dict(max_q_len=1, max_seq_len=48)),
                  "evict_tokens_fp8": ((k, k, w, bt, sl, sl, sl, sl), dict(max_seq_len=48))}[name]
             getattr(ops, name)(*a[0], **a[1])
+
+
+@pytest.mark.parametrize("call", [ops.summarize_blocks, ops.summarize_blocks_fp8])
+def test_a_steps_bounds_need_its_number_of_tokens(lib, call):
+    """Left out beside query_start_loc it is an error, not a call that does nothing."""
+    k = torch.zeros(4, 1, ops.fp8_page_bytes(2, 64), dtype=torch.uint8) \
+        if call is ops.summarize_blocks_fp8 else torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    bt, sl, qsl = torch.zeros(2, 3, dtype=torch.int32), *(
+        torch.zeros(n, dtype=torch.int32) for n in (2, 3))
+    bounds, scales = ops.alloc_bounds(4, 2, 64, device="cpu")
+    with pytest.raises(ValueError, match="num_tokens"):
+        call(k, bt, sl, qsl, bounds, scales)
+    for n in (0, 3):  # given: on to the check of the tensors
+        with pytest.raises(ValueError, match="CUDA"):
+            call(k, bt, sl, qsl, bounds, scales, num_tokens=n)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(k, bt, sl, None, bounds, scales)
