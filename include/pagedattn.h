@@ -696,11 +696,14 @@ int pa_check_device_errors(cudaStream_t stream);
  * Failure-detection self-test.  Every wait inside the library's kernels (on
  * a copy landing, on a tensor-core product, on another warp's hand-off) is
  * bounded: past its limit (2 s) the kernel sets PA_ERR_TIMEOUT's bit in the
- * device error word, stops waiting and returns, so the context stays usable.
+ * device error word, stops waiting, waits (with the limit again) for its own
+ * copies in flight and returns, so the context stays usable.
  * This call runs that same wait, with limit_ns (at most 1 s), on a barrier
- * that nothing completes; pa_check_device_errors afterwards returns
- * PA_ERR_TIMEOUT.  It faults nothing and hangs nothing.  limit_ns of 0 or
- * above 1 s is PA_ERR_INVALID_ARG.
+ * that nothing completes, and then the wait for copies in flight on one that
+ * completes 0.2 s later; pa_check_device_errors afterwards returns
+ * PA_ERR_TIMEOUT (device word 0x2; 0x3 if the second wait gave up too).  It
+ * faults nothing and hangs nothing.  limit_ns of 0 or above 1 s is
+ * PA_ERR_INVALID_ARG.
  */
 int pa_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t stream);
 

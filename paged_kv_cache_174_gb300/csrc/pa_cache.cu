@@ -121,17 +121,29 @@ __global__ void __launch_bounds__(kScatterWarps * 32)
 // Failure-detection self-test: the bounded wait every kernel uses, on a
 // barrier that nothing ever completes, with a short limit.  The wait gives
 // up, sets the timeout bit of the error word and the kernel returns, so the
-// context stays usable.
+// context stays usable.  Before that it waits, as a kernel does for its copies
+// in flight, on a barrier that another warp completes kLateNs after the first
+// wait was given up; not to see that sets the other bit of the word.
+constexpr unsigned long long kLateNs = 200000000ull;  // 0.2 s
 __global__ void wait_timeout_selftest_kernel(unsigned long long limit_ns, unsigned* err) {
-  __shared__ __align__(8) uint64_t bar;
-  __shared__ int abort_flag;
+  __shared__ __align__(8) uint64_t bar[2];
+  __shared__ int abort_flag, late;
   if (threadIdx.x == 0) {
-    mbar_init(smem_addr(&bar), 1);
-    abort_flag = 0;
+    mbar_init(smem_addr(&bar[0]), 1);
+    mbar_init(smem_addr(&bar[1]), 1);
+    abort_flag = late = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  mbar_wait(smem_addr(&bar), 0, err, &abort_flag, limit_ns);  // nothing arrives
+  mbar_wait(smem_addr(&bar[0]), 0, err, &abort_flag, limit_ns);  // nothing arrives
+  if (threadIdx.x == 32) {
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < kLateNs) __nanosleep(1000);
+    mbar_arrive(smem_addr(&bar[1]));
+  } else if (threadIdx.x == 0) {
+    if (!mbar_wait_landed(smem_addr(&bar[1]), 0, err, &late)) flag_error(err, DEVERR_BOUNDS);
+  }
+  __syncthreads();
 }
 
 constexpr int kCopyThreads = 256;

@@ -214,6 +214,15 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, un
   }
 }
 
+// For the end of a kernel in which a wait was given up: waits for a copy that may still be
+// in flight until it has landed or the time limit has passed, whatever the kernel's abort
+// flag says.  *late (0 before the first of these waits) is set by one that gave up, after
+// which the others do not wait long.
+__device__ __forceinline__ bool mbar_wait_landed(uint32_t bar, uint32_t parity, unsigned* err,
+                                                 volatile int* late) {
+  return mbar_wait(bar, parity, err, late);
+}
+
 // --------------------------------------------------------- bulk async copy
 // Global -> shared, completion counted on an mbarrier (transaction bytes).
 // Both addresses 16-byte aligned, bytes a multiple of 16.

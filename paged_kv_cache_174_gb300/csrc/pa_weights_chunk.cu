@@ -68,6 +68,7 @@ struct alignas(16) ChunkShared {
   uint64_t side_full[kSide], raw_full[8][kRaw];
   uint32_t tmem_slot;
   int abort_flag;
+  int late;  // a wait for the last copies was given up too
   int listed;
   // rows pass: the keys' scales times the scores'; columns pass: the rows' log sums
   alignas(16) float side[kSide][kTile];
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     for (int i = 0; i < kBuffers; ++i) mbar_init(smem_addr(&B.s_empty[i]), kSumWarps / 2);
     for (int i = 0; i < kSide; ++i) mbar_init(smem_addr(&B.side_full[i]), COLS ? 1 : KW);
     for (int i = 0; i < 8 * kRaw; ++i) mbar_init(smem_addr(&B.raw_full[i / kRaw][i % kRaw]), 1);
-    B.abort_flag = 0;
+    B.abort_flag = B.late = 0;
     fence_mbar_init();
   }
   after_prior_kernels();
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         U.count = (int)((long long)(rank + 1) * tiles / ctas) - U.first;
       }
     }
+    if (*abort_flag) U.count = 0;  // (a wait was given up: nothing more is begun)
     const int32_t* table = p.block_tables + (int64_t)U.s * p.max_blocks;
     // tokens of query tile i of the request, and how many (columns pass)
     const auto tokens_of = [&](int i) { return min(TM, U.ql - i * TM); };
@@ -307,23 +309,26 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
         }
       } else if (lane == 0 && U.count > 0) {
         const uint32_t bar = smem_addr(&B.a_full);
-        if (loaded > 0)  // (the unit before has copied its tile away)
-          mbar_wait(smem_addr(&B.a_ready), (loaded - 1) & 1, p.err, abort_flag);
-        mbar_arrive_expect_tx(bar, TILE);
+        // (the unit before has copied its tile away)
+        if (loaded == 0 ||
+            mbar_wait(smem_addr(&B.a_ready), (loaded - 1) & 1, p.err, abort_flag)) {
+          mbar_arrive_expect_tx(bar, TILE);
 #pragma unroll
-        for (int hf = 0; hf < NH; ++hf)
-          tc::tma_load_3d(smem_addr(a_s + hf * HALF), &qmap, hf * 64, U.h * G, U.q0, bar);
+          for (int hf = 0; hf < NH; ++hf)
+            tc::tma_load_3d(smem_addr(a_s + hf * HALF), &qmap, hf * 64, U.h * G, U.q0, bar);
+        }
       }
     } else if (warp == 1) {
       // ------------------------------------------------ products
       if (lane == 0 && U.count > 0) {
         const tc::Desc bd = tc::sw128_desc_pair(smem_addr(b_s), 16, 1024);
-        mbar_wait_spin(smem_addr(&B.a_ready), loaded & 1, p.err, abort_flag);
-        for (int i = 0; i < U.count; ++i) {
+        const bool ok = mbar_wait_spin(smem_addr(&B.a_ready), loaded & 1, p.err, abort_flag);
+        for (int i = 0; ok && i < U.count; ++i) {
           const uint32_t c = c0 + i, st = c % NB, sb = c % kBuffers;
-          mbar_wait_spin(smem_addr(&B.b_full[st]), (c / NB) & 1, p.err, abort_flag);
-          if (c >= kBuffers)
-            mbar_wait_spin(smem_addr(&B.s_empty[sb]), (c / kBuffers - 1) & 1, p.err, abort_flag);
+          if (!mbar_wait_spin(smem_addr(&B.b_full[st]), (c / NB) & 1, p.err, abort_flag)) break;
+          if (c >= kBuffers && !mbar_wait_spin(smem_addr(&B.s_empty[sb]), (c / kBuffers - 1) & 1,
+                                               p.err, abort_flag))
+            break;
           tc::fence_after_sync();
           issue_products<D>(tmem + sb * kTile, tmem + A_COLS,
                             tc::Desc{bd.lo + st * (TILE >> 4), bd.hi});
@@ -670,13 +675,13 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   __syncthreads();
   // Every product is done and so every copy landed, unless a wait was given up: then the
   // last copies into each stage are waited for (again with a limit).
-  if (B.abort_flag && tid == 0) {
+  if (*abort_flag && tid == 0) {
     for (uint32_t c = c0 > NB ? c0 - NB : 0; c < c0; ++c)
-      mbar_wait(smem_addr(&B.b_full[c % NB]), (c / NB) & 1, p.err, abort_flag);
-    if (loaded) mbar_wait(smem_addr(&B.a_full), (loaded - 1) & 1, p.err, abort_flag);
+      mbar_wait_landed(smem_addr(&B.b_full[c % NB]), (c / NB) & 1, p.err, &B.late);
+    if (loaded) mbar_wait_landed(smem_addr(&B.a_full), (loaded - 1) & 1, p.err, &B.late);
     for (int w = 0; F8 && w < KW; ++w)
       for (uint32_t c = raw0 > kRaw ? raw0 - kRaw : 0; c < raw0; ++c)
-        mbar_wait(smem_addr(&B.raw_full[w][c % kRaw]), (c / kRaw) & 1, p.err, abort_flag);
+        mbar_wait_landed(smem_addr(&B.raw_full[w][c % kRaw]), (c / kRaw) & 1, p.err, &B.late);
   }
   if (warp == 1) {
     tc::fence_after_sync();

@@ -35,3 +35,14 @@ def test_context_is_usable_after_a_timeout():
     _, out = run_gpu_step(b)
     _, _, ref = run_oracle_step(b)
     assert_attn_close(to_f64(out), ref, "decode after a timed-out wait")
+
+
+def test_copies_in_flight_are_waited_for_after_a_wait_was_given_up():
+    """The wait at a kernel's end does not give up because an earlier one did: the self-test's
+    second barrier completes 0.2 s later and is seen (the bounds bit of the word stays clear)."""
+    t0 = time.perf_counter()
+    ops.selftest_wait_timeout(2_000_000)
+    with pytest.raises(ops.PagedAttnError) as ei:
+        ops.check_device_errors()
+    assert 0.2 <= time.perf_counter() - t0 < 5.0
+    assert ei.value.code == 5 and "(device word 0x2)" in str(ei.value)
