@@ -113,6 +113,7 @@ struct RowsRing {
   int live[kRowsWarps][STAGES];                         // keys of the page that count
   alignas(16) float scales[kRowsWarps][STAGES][32];     // 8-bit cache: 16 of K, 16 of V
   int abort_flag;
+  int late;                                             // a wait of settle() was given up too
 };
 
 template <int D, int G, bool F8>
@@ -346,12 +347,22 @@ struct RowsStream {
   }
   // Page c (all lanes): its stage's bytes and how many of its keys count.  The stage's
   // next use is issued by this warp after it is done with this one, so the phase waited
-  // for is the current one or the one just completed.
-  __device__ __forceinline__ uint32_t wait(uint32_t c, int& live) {
+  // for is the current one or the one just completed.  here: it came; where it did not for
+  // a lane, the warp issues nothing more.
+  __device__ __forceinline__ uint32_t wait(uint32_t c, int& live, bool& here) {
     const uint32_t st = c % Ring::STAGES;
-    mbar_wait(smem_addr(&B.full[warp][st]), (c / Ring::STAGES) & 1, err, &B.abort_flag);
+    here = mbar_wait(smem_addr(&B.full[warp][st]), (c / Ring::STAGES) & 1, err, &B.abort_flag);
     live = B.live[warp][st];
     return smem_addr(smem + st * Ring::STAGE);
+  }
+  // Behind the last page: where a wait was given up, the copies that may still be in flight
+  // are waited for (again with a limit), as others will write in their place.
+  __device__ __forceinline__ void settle() {
+    if (!*static_cast<volatile int*>(&B.abort_flag)) return;
+    for (uint32_t c = issued > Ring::STAGES ? issued - Ring::STAGES : 0; c < issued; ++c)
+      mbar_wait_landed(smem_addr(&B.full[warp][c % Ring::STAGES]), (c / Ring::STAGES) & 1, err,
+                       &B.late);
+    __syncwarp();
   }
   __device__ __forceinline__ float* scales(uint32_t c) { return B.scales[warp][c % Ring::STAGES]; }
   // Rows at and past `live` of the V page of page c hold anything: zeros from here on.
@@ -477,7 +488,7 @@ __device__ __forceinline__ void init_rings(RowsRing<D, F8, ROOM>& B, int4* found
     found->x = -1;
     for (int w = 0; w < kRowsWarps; ++w)
       for (int i = 0; i < Ring::STAGES; ++i) mbar_init(smem_addr(&B.full[w][i]), F8 ? 33 : 1);
-    B.abort_flag = 0;
+    B.abort_flag = B.late = 0;
     fence_mbar_init();
   } else if (threadIdx.x == 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(kmap)) : "memory");

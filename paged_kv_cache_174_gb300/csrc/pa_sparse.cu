@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
   R.begin(p.q + ((int64_t)t * p.n_kv + h) * G * D, p.scale_log2);
   for (uint32_t c = 0; c < S.issued; ++c) {
     int n;
-    const uint32_t at = S.wait(c, n);
+    bool here;
+    const uint32_t at = S.wait(c, n, here);
     float x[4];
     R.scores(at, S.scales(c), x);
     if (n < 16) {
@@ -98,9 +99,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
       S.clear_v(c, n);
     }
     R.add(x, at + Ring::PAGE, S.scales(c));
-    __syncwarp();  // the stage has been read
+    if (!__all_sync(0xffffffffu, here)) break;  // (and the stage has been read)
     issue_next();
   }
+  S.settle();
   join_rows<Ring::BYTES, D, G, F8>(J, R, rings, ctas, rank,
                                    p.out + ((int64_t)t * p.n_kv + h) * G * D);
 }

@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
   uint32_t c = 0;
   for (; c < S.issued; ++c) {
     int mine;
-    const uint32_t at = S.wait(c, mine);
+    bool here;
+    const uint32_t at = S.wait(c, mine, here);
     float x[4];
     R.scores(at, S.scales(c), x);
     const int n = L - ((first + mine) << 4);
@@ -117,9 +118,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
       if (G > 1) to[1] = x[1], to[8 * G + 1] = x[3];
     }
     R.add(x, at + Ring::PAGE, S.scales(c));
-    __syncwarp();  // the stage has been read
+    if (!__all_sync(0xffffffffu, here)) break;  // (and the stage has been read)
     issue_next(true);
   }
+  S.settle();
   join_rows<Ring::BYTES, D, G, F8>(J, R, rings, ctas, rank,
                                    p.out + ((int64_t)token * p.n_kv + h) * G * D);
 
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
       w[j] = (j == fresh ? 0.f : w[j]) + sum;
     }
   }
-  if (pages <= p.kept_pages) return;
+  if (pages <= p.kept_pages || B.abort_flag) return;  // (the flag: of waits before the join)
   float m[2], inv[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -158,7 +160,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
   for (int i = 0; i < Ring::STAGES; ++i) issue_next(false);
   for (; c < S.issued; ++c) {
     int mine;
-    const uint32_t at = S.wait(c, mine);
+    bool here;
+    const uint32_t at = S.wait(c, mine, here);
     float x[4];
     R.scores(at, S.scales(c), x);
     // (a head of no query has scores 0 and no part in the sums)
@@ -178,9 +181,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kCtas<D, F8>)
       const float add = t ? sum[1] : sum[0];
       if (j < keys) w[j] = (j == fresh ? 0.f : w[j]) + add;
     }
-    __syncwarp();
+    if (!__all_sync(0xffffffffu, here)) break;
     issue_next(false);
   }
+  S.settle();
 }
 
 // Shared memory for scores beside the rings, at most.
