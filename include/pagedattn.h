@@ -665,6 +665,13 @@ int pa_paged_attention_weights_fp8(const pa_bf16 *q, const uint8_t *k_cache,
  *                 flagged).  free_count_out [1] may be free_count.
  *   position_offsets  [num_seqs] or NULL: the tokens that went are added, so
  *                 that pa_build_step gives later tokens their true positions
+ * A model of several layers has caches and weights for each, and one set of
+ * tables, lengths and offsets and one free list for all: one call a layer, all
+ * with the same lengths and count.  Every call but the last writes its new
+ * lengths and count elsewhere (seq_lens_out, free_count_out: scratch of their
+ * own) and has position_offsets NULL; the blocks that each pushes are the same,
+ * to the same places.  With lengths updated in place by the first layer's call
+ * the others would find nothing to evict and move no row.
  * A length or budget out of range is flagged and its request left alone.  A
  * table entry that names no block is flagged: a row that would move from or to
  * it does not, and the row and weight in its place stay as they are.

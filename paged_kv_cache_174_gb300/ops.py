@@ -1352,6 +1352,11 @@ def evict_tokens(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Te
     ``seq_lens_out`` / ``free_count_out`` are given.  ``position_offsets`` gets
     the evicted tokens added (pass it to build_step afterwards).  Returns the
     new lengths.
+
+    One call for each layer of a model, whose layers share tables, lengths,
+    offsets and free list: all but the last with a ``seq_lens_out`` and a
+    ``free_count_out`` that are scratch and without ``position_offsets``, as a
+    layer that found the lengths already cut would move nothing.
     """
     return _evict(False, k_cache, v_cache, weights, block_tables, seq_lens, budgets,
                   free_blocks, free_count, num_sinks, num_recent, max_seq_len, seq_lens_out,

@@ -156,3 +156,53 @@ def test_a_row_that_stays_keeps_its_weight(fp8):
     assert np.array_equal(wd.cpu().numpy(), want_w)
     for got, want in zip(c.parts(), want_rows):
         assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_every_layer_of_a_model_is_cut(fp8, captured):
+    """Layers share tables, lengths, offsets and free list: scratch lengths and counts for
+    all calls but the last.  Every layer keeps its own tokens, and the books are kept once."""
+    c = R.Cache([(300, 0), (90, 0), (700, 0), (40, 0)], 2, 64, 16, fp8, seed=3)
+    budgets, sinks, recent, pushed = [100, 60, 333, 50], 3, 20, 1
+    caches = [(c.k, c.v), (c.v.clone(), c.k.clone()), (c.k.flip(0), c.v.flip(0))]
+    g = torch.Generator().manual_seed(3)
+    weights = [torch.rand(4, 2, 703, generator=g) for _ in caches]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    tables, lens, _ = c.step()
+    free, count = torch.full((c.blocks,), -5, **i32), torch.tensor([pushed], **i32)
+    offsets, budgets_d = torch.arange(4, **i32), torch.tensor(budgets, **i32)
+    want, start = [], free.tolist()
+    for (k, v), w in zip(caches, weights):
+        c.k, c.v = k, v
+        rows, w64 = c.parts(), w.numpy().copy()
+        books = R.evict(rows, w64, c.tables, c.lens, budgets, start, pushed, sinks, recent, 16)
+        want.append((rows, w64))
+    on_gpu = [w.cuda() for w in weights]
+    call = ops.evict_tokens_fp8 if fp8 else ops.evict_tokens
+
+    def every_layer():
+        scratch = torch.empty_like(lens), torch.empty_like(count)
+        for i, ((k, v), w) in enumerate(zip(caches, on_gpu)):
+            last = i + 1 == len(caches)
+            call(k, v, w, tables, lens, budgets_d, free, count, num_sinks=sinks,
+                 num_recent=recent, max_seq_len=700, seq_lens_out=None if last else scratch[0],
+                 free_count_out=None if last else scratch[1],
+                 position_offsets=offsets if last else None)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            every_layer()
+        graph.replay()
+    else:
+        every_layer()
+    ops.check_device_errors()
+    for (k, v), w, (rows, w64) in zip(caches, on_gpu, want):
+        c.k, c.v = k, v
+        for got, expected in zip(c.parts(), rows):
+            assert np.array_equal(got, expected)
+        assert np.array_equal(w.cpu().numpy(), w64)
+    assert lens.tolist() == books[0] and free.tolist() == books[1]
+    assert count.tolist() == [books[2]]
+    assert (offsets.cpu() - torch.arange(4)).tolist() == books[3]
