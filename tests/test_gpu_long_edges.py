@@ -206,3 +206,77 @@ def test_every_layer_of_a_model_is_cut(fp8, captured):
     assert lens.tolist() == books[0] and free.tolist() == books[1]
     assert count.tolist() == [books[2]]
     assert (offsets.cpu() - torch.arange(4)).tolist() == books[3]
+
+
+# ------------------------------------------------ longer than what shared memory holds
+STAGED = (196624 - 16) * 32 // (32 * 4 + 8)  # about: bits, prefix counts and weights of a request
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,budgets,most", [
+    ([46_000, 300], [20_000, 200], 46_000),        # the weights held in shared memory ...
+    ([46_800, 300], [20_000, 200], 46_800),        # ... and read from memory in each pass
+    ([200_001, 60_000, 47_000], [150_000, 33, 46_999], 200_001),
+    ([70_000, 9_000], [4_000, 8_000], 524_288),    # the longest that a call may say
+])
+def test_requests_past_the_weights_held(lens, budgets, most, fp8):
+    assert min(abs(n - STAGED) for n in (46_000, 46_800)) < 600 and 46_000 < STAGED < 46_800
+    c = R.Cache([(n, 0) for n in lens], 1, 64, 16, fp8, seed=5)
+    width = -(-most // 16)
+    tables = np.full((len(lens), width), -1, np.int32)
+    tables[:, :c.tables.shape[1]] = c.tables[:, :width]
+    g = torch.Generator().manual_seed(5)
+    w = (torch.randn(len(lens), 1, max(lens), generator=g) * 2).exp()
+    w[0, 0, 1000:1500] = 0.25  # ties across words and windows
+    full = torch.zeros(len(lens), 1, most)
+    full[..., :max(lens)] = w
+    sinks, recent, pushed = 5, 17, 2
+    i32 = dict(dtype=torch.int32, device="cuda")
+    free, count = torch.full((c.blocks,), -1, **i32), torch.tensor([pushed], **i32)
+    rows, w64 = c.parts(), full.numpy().copy()
+    books = R.evict(rows, w64, c.tables, c.lens, budgets, free.tolist(), pushed, sinks, recent, 16)
+    wd, seq = full.cuda(), c.step()[1]
+    call = ops.evict_tokens_fp8 if fp8 else ops.evict_tokens
+    call(c.k, c.v, wd, torch.from_numpy(tables).cuda(), seq, torch.tensor(budgets, **i32), free,
+         count, num_sinks=sinks, num_recent=recent, max_seq_len=most)
+    ops.check_device_errors()
+    assert seq.tolist() == books[0] and free.tolist() == books[1] and count.tolist() == [books[2]]
+    assert np.array_equal(wd.cpu().numpy().view(np.int32), w64.view(np.int32))
+    for got, want in zip(c.parts(), rows):
+        assert np.array_equal(got, want)
+
+
+# --------------------------------------------- weights whose scores are computed again
+KEPT_BYTES, MOST_CTAS = 44 * 1024, 16
+
+
+@pytest.mark.parametrize("n_kv,G,d,block,fp8", [
+    (1, 8, 64, 16, True), (1, 8, 128, 16, True), (2, 8, 128, 32, True), (1, 4, 128, 16, True),
+    (1, 2, 64, 32, True), (1, 8, 128, 32, False), (1, 4, 64, 16, False), (1, 1, 128, 16, False),
+    (1, 1, 64, 16, True),
+])
+def test_scores_past_those_kept(n_kv, G, d, block, fp8):
+    """A context whose scores do not fit beside the pages even over the largest cluster: those
+    of its last pages are computed again from K, and the new token is among them."""
+    kept = KEPT_BYTES // (16 * G * 4)                # pages of a CTA whose scores stay
+    n = MOST_CTAS * (kept + 70) * 16 - 5
+    share = -(-(-(-n // 16)) // MOST_CTAS)
+    assert share >= kept + 70
+    c = R.Cache([(n - 1, 1), (29, 1), (n // 2, 1)], n_kv, d, block, fp8, seed=G, pad=1)
+    q, q64 = c.queries(n_kv * G, 1)
+    tables, lens, starts = c.step()
+    before = torch.rand(3, n_kv, n + 3, generator=torch.Generator().manual_seed(G))
+    for s, m in enumerate(c.lens):
+        before[s, :, m - 1] = float("nan")           # (the new token's entry starts from 0)
+    w = before.cuda()
+    call = ops.paged_attention_weights_fp8 if fp8 else ops.paged_attention_weights
+    out = call(q, c.k, c.v, tables, lens, starts, d ** -0.5, w, max_q_len=1, max_seq_len=n)
+    ops.check_device_errors()
+    o64, A, E, w64, tol = R.weights_attention(q64, c.K, c.V, c.tables, c.lens, c.starts, d ** -0.5,
+                                              block, before.numpy())
+    got = w.double().cpu().numpy()
+    for s, m in enumerate(c.lens):
+        assert (np.abs(got[s, :, :m] - w64[s, :, :m]) <= tol[s, :, :m] + 1e-30).all()
+        assert torch.equal(w[s, :, m:].cpu(), before[s, :, m:])
+    rows = slice(0, 3)
+    R.assert_blocks_close(out.double().cpu().numpy()[rows], (o64[rows], A[rows], E[rows]))
