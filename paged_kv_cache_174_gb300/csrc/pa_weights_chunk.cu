@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
   // the launch's chunk requests and their tiles, in order
   int tiles_all = 0;
   {
-    int listed = 0, tiles = 0;
+    int listed = 0;
     for (int s0 = 0; s0 < p.num_seqs; s0 += THREADS) {
       const int s = s0 + tid;
       int n = 0;
@@ -186,13 +186,12 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
             L <= ((long long)p.max_blocks << p.block_shift) * 16)
           n = COLS ? (L + kTile - 1) / kTile : (b - a + TM - 1) / TM;
       }
-      uint32_t before_n, before_t, all_n, all_t;
-      block_scan2(B.scan, n > 0, (uint32_t)n, before_n, before_t, all_n, all_t);
+      uint32_t before_n, unused, all_n, unused2;
+      block_scan2(B.scan, n > 0, 0u, before_n, unused, all_n, unused2);
       const int at = listed + (int)before_n - p.skip;
       // (requests before this launch's take no tiles of it)
       if (n > 0 && at >= 0 && at < kListed) B.list_seq[at] = s, B.list_base[at] = n;
       listed += (int)all_n;
-      tiles += (int)all_t;
     }
     const int mine = min(max(listed - p.skip, 0), kListed);
     __syncthreads();
@@ -208,7 +207,6 @@ __global__ void __launch_bounds__(Roles<F8>::kThreads, 1)
     }
     tiles_all = (int)run;
     if (tid == 0) B.list_base[mine] = tiles_all, B.listed = mine;
-    (void)tiles;
   }
   tc::fence_before_sync();
   __syncthreads();
