@@ -1,5 +1,5 @@
-// pa_tma_host.h -- tensor maps of the caches for the kernels of the long-context
-// operators: what the host encodes before a launch.
+// pa_tma_host.h -- tensor maps, which the host encodes before a launch: the driver's
+// function, and the caches' maps of the kernels of the long-context operators.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap (types only; nothing is linked from the driver)
