@@ -560,8 +560,9 @@ int pa_summarize_blocks_fp8(const uint8_t *k_cache, int32_t num_blocks, int32_t 
  *                 q's codes x = rint(q / p_q) (nearest, ties to even), p_q by
  *                 the rule of bound_scales, and the block's codes and scale:
  *                 an upper bound of q k over the block's keys, but for the
- *                 rounding of q.  The sums are of integers and exact, so the
- *                 result depends on nothing but the inputs.
+ *                 rounding of q.  The sums are of integers and exact, and
+ *                 scores are compared by them and the powers of two, whatever
+ *                 their size, so the result depends on nothing but the inputs.
  *   max_seq_len   at most 49152 blocks
  * The product is with q as it is given (scale the scores and they keep their
  * order).

@@ -625,7 +625,8 @@ cudaError_t launch_select(SelectArgs p, int sm_count, cudaStream_t stream) {
   const long long units = (long long)p.num_tokens * p.n_kv;
   // CTAs of a cluster: until there are 1.6 an SM, for requests of more than 256 blocks each.
   // One, two, four and eight: 512 pairs of 8 to 256 blocks 10.4* 12.3 19.2 32.7 us; 64 pairs
-  // of 6144 to 8192 blocks 70.9 44.2 37.4* 43.1; 8 pairs of 8192 44.2 27.9 18.8 14.2*.
+  // of 6144 to 8192 blocks 70.9 44.2 37.4* 43.1; 8 pairs of 8192 44.2 27.9 18.8 14.2*.  (With
+  // scores compared in fp32; by their integers and exponents 10.7, 37.9 and 14.6.)
   int ctas = 1;
   while (ctas < 8 && blocks > 256ll * ctas &&
          (5 * units * ctas < 8ll * sm_count || blocks > 4096ll * ctas))

@@ -9,7 +9,7 @@
 // 16-token pages in turn, and the pieces are joined through shared memory of the
 // cluster, so there is no workspace and no second kernel.
 // 512 pairs of 128 blocks of 16 (32 q / 8 kv heads of 128): 84 us, 95% of the copy rate;
-// 8-bit 59 us, 70%, bound by the conversion of the codes.
+// 8-bit 59 us, 70%: each warp's chain of conversions and products, 3 warps a scheduler (48% issue).
 #include <cstdint>
 
 #include "pa_rows.cuh"
@@ -20,7 +20,9 @@ namespace {
 
 // CTAs of an SM, and the bytes of a warp's ring that leaves: three pages in flight a warp.  512
 // pairs with rings of 16, 24 and 32 KB (3, 2 and 1 CTAs) 91 84* 98 us; 256 pairs, 8-bit, with
-// 8, 12 and 16 KB (5, 4 and 3) 36.4 31.9* 38.8.
+// 8, 12 and 16 KB (5, 4 and 3) 36.4 31.9* 38.8.  Heads of 64, with 8, 12, 16 and 24 KB (5, 4, 3
+// and 2 CTAs): 512 pairs 50.1 49.9* 57.2 50.1, 8-bit 40.4 36.8* 51.8 51.9; 256 pairs, 8-bit, 27.0
+// 26.1* 29.2 29.2.
 template <int D, bool F8>
 constexpr int kCtas = D == 128 && !F8 ? 2 : 4;
 template <int D, bool F8>

@@ -10,8 +10,9 @@
 // from K.  One pass over K and V, so their bytes are the bound.  A cluster takes a
 // (request, kv head), each CTA a run of its keys.
 // 64 requests of 128 to 4096 tokens, 32 q / 8 kv heads of 128: 101 us, 82% of the copy rate;
-// 8-bit 84 us, 52% (the conversion of the codes, and the last CTAs of a grid of 2.2 for each
-// place); 8 requests of 16384 to 32767 tokens, 8-bit, 122 us, 52%.
+// 8-bit 84 us, 52% (each warp's chain of conversions and products, 2.6 warps a scheduler and 46%
+// issue, and the last CTAs of a grid of 2.2 for each place); 8 requests of 16384 to 32767 tokens,
+// 8-bit, 122 us, 52%.
 #include <cstdint>
 
 #include "pa_rows.cuh"
@@ -23,6 +24,8 @@ namespace {
 // CTAs of an SM (with short contexts; the scores of long ones take the room of some),
 // and the bytes of a warp's ring: two pages in flight a warp.  512 pairs with rings of 16 and
 // 24 KB 101* 126 us, 8-bit with 8 and 12 KB 84* 90: the longer ones leave room for fewer CTAs.
+// Heads of 64 with 8, 12, 16 and 24 KB (5, 4, 3 and 2 CTAs) 65.3* 70.6 69.9 110, 8-bit 64.0* 76.3
+// 76.7 76.7.
 template <int D, bool F8>
 constexpr int kCtas = D == 128 && !F8 ? 3 : 5;
 template <int D, bool F8>
